@@ -50,6 +50,8 @@
 #define TTT_H
 
 #include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
 
 #ifdef __cplusplus
 extern "C" {
@@ -72,6 +74,19 @@ extern "C" {
 /* Inner loss of ttt_linear_forward_opts and ttt_mlp_forward_opts. */
 #define TTT_LOSS_MSE 0           /* 1/2 ||LN(f_res(XK)) - (XV - XK)||^2 per token */
 #define TTT_LOSS_INNER_PRODUCT 1 /* -< XK + LN(f_res(XK)), XV > per token        */
+
+/* Activation of ttt_conv_* (TTT_ACT_NONE or TTT_ACT_SILU) and of the gate of
+ * ttt_block_norm. */
+#define TTT_ACT_NONE 0
+#define TTT_ACT_SIGMOID 1
+#define TTT_ACT_SILU 2 /* s sigma(s) */
+#define TTT_ACT_TANH 3
+
+/* Shape of ttt_block_norm's gate. */
+#define TTT_GATE_NONE 0
+#define TTT_GATE_CHANNEL 1  /* [D] fp32: a learned gate                     */
+#define TTT_GATE_SEQUENCE 2 /* [B,D] fp32: one for each sequence            */
+#define TTT_GATE_TOKEN 3    /* [B,L,D] io: one for each token               */
 
 /* Storage type of XQ/XK/XV and O. State, eta and LN parameters are fp32. */
 typedef enum { TTT_F32 = 0, TTT_BF16 = 1 } ttt_dtype;
@@ -457,6 +472,116 @@ int ttt_decode_steps_gated(int T, int B, int H, int d, int io, float ln_eps, int
 int ttt_ln_l2_bwd(int rows, int d, const float *Z, const float *target,
                   const float *ln_gamma, const float *ln_beta, float ln_eps, float *G,
                   hipStream_t stream);
+
+/*
+ * Operators around the layer. They share these conventions, besides those at
+ * the top of this file:
+ *   - x_strides and the like: HOST arrays of the batch and token strides (and
+ *     the head stride, where there are heads) in elements, the innermost
+ *     dimension contiguous; NULL is the contiguous array of the stated shape.
+ *     So an operand may be a slice of a wider projection's output, or
+ *     [B,H,L,d] features seen as [B,L,H,d]. Strides are >= 0 (TTT_E_SHAPE);
+ *     those of an output give every element an address of its own. Accesses
+ *     are of up to 16 bytes where addresses and strides allow, else of one
+ *     element: any alignment of the element is accepted.
+ *   - lens: optional [B] int32 on the device, the tokens of each sequence.
+ *     Rows at and past a sequence's length are padding: they are not read,
+ *     their outputs and gradients are written as zeros, and the state is that
+ *     after the last token before them. Values are taken as if clamped to
+ *     [0, L]. NULL: every sequence has L tokens.
+ *   - outputs must not overlap each other or an input (TTT_E_ALIAS), except
+ *     where a pair is named; column slices of the same rows do not overlap.
+ *   - sums, states and statistics are fp32; gradients of io arrays are io,
+ *     those of fp32 arrays fp32. All results are repeatable bit for bit.
+ */
+
+#define TTT_CONV_MAX_C (1 << 20) /* channels of ttt_conv_*                  */
+#define TTT_NORM_MAX_D 8192      /* columns of ttt_block_norm               */
+
+/*
+ * Short causal convolution, a filter of K taps for each channel:
+ *     z_t = bias + sum_k weight[k] x_{t-K+1+k},  y_t = z_t or z_t sigma(z_t)
+ * with the K - 1 tokens before the first taken from `state` (NULL: zeros).
+ *   2 <= K <= 4; 0 <= C <= TTT_CONV_MAX_C; 0 <= B <= 65535; act TTT_ACT_NONE
+ *   or TTT_ACT_SILU.
+ *   x, y      : [B,L,C] io, strided.   weight : [C,K] fp32.
+ *   bias      : [C] fp32 or NULL.      state  : [B,K-1,C] io, oldest first.
+ *   state_out : [B,K-1,C] io or NULL, the last K - 1 tokens of (state, x);
+ *               it may be exactly `state`.
+ */
+int ttt_conv_forward(int B, int L, int C, int K, int io, int act, const void *x,
+                     const int64_t *x_strides, const float *weight, const float *bias,
+                     const void *state, const int *lens, void *y, const int64_t *y_strides,
+                     void *state_out, hipStream_t stream);
+
+/*
+ * One token of ttt_conv_forward: x [B,C] io (x_strides: the batch stride
+ * alone), y [B,C] io contiguous, state [B,K-1,C] io updated in place.
+ * B*C < 2^31.
+ */
+int ttt_conv_step(int B, int C, int K, int io, int act, const void *x, const int64_t *x_strides,
+                  const float *weight, const float *bias, void *state, void *y,
+                  hipStream_t stream);
+
+/*
+ * Gradients of <dy, y> + <dstate_out, state_out> through ttt_conv_forward
+ * (dstate_out NULL: zero) with respect to x, weight, bias (dbias NULL exactly
+ * when bias is) and state (dstate likewise). dy, dx strided [B,L,C] io;
+ * dstate_out, dstate [B,K-1,C] io; dweight [C,K], dbias [C] fp32. The
+ * workspace holds ttt_conv_backward_workspace's bytes of partial sums; calls
+ * that share one must not overlap.
+ */
+int ttt_conv_backward(int B, int L, int C, int K, int io, int act, const void *x,
+                      const int64_t *x_strides, const float *weight, const float *bias,
+                      const void *state, const int *lens, const void *dy,
+                      const int64_t *dy_strides, const void *dstate_out, void *dx,
+                      const int64_t *dx_strides, float *dweight, float *dbias, void *dstate,
+                      void *workspace, size_t workspace_bytes, hipStream_t stream);
+int ttt_conv_backward_workspace(int B, int L, int C, int K, size_t *bytes);
+
+/*
+ * The seam between two blocks: the norm after a block, its gate, the residual
+ * sum and the norm before the next block,
+ *     n = Norm(y) post_gamma + post_beta
+ *     resid_out = scale resid + act(gate) n
+ *     x = Norm(resid_out) pre_gamma + pre_beta
+ * row by row over the last dimension, Norm(u) = u / sqrt(mean u^2 + eps)
+ * (layer = 0) or (u - mean u) / sqrt(var u + eps), biased variance (layer = 1).
+ * x is formed from resid_out before that is rounded to its storage type.
+ *   1 <= D <= TTT_NORM_MAX_D; B*L <= TTT_MAX_L; eps as ln_eps above.
+ *   resid_io  : storage of resid, resid_out: TTT_F32, or io.
+ *   resid, y  : [B,L,D], strided.  gate : by gate_shape (TTT_GATE_*), strided
+ *               where it is for each token; gate_act a TTT_ACT_*.
+ *   gammas, betas, scale : [D] fp32; NULL is 1 (a gamma, scale) or 0 (a beta).
+ *   resid_out : [B,L,D] resid_io, x : [B,L,D] io, contiguous.
+ */
+int ttt_block_norm(int B, int L, int D, int io, int resid_io, int layer, int gate_shape,
+                   int gate_act, float eps, const void *resid, const int64_t *resid_strides,
+                   const void *y, const int64_t *y_strides, const void *gate,
+                   const int64_t *gate_strides, const float *post_gamma, const float *post_beta,
+                   const float *pre_gamma, const float *pre_beta, const float *scale,
+                   const int *lens, void *resid_out, void *x, hipStream_t stream);
+
+/*
+ * Gradients of <dresid_out, resid_out> + <dx, x> through ttt_block_norm from
+ * its inputs (the forward saves nothing). dresid_out, dresid [B,L,D] resid_io
+ * and dx, dy [B,L,D] io, contiguous; dgate shaped and typed as gate,
+ * contiguous; dpost_gamma, dpost_beta, dpre_gamma, dpre_beta, dscale [D] fp32,
+ * each NULL where it is not wanted. The workspace holds
+ * ttt_block_norm_backward_workspace's bytes of partial sums; calls that share
+ * one must not overlap.
+ */
+int ttt_block_norm_backward(int B, int L, int D, int io, int resid_io, int layer, int gate_shape,
+                            int gate_act, float eps, const void *resid,
+                            const int64_t *resid_strides, const void *y, const int64_t *y_strides,
+                            const void *gate, const int64_t *gate_strides, const float *post_gamma,
+                            const float *post_beta, const float *pre_gamma, const float *pre_beta,
+                            const float *scale, const int *lens, const void *dresid_out,
+                            const void *dx, void *dresid, void *dy, void *dgate,
+                            float *dpost_gamma, float *dpost_beta, float *dpre_gamma,
+                            float *dpre_beta, float *dscale, void *workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+int ttt_block_norm_backward_workspace(int B, int L, int D, int gate_shape, size_t *bytes);
 
 /* Message for the last non-zero return on this thread ("" if none). */
 const char *ttt_last_error(void);

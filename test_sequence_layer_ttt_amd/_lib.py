@@ -22,6 +22,8 @@ TTT_E_ALIAS = -5
 TTT_E_HIP = -6
 TTT_F32 = 0
 TTT_BF16 = 1
+TTT_ACT_NONE, TTT_ACT_SIGMOID, TTT_ACT_SILU, TTT_ACT_TANH = range(4)
+TTT_GATE_NONE, TTT_GATE_CHANNEL, TTT_GATE_SEQUENCE, TTT_GATE_TOKEN = range(4)
 
 _lib = None
 
@@ -72,6 +74,18 @@ def load():
                                      + [ctypes.c_size_t, _P])
     lib.ttt_mlp_backward_workspace.argtypes = [_i] * 5 + [ctypes.POINTER(ctypes.c_size_t)]
     lib.ttt_ln_l2_bwd.argtypes = [_i, _i, _P, _P, _P, _P, _f, _P, _P]
+    # operators around the layer: strides are host arrays of int64
+    size = ctypes.c_size_t
+    lib.ttt_conv_forward.argtypes = [_i] * 6 + [_P] * 9 + [_P]
+    lib.ttt_conv_step.argtypes = [_i] * 5 + [_P] * 6 + [_P]
+    lib.ttt_conv_backward.argtypes = [_i] * 6 + [_P] * 15 + [size, _P]
+    lib.ttt_conv_backward_workspace.argtypes = [_i] * 4 + [ctypes.POINTER(size)]
+    lib.ttt_block_norm.argtypes = [_i] * 8 + [_f] + [_P] * 14 + [_P]
+    lib.ttt_block_norm_backward.argtypes = [_i] * 8 + [_f] + [_P] * 23 + [size, _P]
+    lib.ttt_block_norm_backward_workspace.argtypes = [_i] * 4 + [ctypes.POINTER(size)]
+    for name in ("ttt_conv_forward", "ttt_conv_step", "ttt_conv_backward", "ttt_conv_backward_workspace",
+                 "ttt_block_norm", "ttt_block_norm_backward", "ttt_block_norm_backward_workspace"):
+        getattr(lib, name).restype = _i
     for name in ("ttt_linear_forward", "ttt_mlp_forward", "ttt_decode_step", "ttt_decode_steps",
                  "ttt_linear_backward", "ttt_linear_backward_workspace", "ttt_ln_l2_bwd",
                  "ttt_linear_backward_noalloc", "ttt_mlp_backward", "ttt_mlp_backward_workspace",
