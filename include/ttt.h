@@ -540,6 +540,72 @@ int ttt_conv_backward(int B, int L, int C, int K, int io, int act, const void *x
 int ttt_conv_backward_workspace(int B, int L, int C, int K, size_t *bytes);
 
 /*
+ * Selective state space scan: for each head h a state [N,P] that decays and
+ * gains an outer product with every token,
+ *     D_t = log(1 + exp(dt_t + dt_bias)),  a_t = exp(D_t A)
+ *     state <- a_t state + B_t (D_t x_t)^T,   y_t = C_t state + D x_t
+ * with B and C shared by the H / G heads of a group.
+ *   1 <= P, N <= TTT_SSM_MAX_DIM; H a positive multiple of G; B*H and the
+ *   number of segments B*H*ceil(L/256) at most TTT_SSM_MAX_HEADS.
+ *   x, y  : [B,L,H,P] io, strided (batch, token, head).
+ *   dt    : [B,L,H] io, strided (batch, token, head).
+ *   A     : [H] fp32 (decays where negative); D, dt_bias : [H] fp32 or NULL (0).
+ *   B, C  : [B,L,G,N] io, strided (batch, token, group).
+ *   state : [B,H,N,P] fp32 or NULL (zeros); state_out : the same or NULL; it
+ *           may be exactly `state`.
+ * The workspace holds ttt_ssm_forward_workspace's bytes (the states at the
+ * borders of segments that run side by side; may be 0); calls that share one
+ * must not overlap.
+ * Numerics: state and sums in fp32. bf16 inputs with P = 64 and N = 32, 64 or
+ * 128, in rows that allow 16-byte accesses, take MFMA products: the state's
+ * update is exact to about 24 bits (its one unrounded operand is split into
+ * three bf16 parts); the outputs take the decayed products C_t . B_s and the
+ * state as bf16 operands.
+ */
+#define TTT_SSM_MAX_DIM 128
+#define TTT_SSM_MAX_HEADS (1 << 22)
+int ttt_ssm_forward(int B, int L, int H, int P, int G, int N, int io, const void *x,
+                    const int64_t *x_strides, const void *dt, const int64_t *dt_strides,
+                    const float *A, const void *Bm, const int64_t *B_strides, const void *Cm,
+                    const int64_t *C_strides, const float *D, const float *dt_bias,
+                    const float *state, const int *lens, void *y, const int64_t *y_strides,
+                    float *state_out, void *workspace, size_t workspace_bytes,
+                    hipStream_t stream);
+int ttt_ssm_forward_workspace(int B, int L, int H, int P, int G, int N, size_t *bytes);
+
+/*
+ * One token of ttt_ssm_forward for each sequence: x [B,H,P], dt [B,H], B, C
+ * [B,G,N] io, strided (batch, head or group); state [B,H,N,P] fp32 updated in
+ * place; y [B,H,P] io contiguous.
+ */
+int ttt_ssm_step(int B, int H, int P, int G, int N, int io, const void *x,
+                 const int64_t *x_strides, const void *dt, const int64_t *dt_strides,
+                 const float *A, const void *Bm, const int64_t *B_strides, const void *Cm,
+                 const int64_t *C_strides, const float *D, const float *dt_bias, float *state,
+                 void *y, hipStream_t stream);
+
+/*
+ * Gradients of <dy, y> + <dstate_out, state_out> through ttt_ssm_forward from
+ * its inputs (the forward saves nothing; dstate_out NULL: zero): dx, ddt, dB,
+ * dC shaped as their operands, io, strided; dA, dD, ddt_bias [H] and dstate
+ * [B,H,N,P] fp32, the last three NULL exactly when D, dt_bias, state are. The
+ * workspace holds ttt_ssm_backward_workspace's bytes (states at segment
+ * borders, dB and dC of each head in fp32, per-token sums); calls that share
+ * one must not overlap.
+ */
+int ttt_ssm_backward(int B, int L, int H, int P, int G, int N, int io, const void *x,
+                     const int64_t *x_strides, const void *dt, const int64_t *dt_strides,
+                     const float *A, const void *Bm, const int64_t *B_strides, const void *Cm,
+                     const int64_t *C_strides, const float *D, const float *dt_bias,
+                     const float *state, const int *lens, const void *dy,
+                     const int64_t *dy_strides, const float *dstate_out, void *dx,
+                     const int64_t *dx_strides, void *ddt, const int64_t *ddt_strides, float *dA,
+                     void *dB, const int64_t *dB_strides, void *dC, const int64_t *dC_strides,
+                     float *dD, float *ddt_bias, float *dstate, void *workspace,
+                     size_t workspace_bytes, hipStream_t stream);
+int ttt_ssm_backward_workspace(int B, int L, int H, int P, int G, int N, size_t *bytes);
+
+/*
  * The seam between two blocks: the norm after a block, its gate, the residual
  * sum and the norm before the next block,
  *     n = Norm(y) post_gamma + post_beta

@@ -83,7 +83,13 @@ def load():
     lib.ttt_block_norm.argtypes = [_i] * 8 + [_f] + [_P] * 14 + [_P]
     lib.ttt_block_norm_backward.argtypes = [_i] * 8 + [_f] + [_P] * 23 + [size, _P]
     lib.ttt_block_norm_backward_workspace.argtypes = [_i] * 4 + [ctypes.POINTER(size)]
-    for name in ("ttt_conv_forward", "ttt_conv_step", "ttt_conv_backward", "ttt_conv_backward_workspace",
+    lib.ttt_ssm_forward.argtypes = [_i] * 7 + [_P] * 17 + [size, _P]
+    lib.ttt_ssm_forward_workspace.argtypes = [_i] * 6 + [ctypes.POINTER(size)]
+    lib.ttt_ssm_step.argtypes = [_i] * 6 + [_P] * 13 + [_P]
+    lib.ttt_ssm_backward.argtypes = [_i] * 7 + [_P] * 29 + [size, _P]
+    lib.ttt_ssm_backward_workspace.argtypes = [_i] * 6 + [ctypes.POINTER(size)]
+    for name in ("ttt_ssm_forward", "ttt_ssm_forward_workspace", "ttt_ssm_step", "ttt_ssm_backward",
+                 "ttt_ssm_backward_workspace", "ttt_conv_forward", "ttt_conv_step", "ttt_conv_backward", "ttt_conv_backward_workspace",
                  "ttt_block_norm", "ttt_block_norm_backward", "ttt_block_norm_backward_workspace"):
         getattr(lib, name).restype = _i
     for name in ("ttt_linear_forward", "ttt_mlp_forward", "ttt_decode_step", "ttt_decode_steps",

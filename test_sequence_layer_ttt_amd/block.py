@@ -204,6 +204,106 @@ def ttt_conv_backward(x, weight, dy, bias=None, state=None, dstate_out=None, act
     return g
 
 
+# --- selective state space scan -------------------------------------------------
+
+
+def _ssm_args(x, dt, A, B, C, D, dt_bias):
+    """Checks and the operands' part of the argument list; B and C as given."""
+    io, dev = _io(x, "x"), x.device
+    lead, (H, P) = x.shape[:-2], x.shape[-2:]
+    G, N = B.shape[-2:]
+    kind = _S2 if x.dim() == 3 else _S3
+    _check(dt, "dt", lead + (H,), x.dtype, dev, contiguous=False)
+    _check(B, "B", lead + (G, N), x.dtype, dev, contiguous=False)
+    _check(C, "C", lead + (G, N), x.dtype, dev, contiguous=False)
+    _check(A, "A", (H,), torch.float32, dev)
+    if D is not None:
+        _check(D, "D", (H,), torch.float32, dev)
+    if dt_bias is not None:
+        _check(dt_bias, "dt_bias", (H,), torch.float32, dev)
+    return dev, (*lead, H, P, G, N), (io, _ptr(x), _rows(x, "x", kind), _ptr(dt), _rows(dt, "dt", kind, 0),
+                                      _ptr(A), _ptr(B), _rows(B, "B", kind), _ptr(C), _rows(C, "C", kind),
+                                      _ptr(D), _ptr(dt_bias))
+
+
+def ttt_ssm_forward_workspace(B: int, L: int, H: int, P: int, G: int, N: int) -> int:
+    """Bytes of device workspace ttt_ssm_forward needs."""
+    return _need(_lib.load().ttt_ssm_forward_workspace, B, L, H, P, G, N)
+
+
+def ttt_ssm_forward(x, dt, A, B, C, D=None, dt_bias=None, state=None, lens=None, y=None, state_out=None,
+                    workspace=None, stream=None):
+    """Selective state space scan over [B,L,H,P] features: with d_t =
+    softplus(dt_t + dt_bias), state <- exp(d_t A) state + B_t (d_t x_t)^T and
+    y_t = C_t state + D x_t, a state [N,P] for each head. x, y [B,L,H,P], dt
+    [B,L,H], B, C [B,L,G,N] in fp32 or bf16 (views allowed, the features
+    contiguous; [B,H,L,d] features go in as x.transpose(1, 2)); A, D, dt_bias
+    [H] fp32; state, state_out [B,H,N,P] fp32; lens [B] int32 optional lengths.
+    Returns (y, state_out); state_out may be `state` itself."""
+    dev, (Bn, L, H, P, G, N), args = _ssm_args(x, dt, A, B, C, D, dt_bias)
+    if state is not None:
+        _check(state, "state", (Bn, H, N, P), torch.float32, dev)
+    if y is None:
+        y = torch.empty((Bn, L, H, P), device=dev, dtype=x.dtype)
+    if state_out is None:
+        state_out = torch.empty((Bn, H, N, P), device=dev, dtype=torch.float32)
+    _check(y, "y", (Bn, L, H, P), x.dtype, dev, contiguous=False)
+    _check(state_out, "state_out", (Bn, H, N, P), torch.float32, dev)
+    workspace, nbytes = _workspace(workspace, ttt_ssm_forward_workspace(Bn, L, H, P, G, N), dev)
+    _call(_lib.load().ttt_ssm_forward, dev, stream, Bn, L, H, P, G, N, *args, _ptr(state),
+          _lens(lens, Bn, dev), _ptr(y), _rows(y, "y", _S3), _ptr(state_out), _ptr(workspace), nbytes)
+    return y, state_out
+
+
+def ttt_ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, y=None, stream=None):
+    """One token of ttt_ssm_forward for each sequence: x [B,H,P], dt [B,H], B,
+    C [B,G,N] (views allowed), state [B,H,N,P] fp32 updated in place. Returns
+    y [B,H,P]."""
+    dev, (Bn, H, P, G, N), args = _ssm_args(x, dt, A, B, C, D, dt_bias)
+    _check(state, "state", (Bn, H, N, P), torch.float32, dev)
+    if y is None:
+        y = torch.empty((Bn, H, P), device=dev, dtype=x.dtype)
+    _check(y, "y", (Bn, H, P), x.dtype, dev)
+    _call(_lib.load().ttt_ssm_step, dev, stream, Bn, H, P, G, N, *args, _ptr(state), _ptr(y))
+    return y
+
+
+def ttt_ssm_backward_workspace(B: int, L: int, H: int, P: int, G: int, N: int) -> int:
+    """Bytes of device workspace ttt_ssm_backward needs."""
+    return _need(_lib.load().ttt_ssm_backward_workspace, B, L, H, P, G, N)
+
+
+def ttt_ssm_backward(x, dt, A, B, C, dy, D=None, dt_bias=None, state=None, dstate_out=None, lens=None,
+                     workspace=None, grads=None, stream=None) -> dict:
+    """Gradients of <dy, y> + <dstate_out, state_out> through ttt_ssm_forward:
+    dx, ddt, dB, dC shaped as their operands in x's type, dA [H] fp32 and, for
+    those of D, dt_bias and state that are given, dD, ddt_bias [H] and dstate
+    [B,H,N,P] fp32. `grads` may hold the outputs (a dict like the one
+    returned; dx, ddt, dB, dC may be strided, slices of one buffer too)."""
+    dev, (Bn, L, H, P, G, N), args = _ssm_args(x, dt, A, B, C, D, dt_bias)
+    _check(dy, "dy", (Bn, L, H, P), x.dtype, dev, contiguous=False)
+    shapes = {"dx": ((Bn, L, H, P), x.dtype), "ddt": ((Bn, L, H), x.dtype), "dA": ((H,), torch.float32),
+              "dB": ((Bn, L, G, N), x.dtype), "dC": ((Bn, L, G, N), x.dtype)}
+    if D is not None:
+        shapes["dD"] = ((H,), torch.float32)
+    if dt_bias is not None:
+        shapes["ddt_bias"] = ((H,), torch.float32)
+    if state is not None:
+        _check(state, "state", (Bn, H, N, P), torch.float32, dev)
+        shapes["dstate"] = ((Bn, H, N, P), torch.float32)
+    if dstate_out is not None:
+        _check(dstate_out, "dstate_out", (Bn, H, N, P), torch.float32, dev)
+    g = _grads(grads, dev, shapes)
+    workspace, nbytes = _workspace(workspace, ttt_ssm_backward_workspace(Bn, L, H, P, G, N), dev)
+    _call(_lib.load().ttt_ssm_backward, dev, stream, Bn, L, H, P, G, N, *args, _ptr(state),
+          _lens(lens, Bn, dev), _ptr(dy), _rows(dy, "dy", _S3), _ptr(dstate_out),
+          _ptr(g["dx"]), _rows(g["dx"], "dx", _S3), _ptr(g["ddt"]), _rows(g["ddt"], "ddt", _S3, 0),
+          _plain(g, "dA"), _ptr(g["dB"]), _rows(g["dB"], "dB", _S3), _ptr(g["dC"]),
+          _rows(g["dC"], "dC", _S3), _plain(g, "dD"), _plain(g, "ddt_bias"), _plain(g, "dstate"),
+          _ptr(workspace), nbytes)
+    return g
+
+
 # --- norms, gate and residual between two blocks -------------------------------
 
 

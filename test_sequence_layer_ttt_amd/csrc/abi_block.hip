@@ -6,6 +6,7 @@
 
 #include "abi_common.hpp"
 #include "block.hpp"
+#include "ssm.hpp"
 
 using namespace ttt::abi;
 
@@ -368,6 +369,162 @@ int ttt_block_norm_backward(int B, int L, int D, int io, int resid_io, int layer
                        dresid_out, dx, dresid, dy, dgate, dpost_gamma, dpost_beta, dpre_gamma, dpre_beta, dscale,
                        static_cast<float *>(workspace)};
     return launched(ttt::launch_block_norm_backward(g, stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+int ssm_common(int B, int L, int H, int P, int G, int N, int io) {
+    int st;
+    if ((st = check_sizes(B, L, io))) return st;
+    if (P < 1 || P > TTT_SSM_MAX_DIM || N < 1 || N > TTT_SSM_MAX_DIM)
+        return fail(TTT_E_SHAPE, "P = %d or N = %d not in [1, %d]", P, N, TTT_SSM_MAX_DIM);
+    if (H < 1 || G < 1 || H % G) return fail(TTT_E_SHAPE, "H = %d is not a positive multiple of G = %d", H, G);
+    if (static_cast<int64_t>(B) * H > TTT_SSM_MAX_HEADS)
+        return fail(TTT_E_SHAPE, "B*H exceeds %d", TTT_SSM_MAX_HEADS);
+    return TTT_OK;
+}
+
+// a grid's workgroups and its threads (up to 512 a workgroup) are counted in 32 bits
+int ssm_plan(int B, int L, int H, int P, int N, bool backward, int *nseg, int *seglen) {
+    ttt::ssm_segments(B, L, H, P, N, false, backward, nseg, seglen);
+    if (static_cast<int64_t>(B) * H * *nseg > TTT_SSM_MAX_HEADS)
+        return fail(TTT_E_SHAPE, "B*H*L is too large (B = %d, H = %d, L = %d)", B, H, L);
+    return TTT_OK;
+}
+
+ttt::SsmOperand operand(const View &v) { return {v.p, v.sb, v.st, v.sh}; }
+
+// strides of a single token's operand: batch and head
+View token_view(const void *p, const char *name, int64_t nb, int64_t nh, int64_t inner, const int64_t *strides,
+                unsigned es) {
+    View v = view(p, name, nb, 1, nh, inner, nullptr, 0, es);
+    if (strides) {
+        v.sb = strides[0];
+        v.sh = strides[1];
+    }
+    return v;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ttt_ssm_forward_workspace(int B, int L, int H, int P, int G, int N, size_t *bytes) {
+    int st, nseg, seglen;
+    if ((st = ssm_common(B, L, H, P, G, N, TTT_F32)) || (st = ssm_plan(B, L, H, P, N, false, &nseg, &seglen))) return st;
+    if (!bytes) return fail(TTT_E_NULL, "bytes is NULL");
+    *bytes = ttt::ssm_forward_floats(B, H, P, N, nseg) * sizeof(float);
+    return ok();
+}
+
+int ttt_ssm_forward(int B, int L, int H, int P, int G, int N, int io, const void *x, const int64_t *x_strides,
+                    const void *dt, const int64_t *dt_strides, const float *A, const void *Bm,
+                    const int64_t *B_strides, const void *Cm, const int64_t *C_strides, const float *D,
+                    const float *dt_bias, const float *state, const int *lens, void *y, const int64_t *y_strides,
+                    float *state_out, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    int st, nseg, seglen;
+    size_t need;
+    if ((st = ssm_common(B, L, H, P, G, N, io)) || (st = ssm_plan(B, L, H, P, N, false, &nseg, &seglen)) ||
+        (st = ttt_ssm_forward_workspace(B, L, H, P, G, N, &need)))
+        return st;
+    const unsigned es = esize(io);
+    const View vx = view(x, "x", B, L, H, P, x_strides, 3, es), vt = view(dt, "dt", B, L, H, 1, dt_strides, 3, es),
+               vb = view(Bm, "B", B, L, G, N, B_strides, 3, es), vc = view(Cm, "C", B, L, G, N, C_strides, 3, es),
+               vy = view(y, "y", B, L, H, P, y_strides, 3, es);
+    const int64_t sn = static_cast<int64_t>(B) * H * N * P;
+    Views v;
+    if ((st = v.add_in(vx)) || (st = v.add_in(vt)) || (st = v.add_in(flat(A, "A", H, 4))) || (st = v.add_in(vb)) ||
+        (st = v.add_in(vc)) || (st = v.add_in(flat(D, "D", D ? H : 0, 4))) ||
+        (st = v.add_in(flat(dt_bias, "dt_bias", dt_bias ? H : 0, 4))) ||
+        (st = v.add_in(flat(state, "state", state ? sn : 0, 4))) ||
+        (st = v.add_in(flat(lens, "lens", lens ? B : 0, 4))) || (st = v.add_out(vy)) ||
+        (st = v.add_out(flat(state_out, "state_out", state_out ? sn : 0, 4))))
+        return st;
+    if (workspace_bytes < need) return fail(TTT_E_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    if ((st = v.add_out(flat(workspace, "workspace", static_cast<int64_t>(need / 4), 4))) ||
+        (st = v.alias(state_out, state)))
+        return st;
+    if (!B) return ok();
+    ttt::SsmArgs a{B, L, H, P, G, N, io, operand(vx), operand(vt), operand(vb), operand(vc), A, D, dt_bias, state,
+                   lens, operand(vy), state_out, static_cast<float *>(workspace), nseg, seglen};
+    return launched(ttt::launch_ssm_forward(a, stream));
+}
+
+int ttt_ssm_step(int B, int H, int P, int G, int N, int io, const void *x, const int64_t *x_strides, const void *dt,
+                 const int64_t *dt_strides, const float *A, const void *Bm, const int64_t *B_strides, const void *Cm,
+                 const int64_t *C_strides, const float *D, const float *dt_bias, float *state, void *y,
+                 hipStream_t stream) {
+    int st;
+    if ((st = ssm_common(B, 1, H, P, G, N, io))) return st;
+    const unsigned es = esize(io);
+    const View vx = token_view(x, "x", B, H, P, x_strides, es), vt = token_view(dt, "dt", B, H, 1, dt_strides, es),
+               vb = token_view(Bm, "B", B, G, N, B_strides, es), vc = token_view(Cm, "C", B, G, N, C_strides, es),
+               vy = token_view(y, "y", B, H, P, nullptr, es);
+    const int64_t sn = static_cast<int64_t>(B) * H * N * P;
+    Views v;
+    if ((st = v.add_in(vx)) || (st = v.add_in(vt)) || (st = v.add_in(flat(A, "A", H, 4))) || (st = v.add_in(vb)) ||
+        (st = v.add_in(vc)) || (st = v.add_in(flat(D, "D", D ? H : 0, 4))) ||
+        (st = v.add_in(flat(dt_bias, "dt_bias", dt_bias ? H : 0, 4))) ||
+        (st = v.add_out(flat(state, "state", sn, 4))) || (st = v.add_out(vy)) || (st = v.alias()))
+        return st;
+    if (!B) return ok();
+    ttt::SsmArgs a{B, 1, H, P, G, N, io, operand(vx), operand(vt), operand(vb), operand(vc), A, D, dt_bias, nullptr,
+                   nullptr, operand(vy), state, nullptr, 1, 64};
+    return launched(ttt::launch_ssm_step(a, stream));
+}
+
+int ttt_ssm_backward_workspace(int B, int L, int H, int P, int G, int N, size_t *bytes) {
+    int st, nseg, seglen;
+    if ((st = ssm_common(B, L, H, P, G, N, TTT_F32)) || (st = ssm_plan(B, L, H, P, N, true, &nseg, &seglen))) return st;
+    if (!bytes) return fail(TTT_E_NULL, "bytes is NULL");
+    *bytes = ttt::ssm_backward_floats(B, L, H, P, N, nseg) * sizeof(float);
+    return ok();
+}
+
+int ttt_ssm_backward(int B, int L, int H, int P, int G, int N, int io, const void *x, const int64_t *x_strides,
+                     const void *dt, const int64_t *dt_strides, const float *A, const void *Bm,
+                     const int64_t *B_strides, const void *Cm, const int64_t *C_strides, const float *D,
+                     const float *dt_bias, const float *state, const int *lens, const void *dy,
+                     const int64_t *dy_strides, const float *dstate_out, void *dx, const int64_t *dx_strides,
+                     void *ddt, const int64_t *ddt_strides, float *dA, void *dB, const int64_t *dB_strides, void *dC,
+                     const int64_t *dC_strides, float *dD, float *ddt_bias, float *dstate, void *workspace,
+                     size_t workspace_bytes, hipStream_t stream) {
+    int st, nseg, seglen;
+    size_t need;
+    if ((st = ssm_common(B, L, H, P, G, N, io)) || (st = ssm_plan(B, L, H, P, N, true, &nseg, &seglen)) ||
+        (st = ttt_ssm_backward_workspace(B, L, H, P, G, N, &need)))
+        return st;
+    const int64_t sn = static_cast<int64_t>(B) * H * N * P;
+    if ((dD != nullptr) != (D != nullptr)) return fail(TTT_E_NULL, "dD is given exactly when D is");
+    if ((ddt_bias != nullptr) != (dt_bias != nullptr)) return fail(TTT_E_NULL, "ddt_bias is given exactly when dt_bias is");
+    if ((dstate != nullptr) != (state != nullptr) && sn) return fail(TTT_E_NULL, "dstate is given exactly when state is");
+    const unsigned es = esize(io);
+    const View vx = view(x, "x", B, L, H, P, x_strides, 3, es), vt = view(dt, "dt", B, L, H, 1, dt_strides, 3, es),
+               vb = view(Bm, "B", B, L, G, N, B_strides, 3, es), vc = view(Cm, "C", B, L, G, N, C_strides, 3, es),
+               vdy = view(dy, "dy", B, L, H, P, dy_strides, 3, es), vdx = view(dx, "dx", B, L, H, P, dx_strides, 3, es),
+               vdt = view(ddt, "ddt", B, L, H, 1, ddt_strides, 3, es),
+               vdb = view(dB, "dB", B, L, G, N, dB_strides, 3, es), vdc = view(dC, "dC", B, L, G, N, dC_strides, 3, es);
+    Views v;
+    if ((st = v.add_in(vx)) || (st = v.add_in(vt)) || (st = v.add_in(flat(A, "A", H, 4))) || (st = v.add_in(vb)) ||
+        (st = v.add_in(vc)) || (st = v.add_in(flat(D, "D", D ? H : 0, 4))) ||
+        (st = v.add_in(flat(dt_bias, "dt_bias", dt_bias ? H : 0, 4))) ||
+        (st = v.add_in(flat(state, "state", state ? sn : 0, 4))) ||
+        (st = v.add_in(flat(lens, "lens", lens ? B : 0, 4))) || (st = v.add_in(vdy)) ||
+        (st = v.add_in(flat(dstate_out, "dstate_out", dstate_out ? sn : 0, 4))) || (st = v.add_out(vdx)) ||
+        (st = v.add_out(vdt)) || (st = v.add_out(flat(dA, "dA", H, 4))) || (st = v.add_out(vdb)) ||
+        (st = v.add_out(vdc)) || (st = v.add_out(flat(dD, "dD", dD ? H : 0, 4))) ||
+        (st = v.add_out(flat(ddt_bias, "ddt_bias", ddt_bias ? H : 0, 4))) ||
+        (st = v.add_out(flat(dstate, "dstate", dstate ? sn : 0, 4))))
+        return st;
+    if (workspace_bytes < need) return fail(TTT_E_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    if ((st = v.add_out(flat(workspace, "workspace", static_cast<int64_t>(need / 4), 4))) || (st = v.alias())) return st;
+    ttt::SsmBwdArgs g{{B, L, H, P, G, N, io, operand(vx), operand(vt), operand(vb), operand(vc), A, D, dt_bias,
+                       state, lens, {nullptr, 0, 0, 0}, nullptr, static_cast<float *>(workspace), nseg, seglen},
+                      operand(vdy), dstate_out, operand(vdx), operand(vdt), operand(vdb), operand(vdc), dA, dD,
+                      ddt_bias, dstate};
+    return launched(ttt::launch_ssm_backward(g, stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,79 @@
+// Internal interface of the selective state space scan (see ttt.h for the
+// formulas). A sequence is cut into segments; each segment's own contribution
+// to the state is formed for all segments at once, carried over the segments
+// in order, and the outputs are then formed for all segments at once from the
+// states at their borders.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ttt {
+
+// A per-token, per-head operand: element (b, t, h, i) at p + b*sb + t*st + h*sh + i.
+// `shared`: h counts groups of heads.
+struct SsmOperand {
+    const void *p;
+    int64_t sb, st, sh;
+};
+
+struct SsmArgs {
+    int B, L, H, P, G, N, io;
+    SsmOperand x, dt, Bm, Cm;  // dt has no innermost dimension
+    const float *A, *D, *dt_bias;  // [H]; D, dt_bias may be null
+    const float *state;            // [B,H,N,P] or null
+    const int *lens;
+    SsmOperand y;
+    float *state_out;  // [B,H,N,P] or null
+    float *ws;
+    int nseg, seglen;
+};
+
+struct SsmBwdArgs {
+    SsmArgs f;
+    SsmOperand dy;
+    const float *dstate_out;  // [B,H,N,P] or null
+    SsmOperand dx, ddt, dB, dC;
+    float *dA, *dD, *ddt_bias, *dstate;  // dD, ddt_bias, dstate may be null
+};
+
+// segments of the forward and of the backward
+void ssm_segments(int B, int L, int H, int P, int N, bool mfma, bool backward, int *nseg, int *seglen);
+bool ssm_mfma_supported(const SsmArgs &a);
+// workspace floats
+size_t ssm_forward_floats(int B, int H, int P, int N, int nseg);
+size_t ssm_backward_floats(int B, int L, int H, int P, int N, int nseg);
+
+hipError_t launch_ssm_step(const SsmArgs &a, hipStream_t stream);  // L = 1, state_out in place
+hipError_t launch_ssm_forward(const SsmArgs &a, hipStream_t stream);
+hipError_t launch_ssm_backward(const SsmBwdArgs &a, hipStream_t stream);
+
+// Parts of the launches above.
+//
+// The carry over segments, forward: S[0] = state, S[s+1] = decay[s] S[s] +
+// share[s]; on entry seg holds the shares [B,H,nseg,N,P], on return the state
+// before each segment. Reverse: S[nseg] = last, S[s] = decay[s] S[s+1] +
+// share[s]; on return seg[s] = S[s+1], the state's gradient behind segment s.
+// `out` (or null) receives what the walk ends with.
+hipError_t launch_ssm_carry(int BH, int NP, int nseg, bool reverse, const float *first, const float *decay,
+                            float *seg, float *out, hipStream_t stream);
+
+// What the backward's second half needs: per-token sums over a head's
+// features (pb blocks of them), see ssm_bwd.hip.
+struct SsmBwdWs {
+    float *sf, *sr;          // [B,H,nseg,N,P] states before, gradients behind each segment
+    float *last;             // [B,H,N,P] state after the last segment
+    float *decay;            // [B,H,nseg]
+    float *dBh, *dCh;        // [B,H,L,N] per head
+    float *row, *col, *xdu, *dyx;  // [2,B,H,L] partial sums (two blocks of features)
+    float *part;             // [B*nseg][3][H]
+    size_t floats;           // of all of them
+};
+SsmBwdWs ssm_backward_ws(const SsmArgs &a);
+hipError_t launch_ssm_bwd_finish(const SsmBwdArgs &g, int blocks_row, int blocks_col, hipStream_t stream);
+
+hipError_t launch_ssm_states_valu(const SsmArgs &a, const SsmOperand *dy, float *seg, float *decay,
+                                  hipStream_t stream);
+hipError_t launch_ssm_mfma(const SsmArgs &a, hipStream_t stream);
+
+}  // namespace ttt

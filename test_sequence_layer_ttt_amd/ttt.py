@@ -14,7 +14,9 @@ import torch
 from . import _lib
 from ._lib import TTT_BF16, TTT_F32, TTTError  # noqa: F401
 from .block import (ttt_block_norm, ttt_block_norm_backward, ttt_block_norm_backward_workspace,  # noqa: F401
-                    ttt_conv_backward, ttt_conv_backward_workspace, ttt_conv_forward, ttt_conv_step)
+                    ttt_conv_backward, ttt_conv_backward_workspace, ttt_conv_forward, ttt_conv_step,
+                    ttt_ssm_backward, ttt_ssm_backward_workspace, ttt_ssm_forward,
+                    ttt_ssm_forward_workspace, ttt_ssm_step)
 
 _IO = {torch.float32: TTT_F32, torch.bfloat16: TTT_BF16}
 

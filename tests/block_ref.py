@@ -36,8 +36,9 @@ def conv(x, w, bias, state, act, lens):
     return torch.stack(y), torch.stack(so)
 
 
-def scan(x, dt, A, Bm, Cm, D, dt_bias, state, lens):
-    """(y, state_out) of the state space scan, token by token."""
+def scan(x, dt, A, Bm, Cm, D, dt_bias, state, lens, dt_in=None):
+    """(y, state_out) of the state space scan, token by token. dt_in: a second
+    dt for the inputs alone, to tell its two gradients apart."""
     B, L, H, P = x.shape
     G, N = Bm.shape[2:]
     n, _ = live(lens, B, L)
@@ -49,7 +50,11 @@ def scan(x, dt, A, Bm, Cm, D, dt_bias, state, lens):
         for t in range(int(n[b])):
             z = dt[b, t] + (0 if dt_bias is None else dt_bias)
             d = torch.logaddexp(z, torch.zeros_like(z))
-            h = torch.exp(d * A)[:, None, None] * h + Bm[b, t][head][:, :, None] * (d[:, None] * x[b, t])[:, None, :]
+            a = torch.exp(d * A)
+            if dt_in is not None:
+                z = dt_in[b, t] + (0 if dt_bias is None else dt_bias)
+                d = torch.logaddexp(z, torch.zeros_like(z))
+            h = a[:, None, None] * h + Bm[b, t][head][:, :, None] * (d[:, None] * x[b, t])[:, None, :]
             row = (Cm[b, t][head][:, :, None] * h).sum(1)
             rows.append(row if D is None else row + D[:, None] * x[b, t])
         rows += [x.new_zeros(H, P)] * (L - int(n[b]))
