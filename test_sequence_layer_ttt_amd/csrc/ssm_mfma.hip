@@ -1,5 +1,283 @@
-#include "ssm.hpp"
+// The selective state space scan on the matrix cores: bf16 features, P = 64,
+// N = 32, 64 or 128 (formulas in ttt.h). A workgroup of four waves walks over
+// the 64-token chunks of one head's segment. With l_i the sum of D_t A over
+// the chunk's tokens up to i and S the state before the chunk, a chunk is
+//     M_ij = (C_i . B_j) exp(l_i - l_j) D_j  for j <= i, else 0
+//     Y = M X + diag(exp(l)) C S + D X
+//     S <- exp(l_63) S + (B diag(exp(l_63 - l) D))^T X.
+//  * Wave w makes the outputs of tokens 16 w .. + 15, all transposed: B C^T
+//    gives M^T with four tokens j of one i in a lane, which is the operand of
+//    X^T M^T as it stands (no trip through LDS); Y^T gives eight features of
+//    one token to a lane, one 16-byte store.
+//  * The state lives in accumulators, fp32: wave w holds N / 4 of its rows
+//    (N = 32: half of the columns of 16). Its update takes X exactly as it is
+//    and B D exp(..) split into three bf16 parts, so the state is that of fp32
+//    arithmetic; only its copy for C S, in LDS, is rounded to bf16, as is M.
+//  * X and B of the next chunk are fetched to registers while this one is
+//    worked on, C straight to the fragment that needs it; X^T and B^T are read
+//    from the row-major tiles by transposing LDS reads.
+//  * Few heads: the sequence is cut into segments that run side by side. A
+//    first launch of the same walk without outputs gives each segment's share
+//    of the state, carried over the segments by ssm_carry.
+// Floor: x, y once (2 * 128 bytes a token and head), B and C from the L2 that
+// the heads of a segment share; about 8 N * 64 + 4 * 64 * (N + 64) flops a
+// token and head.
+#include "ssm_tile.hpp"
+
 namespace ttt {
-bool ssm_mfma_supported(const SsmArgs &) { return false; }
-hipError_t launch_ssm_mfma(const SsmArgs &, hipStream_t) { return hipErrorNotSupported; }
+namespace {
+
+using namespace ssm;
+
+template <int N, bool OUT> struct Smem {
+    static constexpr int NS = N + 8;
+    uint16_t x[2][Q * XS];   // [token][feature]
+    uint16_t b[2][Q * NS];   // [token][n]
+    uint16_t s[OUT ? 64 * NS : 8];  // the state's bf16 copy, [feature][n]
+    ChunkDecay d[2];
+};
+
+struct MfmaArgs {
+    SsmArgs a;
+    const float *init;    // [B,H,(nseg,)N,P]
+    int64_t init_stride;  // as in WalkArgs
+    float *fin, *decay;
+};
+
+template <int N, bool OUT>
+__global__ __launch_bounds__(256) void chunks(MfmaArgs w) {
+    constexpr int NS = Smem<N, OUT>::NS, KB = N / 32;
+    constexpr int NT = N >= 64 ? N / 64 : 1;  // row tiles of the state in a wave
+    constexpr int UT = N >= 64 ? 4 : 2;       // its feature tiles
+    __shared__ Smem<N, OUT> sm;
+    const SsmArgs &a = w.a;
+    const int lane = threadIdx.x % 64, wv = threadIdx.x / 64, g = lane / 16, c = lane % 16;
+    int bs, h;
+    place(blockIdx.x, a.B * a.nseg, a.H, bs, h);
+    const int b = bs / a.nseg, seg = bs % a.nseg, gr = h / (a.H / a.G), bh = b * a.H + h;
+    const int n = a.lens ? max(0, min(a.lens[b], a.L)) : a.L;
+    const int64_t s0 = static_cast<int64_t>(seg) * a.seglen;
+    const int t0 = static_cast<int>(s0 < a.L ? s0 : a.L);
+    const int t1 = static_cast<int>(s0 + a.seglen < a.L ? s0 + a.seglen : a.L);
+    const int te = max(t0, min(t1, n));
+    const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
+    const bf16_t *xp = static_cast<const bf16_t *>(a.x.p) + b * a.x.sb + h * a.x.sh;
+    const bf16_t *bp = static_cast<const bf16_t *>(a.Bm.p) + b * a.Bm.sb + gr * a.Bm.sh;
+    const bf16_t *cp = static_cast<const bf16_t *>(a.Cm.p) + b * a.Cm.sb + gr * a.Cm.sh;
+    const bf16_t *dp = static_cast<const bf16_t *>(a.dt.p) + b * a.dt.sb + h * a.dt.sh;
+    bf16_t *yp = static_cast<bf16_t *>(const_cast<void *>(a.y.p)) + b * a.y.sb + h * a.y.sh;
+    const int nt0 = N >= 64 ? NT * wv : wv % 2, u0 = N >= 64 ? 0 : 2 * (wv / 2);
+    constexpr int64_t NP = static_cast<int64_t>(N) * 64;
+
+    f32x4 st[NT][UT];
+    const float *init = w.init ? w.init + (w.init_stride ? (static_cast<int64_t>(bh) * a.nseg + seg) * NP : bh * NP) : nullptr;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int u = 0; u < UT; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                st[i][u][r] = init ? init[(16 * (nt0 + i) + 4 * g + r) * 64 + feature(u0 + u, c)] : 0.f;
+
+    Stage<64> sx;
+    Stage<N> sb;
+    bf16x8 cf[KB], cn[KB];
+    float dt = 0.f;
+    auto fetch = [&](int t) {  // the chunk at token t < te
+        const int count = min(Q, te - t);
+        sx.fetch(xp + static_cast<int64_t>(t) * a.x.st, a.x.st, count);
+        sb.fetch(bp + static_cast<int64_t>(t) * a.Bm.st, a.Bm.st, count);
+        if constexpr (OUT) {
+            const bf16_t *p = cp + static_cast<int64_t>(t + min(16 * wv + c, count - 1)) * a.Cm.st + 8 * g;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) cn[kb] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4 *>(p + 32 * kb));
+        }
+        if (wv == 0 && lane < count) dt = bf16_to_f32(dp[static_cast<int64_t>(t + lane) * a.dt.st]);
+    };
+    auto put = [&](int t, int buf) {
+        sx.put(sm.x[buf], XS);
+        sb.put(sm.b[buf], NS);
+        if (wv == 0) chunk_decay<bf16_t>(sm.d[buf], a, dt, bias, A, lane, min(Q, te - t));
+    };
+    auto share_state = [&]() {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int u = 0; u < UT; ++u)
+                *reinterpret_cast<s16x4 *>(&sm.s[feature(u0 + u, c) * NS + 16 * (nt0 + i) + 4 * g]) = pack4(st[i][u]);
+    };
+    float total = 0.f;
+    if (t0 < te) {
+        fetch(t0);
+        put(t0, 0);
+        if constexpr (OUT) share_state();
+    }
+    int buf = 0;
+    for (int t = t0; t < te; t += Q, buf ^= 1) {
+        __syncthreads();
+        if constexpr (OUT) {
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) cf[kb] = cn[kb];
+        }
+        const bool more = t + Q < te;
+        if (more) fetch(t + Q);
+        const uint16_t *x = sm.x[buf], *bt = sm.b[buf];
+        const ChunkDecay &d = sm.d[buf];
+        bf16x8 xf[2][4];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) xf[kb][u] = tokens_frag(x, XS, kb, u, g, c);
+        if constexpr (OUT) {
+            const int i = 16 * wv + c;  // this lane's token
+            const float hi = d.hi[i], lo = d.lo[i];
+            bf16x8 mf[2];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                f32x4 m[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int jt = 2 * kb + k;
+                    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                    if (jt <= wv) {
+#pragma unroll
+                        for (int q = 0; q < KB; ++q)
+                            acc = mfma32(read16(&bt[(16 * jt + c) * NS + 32 * q + 8 * g]), cf[q], acc);
+                        const int j = 16 * jt + 4 * g;
+                        const f32x4 hj = *reinterpret_cast<const f32x4 *>(&d.hi[j]);
+                        const f32x4 lj = *reinterpret_cast<const f32x4 *>(&d.lo[j]);
+                        const f32x4 sj = *reinterpret_cast<const f32x4 *>(&d.step[j]);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float e = fast_exp2((hi - hj[r]) + (lo - lj[r])) * sj[r];
+                            acc[r] = j + r <= i ? acc[r] * e : 0.f;
+                        }
+                    }
+                    m[k] = acc;
+                }
+                mf[kb] = pack8(m[0], m[1]);
+            }
+            f32x4 y[4];
+            const float ei = fast_exp2(hi);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                y[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < KB; ++q) y[u] = mfma32(read16(&sm.s[feature(u, c) * NS + 32 * q + 8 * g]), cf[q], y[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) y[u][r] *= ei;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                if (2 * kb <= wv) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) y[u] = mfma32(xf[kb][u], mf[kb], y[u]);
+                }
+            }
+            if (t + i < te) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float xv[8], o[8];
+                    vec_load<bf16_t, 8>(&x[i * XS + 32 * q + 8 * g], xv);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = fmaf(Dh, xv[e], y[2 * q + e / 4][e % 4]);
+                    VecIO<bf16_t, 8>::store(yp + static_cast<int64_t>(t + i) * a.y.st + 32 * q + 8 * g, o);
+                }
+            }
+        }
+        const float whole = fast_exp2(d.total);
+        total += d.total;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int u = 0; u < UT; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) st[i][u][r] *= whole;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            const int j0 = 32 * kb + 4 * g, j1 = j0 + 16;
+            f32x4 w0 = *reinterpret_cast<const f32x4 *>(&d.tail[j0]), w1 = *reinterpret_cast<const f32x4 *>(&d.tail[j1]);
+            const f32x4 p0 = *reinterpret_cast<const f32x4 *>(&d.step[j0]), p1 = *reinterpret_cast<const f32x4 *>(&d.step[j1]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                w0[r] *= p0[r];
+                w1[r] *= p1[r];
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                bf16x8 bw[3];
+                weigh(tokens_frag16(bt, NS, kb, 16 * (nt0 + i), g, c), w0, w1, bw);
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+#pragma unroll
+                    for (int u = 0; u < UT; ++u)
+                        st[i][u] = mfma32(bw[k], N >= 64 || wv < 2 ? xf[kb][u] : xf[kb][2 + u % 2], st[i][u]);
+            }
+        }
+        if (more) put(t + Q, buf ^ 1);
+        if constexpr (OUT) {
+            if (more) {
+                __syncthreads();  // every wave has read the state's copy
+                share_state();
+            }
+        }
+    }
+    if constexpr (OUT) {  // rows past the sequence's end are zeros
+        for (int t = te + threadIdx.x / 8; t < t1; t += 32)
+            *reinterpret_cast<uint4 *>(yp + static_cast<int64_t>(t) * a.y.st + threadIdx.x % 8 * 8) = make_uint4(0, 0, 0, 0);
+    }
+    if (w.fin) {
+        float *f = w.fin + (static_cast<int64_t>(bh) * (OUT ? 1 : a.nseg) + (OUT ? 0 : seg)) * NP;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int u = 0; u < UT; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) f[(16 * (nt0 + i) + 4 * g + r) * 64 + feature(u0 + u, c)] = st[i][u][r];
+    }
+    if (!OUT && threadIdx.x == 0) w.decay[static_cast<int64_t>(bh) * a.nseg + seg] = exp2f(total);
+}
+
+template <bool OUT> hipError_t run(const MfmaArgs &w, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(w.a.B) * w.a.H * w.a.nseg);
+    if (w.a.N == 32)
+        hipLaunchKernelGGL((chunks<32, OUT>), grid, dim3(256), 0, s, w);
+    else if (w.a.N == 64)
+        hipLaunchKernelGGL((chunks<64, OUT>), grid, dim3(256), 0, s, w);
+    else
+        hipLaunchKernelGGL((chunks<128, OUT>), grid, dim3(256), 0, s, w);
+    return hipGetLastError();
+}
+
+bool wide(const SsmOperand &o) {  // rows of 16-byte accesses
+    return (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && o.sb % 8 == 0 && o.st % 8 == 0 && o.sh % 8 == 0;
+}
+
+}  // namespace
+
+bool ssm_mfma_supported(const SsmArgs &a) {
+    return a.io == 1 && a.P == 64 && (a.N == 32 || a.N == 64 || a.N == 128) && wide(a.x) && wide(a.Bm) &&
+           wide(a.Cm) && wide(a.y);
+}
+
+hipError_t launch_ssm_mfma(const SsmArgs &a, hipStream_t stream) {
+    const int64_t NP = static_cast<int64_t>(a.N) * a.P;
+    MfmaArgs w{a, a.state, 0, a.state_out, nullptr};
+    if (a.nseg > 1) {
+        float *seg = a.ws, *decay = a.ws + static_cast<int64_t>(a.B) * a.H * a.nseg * NP;
+        MfmaArgs p{a, nullptr, 0, seg, decay};
+        hipError_t e;
+        if ((e = run<false>(p, stream)) != hipSuccess) return e;
+        if ((e = launch_ssm_carry(a.B * a.H, static_cast<int>(NP), a.nseg, false, a.state, decay, seg, a.state_out,
+                                  stream)) != hipSuccess)
+            return e;
+        w.init = seg;
+        w.init_stride = NP;
+        w.fin = nullptr;
+    }
+    return run<true>(w, stream);
+}
+
 }  // namespace ttt

@@ -1,0 +1,166 @@
+// Pieces of the state space scan's MFMA kernels (gfx950): 64-token chunks of
+// bf16 operands in LDS, transposed fragment reads, and the chunk's decays.
+//
+// 16x16x32 products: lane (g = lane / 16, c = lane % 16) gives row or column c
+// and, of the contraction, either 32 kb + 8 g .. + 7 (features: 16 bytes of a
+// row) or tokens 32 kb + 4 g .. + 3 and 32 kb + 16 + 4 g .. + 3 (the order in
+// which two products' outputs lie in a lane, so an output tile is the next
+// product's operand as it stands). It receives rows 4 g .. 4 g + 3 of column c.
+#pragma once
+
+#include "ssm.hpp"
+#include "vec.hpp"
+
+namespace ttt {
+namespace ssm {
+
+using namespace tile;
+
+constexpr int Q = 64;       // tokens of a chunk
+constexpr int XS = 64 + 8;  // row stride (elements) of 64 features: rows 4 banks apart
+constexpr float LOG2E = 1.4426950408889634f;
+
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// Four tokens' values of one feature for each lane: in a group of 16 lanes,
+// lane 4 r + q points at four features of row r; lane 4 q + s receives feature
+// s of those that q points at, of rows 0 .. 3.
+__device__ __forceinline__ s16x4 read_tr(const uint16_t *p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p));
+}
+__device__ __forceinline__ bf16x8 join(s16x4 a, s16x4 b) {
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+__device__ __forceinline__ bf16x8 read16(const uint16_t *p) {
+    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4 *>(p));
+}
+
+// Feature of row or column c of feature tile u, where 64 features are cut into
+// four tiles such that a lane's rows of tiles 2 q and 2 q + 1 are the eight
+// features 32 q + 8 g .. + 7 (one 16-byte access).
+__device__ __forceinline__ int feature(int u, int c) { return 32 * (u / 2) + 8 * (c / 4) + 4 * (u % 2) + c % 4; }
+
+// Transposed fragment (contraction over tokens 32 kb .. + 31) of feature tile
+// u of a [64 tokens][stride] tile, features from `f0` on in the order above.
+__device__ __forceinline__ bf16x8 tokens_frag(const uint16_t *tile, int stride, int kb, int u, int g, int c) {
+    const uint16_t *p = tile + (32 * kb + 4 * g + c / 4) * stride + 32 * (u / 2) + 8 * (c % 4) + 4 * (u % 2);
+    return join(read_tr(p), read_tr(p + 16 * stride));
+}
+// the same of 16 adjacent features n0 .. n0 + 15
+__device__ __forceinline__ bf16x8 tokens_frag16(const uint16_t *tile, int stride, int kb, int n0, int g, int c) {
+    const uint16_t *p = tile + (32 * kb + 4 * g + c / 4) * stride + n0 + 4 * (c % 4);
+    return join(read_tr(p), read_tr(p + 16 * stride));
+}
+
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_add64(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, ROWS, 0xF, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, ROWS, 0xF, true);
+    return v + __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+// Inclusive sums over the lanes 0 .. lane: within rows of 16 lanes, then the
+// rows' totals.
+__device__ __forceinline__ double wave_scan(double v) {
+    v = dpp_add64<0x111, 0xF>(v);  // row_shr:1
+    v = dpp_add64<0x112, 0xF>(v);  // row_shr:2
+    v = dpp_add64<0x114, 0xF>(v);  // row_shr:4
+    v = dpp_add64<0x118, 0xF>(v);  // row_shr:8
+    v = dpp_add64<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+    v = dpp_add64<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
+    return v;
+}
+
+// Per token of a chunk: log2 of the decay since the chunk's start, split into
+// two floats (their differences are decays between two tokens: one float would
+// lose up to |sum| 2^-24 of them), and D_t; the decay to the chunk's end.
+struct ChunkDecay {
+    alignas(16) float hi[Q], lo[Q], step[Q], tail[Q];
+    float total;  // log2 of the whole chunk's decay
+};
+
+// One wave, lane = token. Tokens at and past `count` decay nothing and add
+// nothing. A factor below 2^-160 is zero in fp32 as it is, so the logarithms
+// are held above that.
+template <typename T>
+__device__ __forceinline__ void chunk_decay(ChunkDecay &d, const SsmArgs &a, float raw_dt, float bias, float A,
+                                            int lane, int count) {
+    const float step = lane < count ? softplus_f(raw_dt + bias) : 0.f;
+    const double l = lane < count ? fmax(static_cast<double>(step) * A * 1.4426950408889634, -160.0) : 0.0;
+    const double s = wave_scan(l);
+    const double all = __shfl(s, 63, 64);
+    const float hi = static_cast<float>(s);
+    d.hi[lane] = hi;
+    d.lo[lane] = static_cast<float>(s - hi);
+    d.step[lane] = step;
+    d.tail[lane] = exp2f(static_cast<float>(all - s));
+    if (lane == 0) d.total = static_cast<float>(all);
+}
+
+// x = a + b + c to about 24 bits, each a bf16 (two floats at a time)
+__device__ __forceinline__ void split3(float x0, float x1, uint32_t &a, uint32_t &b, uint32_t &c) {
+    a = pack2(x0, x1);
+    x0 -= lo_bf(a);
+    x1 -= hi_bf(a);
+    b = pack2(x0, x1);
+    c = pack2(x0 - lo_bf(b), x1 - hi_bf(b));
+}
+
+// A fragment of a transposed read times one weight for each of its tokens
+// (w0: the first four, w1: the others), in three bf16 parts.
+__device__ __forceinline__ void weigh(bf16x8 f, f32x4 w0, f32x4 w1, bf16x8 (&out)[3]) {
+    const uint4 r = __builtin_bit_cast(uint4, f);
+    const uint32_t in[4] = {r.x, r.y, r.z, r.w};
+    uint32_t p[3][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = lo_bf(in[i]) * (i < 2 ? w0[2 * i] : w1[2 * i - 4]);
+        const float b = hi_bf(in[i]) * (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]);
+        split3(a, b, p[0][i], p[1][i], p[2][i]);
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) out[k] = __builtin_bit_cast(bf16x8, make_uint4(p[k][0], p[k][1], p[k][2], p[k][3]));
+}
+
+__device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// 64 rows of F features (F = 32, 64, 128) from global memory to LDS by 256
+// threads, 16 bytes each, through registers: fetched while the chunk before is
+// worked on. Rows at and past `count` are zeros and are not read.
+template <int F> struct Stage {
+    static constexpr int PER = F / 8;         // accesses of a row
+    static constexpr int ROWS = 256 / PER;    // rows of a pass
+    static constexpr int NP = Q / ROWS;       // passes
+    uint4 r[NP];
+    __device__ __forceinline__ void fetch(const bf16_t *base, int64_t stride, int count) {
+        const int row = threadIdx.x / PER, f = threadIdx.x % PER * 8;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int t = row + i * ROWS;
+            r[i] = make_uint4(0, 0, 0, 0);
+            if (t < count) r[i] = *reinterpret_cast<const uint4 *>(base + t * stride + f);
+        }
+    }
+    __device__ __forceinline__ void put(uint16_t *tile, int lds_stride) const {
+        const int row = threadIdx.x / PER, f = threadIdx.x % PER * 8;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) *reinterpret_cast<uint4 *>(tile + (row + i * ROWS) * lds_stride + f) = r[i];
+    }
+};
+
+// Workgroup -> (sequence and segment, head) such that the heads of one segment,
+// which read the same B and C, run on one XCD (workgroups go to the eight XCDs
+// in turn). The last few segments that do not fill a round of eight are spread.
+__device__ __forceinline__ void place(int blk, int segs, int heads, int &bs, int &h) {
+    const int full = segs / 8 * 8;
+    if (blk < full * heads) {
+        const int i = blk / 8;
+        bs = i / heads * 8 + blk % 8;
+        h = i % heads;
+    } else {
+        bs = blk / heads;
+        h = blk % heads;
+    }
+}
+
+}  // namespace ssm
+}  // namespace ttt
