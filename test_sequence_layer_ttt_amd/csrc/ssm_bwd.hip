@@ -172,18 +172,19 @@ size_t ssm_forward_floats(int B, int H, int P, int N, int nseg) {
 
 void ssm_segments(int B, int L, int H, int P, int N, bool mfma, bool backward, int *nseg, int *seglen) {
     (void)P;
-    (void)N;
-    // about 768 workgroups, segments of whole 64-token chunks; the backward's
-    // running sums over a segment hold at most 256 tokens
+    (void)mfma;
+    // as many workgroups as run at once (three a compute unit, two where N
+    // takes more of its LDS and registers), segments of whole 64-token chunks;
+    // the backward's running sums over a segment hold at most 256 tokens
+    const int64_t slots = N > 64 ? 512 : 768;
     const int64_t heads = static_cast<int64_t>(B) * H;
     const int64_t chunks = (static_cast<int64_t>(L) + 63) / 64;
-    int64_t want = heads > 0 ? (768 + heads - 1) / heads : 1;
+    int64_t want = heads > 0 ? slots / heads : 1;
     if (want > chunks) want = chunks;
     if (want < 1) want = 1;
     int64_t per = (chunks + want - 1) / want;
     if (backward && per > 4) per = 4;
     if (per < 1) per = 1;
-    (void)mfma;
     *seglen = static_cast<int>(per * 64);
     *nseg = static_cast<int>(chunks > 0 ? (chunks + per - 1) / per : 1);
 }

@@ -7,8 +7,8 @@
 //     S <- exp(l_63) S + (B diag(exp(l_63 - l) D))^T X.
 //  * Wave w makes the outputs of tokens 16 w .. + 15, all transposed: B C^T
 //    gives M^T with four tokens j of one i in a lane, which is the operand of
-//    X^T M^T as it stands (no trip through LDS); Y^T gives eight features of
-//    one token to a lane, one 16-byte store.
+//    X^T M^T as it stands (no trip through LDS); Y^T gives four adjacent
+//    features of one token to a lane.
 //  * The state lives in accumulators, fp32: wave w holds N / 4 of its rows
 //    (N = 32: half of the columns of 16). Its update takes X exactly as it is
 //    and B D exp(..) split into three bf16 parts, so the state is that of fp32
@@ -35,6 +35,7 @@ template <int N, bool OUT> struct Smem {
     uint16_t b[2][Q * NS];   // [token][n]
     uint16_t s[OUT ? 64 * NS : 8];  // the state's bf16 copy, [feature][n]
     ChunkDecay d[2];
+    alignas(16) float f[OUT ? 4 : 1][Q];  // each wave's decays to its tokens' tile
 };
 
 struct MfmaArgs {
@@ -45,7 +46,7 @@ struct MfmaArgs {
 };
 
 template <int N, bool OUT>
-__global__ __launch_bounds__(256) void chunks(MfmaArgs w) {
+__global__ __launch_bounds__(256, N == 128 ? 2 : 3) void chunks(MfmaArgs w) {
     constexpr int NS = Smem<N, OUT>::NS, KB = N / 32;
     constexpr int NT = N >= 64 ? N / 64 : 1;  // row tiles of the state in a wave
     constexpr int UT = N >= 64 ? 4 : 2;       // its feature tiles
@@ -77,7 +78,7 @@ __global__ __launch_bounds__(256) void chunks(MfmaArgs w) {
         for (int u = 0; u < UT; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                st[i][u][r] = init ? init[(16 * (nt0 + i) + 4 * g + r) * 64 + feature(u0 + u, c)] : 0.f;
+                st[i][u][r] = init ? init[(16 * (nt0 + i) + 4 * g + r) * 64 + 16 * (u0 + u) + c] : 0.f;
 
     Stage<64> sx;
     Stage<N> sb;
@@ -104,7 +105,7 @@ __global__ __launch_bounds__(256) void chunks(MfmaArgs w) {
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int u = 0; u < UT; ++u)
-                *reinterpret_cast<s16x4 *>(&sm.s[feature(u0 + u, c) * NS + 16 * (nt0 + i) + 4 * g]) = pack4(st[i][u]);
+                *reinterpret_cast<s16x4 *>(&sm.s[(16 * (u0 + u) + c) * NS + 16 * (nt0 + i) + 4 * g]) = pack4(st[i][u]);
     };
     float total = 0.f;
     if (t0 < te) {
@@ -127,10 +128,16 @@ __global__ __launch_bounds__(256) void chunks(MfmaArgs w) {
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) xf[kb][u] = tokens_frag(x, XS, kb, u, g, c);
+            for (int u = 0; u < 4; ++u) xf[kb][u] = tokens_frag(x, XS, kb, 16 * u, g, c);
         if constexpr (OUT) {
             const int i = 16 * wv + c;  // this lane's token
-            const float hi = d.hi[i], lo = d.lo[i];
+            const float hi = d.hi[i];
+            // decay from a token j of an earlier tile to the end of the tile
+            // before this wave's, times D_j (one exp a lane), and from there
+            // to token i: neither is above 1
+            const float edge = wv ? d.hi[16 * wv - 1] : 0.f;
+            sm.f[wv][lane] = fast_exp2(fminf(edge - d.hi[lane], 0.f)) * d.step[lane];
+            const float ef = fast_exp2(hi - edge);
             bf16x8 mf[2];
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
@@ -144,13 +151,16 @@ __global__ __launch_bounds__(256) void chunks(MfmaArgs w) {
                         for (int q = 0; q < KB; ++q)
                             acc = mfma32(read16(&bt[(16 * jt + c) * NS + 32 * q + 8 * g]), cf[q], acc);
                         const int j = 16 * jt + 4 * g;
-                        const f32x4 hj = *reinterpret_cast<const f32x4 *>(&d.hi[j]);
-                        const f32x4 lj = *reinterpret_cast<const f32x4 *>(&d.lo[j]);
-                        const f32x4 sj = *reinterpret_cast<const f32x4 *>(&d.step[j]);
+                        if (jt < wv) {
+                            const f32x4 fj = *reinterpret_cast<const f32x4 *>(&sm.f[wv][j]);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const float e = fast_exp2((hi - hj[r]) + (lo - lj[r])) * sj[r];
-                            acc[r] = j + r <= i ? acc[r] * e : 0.f;
+                            for (int r = 0; r < 4; ++r) acc[r] *= fj[r] * ef;
+                        } else {
+                            const f32x4 hj = *reinterpret_cast<const f32x4 *>(&d.hi[j]);
+                            const f32x4 sj = *reinterpret_cast<const f32x4 *>(&d.step[j]);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                acc[r] = j + r <= i ? acc[r] * (fast_exp2(hi - hj[r]) * sj[r]) : 0.f;
                         }
                     }
                     m[k] = acc;
@@ -163,7 +173,7 @@ __global__ __launch_bounds__(256) void chunks(MfmaArgs w) {
             for (int u = 0; u < 4; ++u) {
                 y[u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int q = 0; q < KB; ++q) y[u] = mfma32(read16(&sm.s[feature(u, c) * NS + 32 * q + 8 * g]), cf[q], y[u]);
+                for (int q = 0; q < KB; ++q) y[u] = mfma32(read16(&sm.s[(16 * u + c) * NS + 32 * q + 8 * g]), cf[q], y[u]);
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u)
@@ -178,12 +188,12 @@ __global__ __launch_bounds__(256) void chunks(MfmaArgs w) {
             }
             if (t + i < te) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float xv[8], o[8];
-                    vec_load<bf16_t, 8>(&x[i * XS + 32 * q + 8 * g], xv);
+                for (int u = 0; u < 4; ++u) {
+                    float xv[4], o[4];
+                    vec_load<bf16_t, 4>(&x[i * XS + 16 * u + 4 * g], xv);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = fmaf(Dh, xv[e], y[2 * q + e / 4][e % 4]);
-                    VecIO<bf16_t, 8>::store(yp + static_cast<int64_t>(t + i) * a.y.st + 32 * q + 8 * g, o);
+                    for (int r = 0; r < 4; ++r) o[r] = fmaf(Dh, xv[r], y[u][r]);
+                    VecIO<bf16_t, 4>::store(yp + static_cast<int64_t>(t + i) * a.y.st + 16 * u + 4 * g, o);
                 }
             }
         }
@@ -208,7 +218,7 @@ __global__ __launch_bounds__(256) void chunks(MfmaArgs w) {
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 bf16x8 bw[3];
-                weigh(tokens_frag16(bt, NS, kb, 16 * (nt0 + i), g, c), w0, w1, bw);
+                weigh(tokens_frag(bt, NS, kb, 16 * (nt0 + i), g, c), w0, w1, bw);
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
 #pragma unroll
@@ -235,7 +245,7 @@ __global__ __launch_bounds__(256) void chunks(MfmaArgs w) {
 #pragma unroll
             for (int u = 0; u < UT; ++u)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) f[(16 * (nt0 + i) + 4 * g + r) * 64 + feature(u0 + u, c)] = st[i][u][r];
+                for (int r = 0; r < 4; ++r) f[(16 * (nt0 + i) + 4 * g + r) * 64 + 16 * (u0 + u) + c] = st[i][u][r];
     }
     if (!OUT && threadIdx.x == 0) w.decay[static_cast<int64_t>(bh) * a.nseg + seg] = exp2f(total);
 }

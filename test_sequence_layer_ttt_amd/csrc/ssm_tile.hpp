@@ -35,20 +35,10 @@ __device__ __forceinline__ bf16x8 read16(const uint16_t *p) {
     return __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4 *>(p));
 }
 
-// Feature of row or column c of feature tile u, where 64 features are cut into
-// four tiles such that a lane's rows of tiles 2 q and 2 q + 1 are the eight
-// features 32 q + 8 g .. + 7 (one 16-byte access).
-__device__ __forceinline__ int feature(int u, int c) { return 32 * (u / 2) + 8 * (c / 4) + 4 * (u % 2) + c % 4; }
-
-// Transposed fragment (contraction over tokens 32 kb .. + 31) of feature tile
-// u of a [64 tokens][stride] tile, features from `f0` on in the order above.
-__device__ __forceinline__ bf16x8 tokens_frag(const uint16_t *tile, int stride, int kb, int u, int g, int c) {
-    const uint16_t *p = tile + (32 * kb + 4 * g + c / 4) * stride + 32 * (u / 2) + 8 * (c % 4) + 4 * (u % 2);
-    return join(read_tr(p), read_tr(p + 16 * stride));
-}
-// the same of 16 adjacent features n0 .. n0 + 15
-__device__ __forceinline__ bf16x8 tokens_frag16(const uint16_t *tile, int stride, int kb, int n0, int g, int c) {
-    const uint16_t *p = tile + (32 * kb + 4 * g + c / 4) * stride + n0 + 4 * (c % 4);
+// Transposed fragment (contraction over tokens 32 kb .. + 31) of the 16
+// features f0 .. f0 + 15 of a [64 tokens][stride] tile.
+__device__ __forceinline__ bf16x8 tokens_frag(const uint16_t *tile, int stride, int kb, int f0, int g, int c) {
+    const uint16_t *p = tile + (32 * kb + 4 * g + c / 4) * stride + f0 + 4 * (c % 4);
     return join(read_tr(p), read_tr(p + 16 * stride));
 }
 
