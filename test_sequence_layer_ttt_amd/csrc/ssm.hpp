@@ -75,5 +75,10 @@ hipError_t launch_ssm_bwd_finish(const SsmBwdArgs &g, int blocks_row, int blocks
 hipError_t launch_ssm_states_valu(const SsmArgs &a, const SsmOperand *dy, float *seg, float *decay,
                                   hipStream_t stream);
 hipError_t launch_ssm_mfma(const SsmArgs &a, hipStream_t stream);
+// the segments' shares of the states and of their gradients, one launch
+hipError_t launch_ssm_shares_mfma(const SsmArgs &a, const SsmOperand &dy, float *sf, float *sr, float *decay,
+                                  hipStream_t stream);
+bool ssm_bwd_mfma_supported(const SsmBwdArgs &g);
+hipError_t launch_ssm_bwd_mfma(const SsmBwdArgs &g, hipStream_t stream);
 
 }  // namespace ttt

@@ -45,12 +45,15 @@ struct MfmaArgs {
     float *fin, *decay;
 };
 
-template <int N, bool OUT>
-__global__ __launch_bounds__(256, N == 128 ? 2 : 3) void chunks(MfmaArgs w) {
+// OUT: outputs and the state's update. Otherwise the segment's share of the
+// state alone, or (REV) of the state's gradient: a walk from the segment's end
+// over S <- exp(l_63) S + (C diag(exp(l)))^T dY, with C in Bm and dY in x.
+template <int N, bool OUT, bool REV>
+__device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
     constexpr int NS = Smem<N, OUT>::NS, KB = N / 32;
     constexpr int NT = N >= 64 ? N / 64 : 1;  // row tiles of the state in a wave
     constexpr int UT = N >= 64 ? 4 : 2;       // its feature tiles
-    __shared__ Smem<N, OUT> sm;
+    static_assert(!(OUT && REV), "outputs are made forwards");
     const SsmArgs &a = w.a;
     const int lane = threadIdx.x % 64, wv = threadIdx.x / 64, g = lane / 16, c = lane % 16;
     int bs, h;
@@ -108,20 +111,22 @@ __global__ __launch_bounds__(256, N == 128 ? 2 : 3) void chunks(MfmaArgs w) {
                 *reinterpret_cast<s16x4 *>(&sm.s[(16 * (u0 + u) + c) * NS + 16 * (nt0 + i) + 4 * g]) = pack4(st[i][u]);
     };
     float total = 0.f;
-    if (t0 < te) {
-        fetch(t0);
-        put(t0, 0);
+    const int nc = (te - t0 + Q - 1) / Q;
+    auto chunk = [&](int i) { return t0 + (REV ? nc - 1 - i : i) * Q; };
+    if (nc) {
+        fetch(chunk(0));
+        put(chunk(0), 0);
         if constexpr (OUT) share_state();
     }
-    int buf = 0;
-    for (int t = t0; t < te; t += Q, buf ^= 1) {
+    for (int ci = 0; ci < nc; ++ci) {
+        const int t = chunk(ci), buf = ci % 2;
         __syncthreads();
         if constexpr (OUT) {
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) cf[kb] = cn[kb];
         }
-        const bool more = t + Q < te;
-        if (more) fetch(t + Q);
+        const bool more = ci + 1 < nc;
+        if (more) fetch(chunk(ci + 1));
         const uint16_t *x = sm.x[buf], *bt = sm.b[buf];
         const ChunkDecay &d = sm.d[buf];
         bf16x8 xf[2][4];
@@ -208,12 +213,24 @@ __global__ __launch_bounds__(256, N == 128 ? 2 : 3) void chunks(MfmaArgs w) {
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             const int j0 = 32 * kb + 4 * g, j1 = j0 + 16;
-            f32x4 w0 = *reinterpret_cast<const f32x4 *>(&d.tail[j0]), w1 = *reinterpret_cast<const f32x4 *>(&d.tail[j1]);
-            const f32x4 p0 = *reinterpret_cast<const f32x4 *>(&d.step[j0]), p1 = *reinterpret_cast<const f32x4 *>(&d.step[j1]);
+            f32x4 w0, w1;
+            if constexpr (REV) {
+                w0 = *reinterpret_cast<const f32x4 *>(&d.hi[j0]);
+                w1 = *reinterpret_cast<const f32x4 *>(&d.hi[j1]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                w0[r] *= p0[r];
-                w1[r] *= p1[r];
+                for (int r = 0; r < 4; ++r) {
+                    w0[r] = fast_exp2(w0[r]);
+                    w1[r] = fast_exp2(w1[r]);
+                }
+            } else {
+                w0 = *reinterpret_cast<const f32x4 *>(&d.tail[j0]);
+                w1 = *reinterpret_cast<const f32x4 *>(&d.tail[j1]);
+                const f32x4 p0 = *reinterpret_cast<const f32x4 *>(&d.step[j0]), p1 = *reinterpret_cast<const f32x4 *>(&d.step[j1]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    w0[r] *= p0[r];
+                    w1[r] *= p1[r];
+                }
             }
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
@@ -226,7 +243,7 @@ __global__ __launch_bounds__(256, N == 128 ? 2 : 3) void chunks(MfmaArgs w) {
                         st[i][u] = mfma32(bw[k], N >= 64 || wv < 2 ? xf[kb][u] : xf[kb][2 + u % 2], st[i][u]);
             }
         }
-        if (more) put(t + Q, buf ^ 1);
+        if (more) put(chunk(ci + 1), buf ^ 1);
         if constexpr (OUT) {
             if (more) {
                 __syncthreads();  // every wave has read the state's copy
@@ -250,15 +267,33 @@ __global__ __launch_bounds__(256, N == 128 ? 2 : 3) void chunks(MfmaArgs w) {
     if (!OUT && threadIdx.x == 0) w.decay[static_cast<int64_t>(bh) * a.nseg + seg] = exp2f(total);
 }
 
-template <bool OUT> hipError_t run(const MfmaArgs &w, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(w.a.B) * w.a.H * w.a.nseg);
-    if (w.a.N == 32)
-        hipLaunchKernelGGL((chunks<32, OUT>), grid, dim3(256), 0, s, w);
-    else if (w.a.N == 64)
-        hipLaunchKernelGGL((chunks<64, OUT>), grid, dim3(256), 0, s, w);
+template <int N>
+__global__ __launch_bounds__(256, N == 128 ? 2 : 3) void outputs(MfmaArgs w) {
+    __shared__ Smem<N, true> sm;
+    chunks<N, true, false>(w, sm);
+}
+// blockIdx.y: the states' shares, then those of their gradients
+template <int N>
+__global__ __launch_bounds__(256, N == 128 ? 2 : 3) void shares(MfmaArgs f, MfmaArgs r) {
+    __shared__ Smem<N, false> sm;
+    if (blockIdx.y == 0)
+        chunks<N, false, false>(f, sm);
     else
-        hipLaunchKernelGGL((chunks<128, OUT>), grid, dim3(256), 0, s, w);
+        chunks<N, false, true>(r, sm);
+}
+
+template <int N> hipError_t run(const MfmaArgs *out, const MfmaArgs *f, const MfmaArgs *r, hipStream_t s) {
+    const SsmArgs &a = out ? out->a : f->a;
+    const unsigned blocks = static_cast<unsigned>(a.B) * a.H * a.nseg;
+    if (out)
+        hipLaunchKernelGGL((outputs<N>), dim3(blocks), dim3(256), 0, s, *out);
+    else
+        hipLaunchKernelGGL((shares<N>), dim3(blocks, r ? 2 : 1), dim3(256), 0, s, *f, r ? *r : *f);
     return hipGetLastError();
+}
+hipError_t run(const MfmaArgs *out, const MfmaArgs *f, const MfmaArgs *r, hipStream_t s) {
+    const int N = out ? out->a.N : f->a.N;
+    return N == 32 ? run<32>(out, f, r, s) : N == 64 ? run<64>(out, f, r, s) : run<128>(out, f, r, s);
 }
 
 bool wide(const SsmOperand &o) {  // rows of 16-byte accesses
@@ -272,6 +307,14 @@ bool ssm_mfma_supported(const SsmArgs &a) {
            wide(a.Cm) && wide(a.y);
 }
 
+hipError_t launch_ssm_shares_mfma(const SsmArgs &a, const SsmOperand &dy, float *sf, float *sr, float *decay,
+                                  hipStream_t stream) {
+    MfmaArgs f{a, nullptr, 0, sf, decay}, r{a, nullptr, 0, sr, decay};
+    r.a.x = dy;
+    r.a.Bm = a.Cm;
+    return run(nullptr, &f, &r, stream);
+}
+
 hipError_t launch_ssm_mfma(const SsmArgs &a, hipStream_t stream) {
     const int64_t NP = static_cast<int64_t>(a.N) * a.P;
     MfmaArgs w{a, a.state, 0, a.state_out, nullptr};
@@ -279,7 +322,7 @@ hipError_t launch_ssm_mfma(const SsmArgs &a, hipStream_t stream) {
         float *seg = a.ws, *decay = a.ws + static_cast<int64_t>(a.B) * a.H * a.nseg * NP;
         MfmaArgs p{a, nullptr, 0, seg, decay};
         hipError_t e;
-        if ((e = run<false>(p, stream)) != hipSuccess) return e;
+        if ((e = run(nullptr, &p, nullptr, stream)) != hipSuccess) return e;
         if ((e = launch_ssm_carry(a.B * a.H, static_cast<int>(NP), a.nseg, false, a.state, decay, seg, a.state_out,
                                   stream)) != hipSuccess)
             return e;
@@ -287,7 +330,7 @@ hipError_t launch_ssm_mfma(const SsmArgs &a, hipStream_t stream) {
         w.init_stride = NP;
         w.fin = nullptr;
     }
-    return run<true>(w, stream);
+    return run(&w, nullptr, nullptr, stream);
 }
 
 }  // namespace ttt

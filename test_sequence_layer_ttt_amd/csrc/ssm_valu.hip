@@ -384,6 +384,7 @@ hipError_t launch_ssm_backward(const SsmBwdArgs &g, hipStream_t stream) {
     const SsmBwdWs s = ssm_backward_ws(a);
     hipError_t e;
     if (!a.B) return launch_ssm_bwd_finish(g, 0, 0, stream);  // the sums over no tokens
+    if (ssm_bwd_mfma_supported(g)) return launch_ssm_bwd_mfma(g, stream);
     if ((e = launch_ssm_states_valu(a, nullptr, s.sf, s.decay, stream)) != hipSuccess) return e;
     if ((e = launch_ssm_carry(a.B * a.H, static_cast<int>(NP), a.nseg, false, a.state, s.decay, s.sf, s.last,
                               stream)) != hipSuccess)
