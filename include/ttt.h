@@ -545,8 +545,8 @@ int ttt_conv_backward_workspace(int B, int L, int C, int K, size_t *bytes);
  *     D_t = log(1 + exp(dt_t + dt_bias)),  a_t = exp(D_t A)
  *     state <- a_t state + B_t (D_t x_t)^T,   y_t = C_t state + D x_t
  * with B and C shared by the H / G heads of a group.
- *   1 <= P, N <= TTT_SSM_MAX_DIM; H a positive multiple of G; B*H and the
- *   number of segments B*H*ceil(L/256) at most TTT_SSM_MAX_HEADS.
+ *   1 <= P, N <= TTT_SSM_MAX_DIM; H a positive multiple of G; B*H and
+ *   B*H*ceil(L/64) at most TTT_SSM_MAX_HEADS.
  *   x, y  : [B,L,H,P] io, strided (batch, token, head).
  *   dt    : [B,L,H] io, strided (batch, token, head).
  *   A     : [H] fp32 (decays where negative); D, dt_bias : [H] fp32 or NULL (0).

@@ -387,10 +387,9 @@ int ssm_common(int B, int L, int H, int P, int G, int N, int io) {
 }
 
 // a grid's workgroups and its threads (up to 512 a workgroup) are counted in 32 bits
-int ssm_plan(int B, int L, int H, int P, int N, bool backward, int *nseg, int *seglen) {
-    ttt::ssm_segments(B, L, H, P, N, false, backward, nseg, seglen);
-    if (static_cast<int64_t>(B) * H * *nseg > TTT_SSM_MAX_HEADS)
-        return fail(TTT_E_SHAPE, "B*H*L is too large (B = %d, H = %d, L = %d)", B, H, L);
+int ssm_plan(int B, int L, int H, int P, int N) {
+    if (static_cast<int64_t>(B) * H * ((static_cast<int64_t>(L) + 63) / 64) > TTT_SSM_MAX_HEADS)
+        return fail(TTT_E_SHAPE, "B*H*ceil(L/64) exceeds %d (B = %d, H = %d, L = %d)", TTT_SSM_MAX_HEADS, B, H, L);
     return TTT_OK;
 }
 
@@ -413,8 +412,9 @@ extern "C" {
 
 int ttt_ssm_forward_workspace(int B, int L, int H, int P, int G, int N, size_t *bytes) {
     int st, nseg, seglen;
-    if ((st = ssm_common(B, L, H, P, G, N, TTT_F32)) || (st = ssm_plan(B, L, H, P, N, false, &nseg, &seglen))) return st;
+    if ((st = ssm_common(B, L, H, P, G, N, TTT_F32)) || (st = ssm_plan(B, L, H, P, N))) return st;
     if (!bytes) return fail(TTT_E_NULL, "bytes is NULL");
+    ttt::ssm_segments(B, L, H, P, N, false, false, &nseg, &seglen);
     *bytes = ttt::ssm_forward_floats(B, H, P, N, nseg) * sizeof(float);
     return ok();
 }
@@ -426,9 +426,9 @@ int ttt_ssm_forward(int B, int L, int H, int P, int G, int N, int io, const void
                     float *state_out, void *workspace, size_t workspace_bytes, hipStream_t stream) {
     int st, nseg, seglen;
     size_t need;
-    if ((st = ssm_common(B, L, H, P, G, N, io)) || (st = ssm_plan(B, L, H, P, N, false, &nseg, &seglen)) ||
-        (st = ttt_ssm_forward_workspace(B, L, H, P, G, N, &need)))
+    if ((st = ssm_common(B, L, H, P, G, N, io)) || (st = ttt_ssm_forward_workspace(B, L, H, P, G, N, &need)))
         return st;
+    ttt::ssm_segments(B, L, H, P, N, false, false, &nseg, &seglen);
     const unsigned es = esize(io);
     const View vx = view(x, "x", B, L, H, P, x_strides, 3, es), vt = view(dt, "dt", B, L, H, 1, dt_strides, 3, es),
                vb = view(Bm, "B", B, L, G, N, B_strides, 3, es), vc = view(Cm, "C", B, L, G, N, C_strides, 3, es),
@@ -477,8 +477,10 @@ int ttt_ssm_step(int B, int H, int P, int G, int N, int io, const void *x, const
 
 int ttt_ssm_backward_workspace(int B, int L, int H, int P, int G, int N, size_t *bytes) {
     int st, nseg, seglen;
-    if ((st = ssm_common(B, L, H, P, G, N, TTT_F32)) || (st = ssm_plan(B, L, H, P, N, true, &nseg, &seglen))) return st;
+    if ((st = ssm_common(B, L, H, P, G, N, TTT_F32)) || (st = ssm_plan(B, L, H, P, N))) return st;
     if (!bytes) return fail(TTT_E_NULL, "bytes is NULL");
+    // the walks' segments, which are the shorter: the call takes them or the sweeps'
+    ttt::ssm_segments(B, L, H, P, N, false, true, &nseg, &seglen);
     *bytes = ttt::ssm_backward_floats(B, L, H, P, N, nseg) * sizeof(float);
     return ok();
 }
@@ -491,10 +493,9 @@ int ttt_ssm_backward(int B, int L, int H, int P, int G, int N, int io, const voi
                      void *ddt, const int64_t *ddt_strides, float *dA, void *dB, const int64_t *dB_strides, void *dC,
                      const int64_t *dC_strides, float *dD, float *ddt_bias, float *dstate, void *workspace,
                      size_t workspace_bytes, hipStream_t stream) {
-    int st, nseg, seglen;
+    int st;
     size_t need;
-    if ((st = ssm_common(B, L, H, P, G, N, io)) || (st = ssm_plan(B, L, H, P, N, true, &nseg, &seglen)) ||
-        (st = ttt_ssm_backward_workspace(B, L, H, P, G, N, &need)))
+    if ((st = ssm_common(B, L, H, P, G, N, io)) || (st = ttt_ssm_backward_workspace(B, L, H, P, G, N, &need)))
         return st;
     const int64_t sn = static_cast<int64_t>(B) * H * N * P;
     if ((dD != nullptr) != (D != nullptr)) return fail(TTT_E_NULL, "dD is given exactly when D is");
@@ -521,9 +522,10 @@ int ttt_ssm_backward(int B, int L, int H, int P, int G, int N, int io, const voi
     if (workspace_bytes < need) return fail(TTT_E_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     if ((st = v.add_out(flat(workspace, "workspace", static_cast<int64_t>(need / 4), 4))) || (st = v.alias())) return st;
     ttt::SsmBwdArgs g{{B, L, H, P, G, N, io, operand(vx), operand(vt), operand(vb), operand(vc), A, D, dt_bias,
-                       state, lens, {nullptr, 0, 0, 0}, nullptr, static_cast<float *>(workspace), nseg, seglen},
+                       state, lens, {nullptr, 0, 0, 0}, nullptr, static_cast<float *>(workspace), 1, 64},
                       operand(vdy), dstate_out, operand(vdx), operand(vdt), operand(vdb), operand(vdc), dA, dD,
                       ddt_bias, dstate};
+    ttt::ssm_segments(B, L, H, P, N, ttt::ssm_bwd_mfma_supported(g), true, &g.f.nseg, &g.f.seglen);
     return launched(ttt::launch_ssm_backward(g, stream));
 }
 

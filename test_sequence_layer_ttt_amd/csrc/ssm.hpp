@@ -58,19 +58,24 @@ hipError_t launch_ssm_backward(const SsmBwdArgs &a, hipStream_t stream);
 hipError_t launch_ssm_carry(int BH, int NP, int nseg, bool reverse, const float *first, const float *decay,
                             float *seg, float *out, hipStream_t stream);
 
-// What the backward's second half needs: per-token sums over a head's
-// features (pb blocks of them), see ssm_bwd.hip.
+// What the backward's second half needs (ssm_bwd.hip).
 struct SsmBwdWs {
-    float *sf, *sr;          // [B,H,nseg,N,P] states before, gradients behind each segment
-    float *last;             // [B,H,N,P] state after the last segment
-    float *decay;            // [B,H,nseg]
-    float *dBh, *dCh;        // [B,H,L,N] per head
-    float *row, *col, *xdu, *dyx;  // [2,B,H,L] partial sums (two blocks of features)
-    float *part;             // [B*nseg][3][H]
-    size_t floats;           // of all of them
+    float *sf, *sr;   // [B,H,nseg,N,P] states before, gradients behind each segment
+    float *last;      // [B,H,N,P] state after the last segment
+    float *decay;     // [B,H,nseg]
+    float *dBh, *dCh; // [B,H,L,N] per head
+    // [2,B,H,L] per token. From the walks: two blocks of features' shares of
+    // the strict products. From the sweeps: the part within the 64-token
+    // chunk, then the part through the state before (behind) it.
+    float *row, *col;
+    float *xdu, *dyx;  // [2,B,H,L] x . du and dy . x, by blocks of features (sweeps: the first)
+    float *tiles;      // [B,H,ceil(L/64),8] sweeps: sums over pairs of 16-token tiles (i, j),
+                       // (1,0) (2,0) (3,0) (2,1) (3,1) (3,2)
+    float *part;       // [B*nseg][3][H]
+    size_t floats;     // of all of them
 };
 SsmBwdWs ssm_backward_ws(const SsmArgs &a);
-hipError_t launch_ssm_bwd_finish(const SsmBwdArgs &g, int blocks_row, int blocks_col, hipStream_t stream);
+hipError_t launch_ssm_bwd_finish(const SsmBwdArgs &g, bool sweeps, hipStream_t stream);
 
 hipError_t launch_ssm_states_valu(const SsmArgs &a, const SsmOperand *dy, float *seg, float *decay,
                                   hipStream_t stream);

@@ -1,12 +1,21 @@
 // The state space scan's backward, last part. The gradient of the log-decay
-// l_t = D_t A of a token is q_t = <g_t, a_t h_{t-1}>, and from the two
-// recurrences
-//     q_t = q_{t+1} + dy_t . C_t (a_t h_{t-1}) - u_t . B_t (a_{t+1} g_{t+1}),
-// so it is a running sum, from each segment's end backwards, of two per-token
-// products that the walks have (row and col: both without the token's own
-// term, which is in both and would only cancel), starting from the product of
-// the state and its gradient at the segment's end. Sums run in 64 bits within
-// a segment of at most 256 tokens. Then
+// D_t A of a token is q_t = <g_t, a_t h_{t-1}>: of everything that passes from
+// the tokens before t to those from t on. With dy . (strict read of h) = row
+// and u . (strict read of g) = col, both without the token's own term,
+//     q_t = q_{t+1} + row_t - col_t,
+// a running sum from the segment's end, where q is the product of the state
+// and its gradient. Rounding errors in such a sum never leave it again, while
+// what q_t measures decays; so it starts anew as often as can be.
+//  * Walks: a segment has 64 tokens.
+//  * Sweeps, in 64-token chunks: with re and co the parts that pass through the
+//    state before and behind the chunk, and W (row_i = sum_j W_ij, col_j =
+//    sum_i W_ij) what passes within it,
+//        q_t = base + sum_{j < t} co_j + sum_{i >= t} re_i + sum_{i >= t > j} W_ij,
+//    where base passes the whole chunk: q at its end less all of co, and
+//    taken as 0 where the chunk's decay is below 2^-24 and that difference is
+//    nothing but rounding. The last sum is known at the borders of the
+//    16-token tiles from the tiles' sums and runs within a tile.
+// All in 64 bits. Then
 //     ddt_t = (A q_t + x_t . du_t) sigma(dt_t + dt_bias),
 //     dA = sum D_t q_t,  dD = sum dy_t . x_t,  ddt_bias = sum ddt_t,
 // and dB, dC are summed over the heads of a group.
@@ -22,7 +31,6 @@ constexpr int NT = 256;
 struct FinishArgs {
     SsmBwdArgs g;
     SsmBwdWs w;
-    int brow, bcol;
 };
 
 __device__ __forceinline__ double block_sum(double v, double (&red)[NT / 64]) {
@@ -34,10 +42,31 @@ __device__ __forceinline__ double block_sum(double v, double (&red)[NT / 64]) {
     return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-template <typename TIO>
+// sums over the lanes below (above) this one and it, in groups of W lanes
+template <int W> __device__ __forceinline__ double sum_before(double v) {
+    const int lane = threadIdx.x % W;
+#pragma unroll
+    for (int m = 1; m < W; m *= 2) {
+        const double o = __shfl_up(v, m, W);
+        if (lane >= m) v += o;
+    }
+    return v;
+}
+template <int W> __device__ __forceinline__ double sum_behind(double v) {
+    const int lane = threadIdx.x % W;
+#pragma unroll
+    for (int m = 1; m < W; m *= 2) {
+        const double o = __shfl_down(v, m, W);
+        if (lane + m < W) v += o;
+    }
+    return v;
+}
+
+// A workgroup takes a segment, a thread a token, a wave a 64-token chunk.
+template <typename TIO, bool SWEEPS>
 __global__ __launch_bounds__(NT) void decay_gradient(FinishArgs f) {
     const SsmArgs &a = f.g.f;
-    __shared__ double red[NT / 64], scan[2][NT];
+    __shared__ double red[NT / 64], all_re[NT / 64], all_co[NT / 64], all_l[NT / 64];
     const int seg = blockIdx.x % a.nseg, bh = blockIdx.x / a.nseg, b = bh / a.H, h = bh % a.H;
     const int64_t NP = static_cast<int64_t>(a.N) * a.P;
     const int n = a.lens ? max(0, min(a.lens[b], a.L)) : a.L;
@@ -49,35 +78,68 @@ __global__ __launch_bounds__(NT) void decay_gradient(FinishArgs f) {
     double e = 0.0;
     for (int64_t i = threadIdx.x; i < NP; i += NT) e += static_cast<double>(se[i]) * ge[i];
     e = block_sum(e, red);
-    // sum over the tokens from this one to the segment's end
     const int64_t tok = static_cast<int64_t>(bh) * a.L + t, blk = static_cast<int64_t>(a.B) * a.H * a.L;
-    double v = 0.0, xdu = 0.0, dyx = 0.0;
+    double xdu = 0.0, dyx = 0.0, z = 0.0, step = 0.0, q;
     if (live) {
-        for (int i = 0; i < f.brow; ++i) v += f.w.row[i * blk + tok];
-        for (int i = 0; i < f.bcol; ++i) {
-            v -= f.w.col[i * blk + tok];
-            xdu += f.w.xdu[i * blk + tok];
-            dyx += f.w.dyx[i * blk + tok];
+        z = static_cast<double>(io_traits<TIO>::load(static_cast<const TIO *>(a.dt.p), b * a.dt.sb + t * a.dt.st + h * a.dt.sh)) +
+            (a.dt_bias ? a.dt_bias[h] : 0.f);
+        step = softplus_f(static_cast<float>(z));
+    }
+    if constexpr (SWEEPS) {
+        double w = 0.0, re = 0.0, co = 0.0;
+        if (live) {
+            w = static_cast<double>(f.w.row[tok]) - f.w.col[tok];
+            re = f.w.row[blk + tok];
+            co = f.w.col[blk + tok];
+            xdu = f.w.xdu[tok];
+            dyx = f.w.dyx[tok];
         }
-    }
-    int from = 0;
-    scan[0][threadIdx.x] = v;
-    __syncthreads();
+        const int wv = threadIdx.x / 64, lane = threadIdx.x % 64;
+        const double re_behind = sum_behind<64>(re), co_here = sum_before<64>(co), co_before = co_here - co;
+        const double l = sum_before<64>(step * a.A[h]);
+        double within = sum_behind<16>(w);
+        if (mine && lane < 48) {  // what passes the end of this token's tile
+            const float *p = f.w.tiles + (static_cast<int64_t>(bh) * ((a.L + 63) / 64) + t / 64) * 8;
+            const int tile = lane / 16;
+            // the pairs (i, j) with j <= tile < i; those of a tile that has no tokens were never
+            // made, so only what the sequence holds is read
+            const int held = static_cast<int>((n - (t - lane) + 15) / 16);  // tiles with tokens
+            const int place[3][3] = {{0, 1, 2}, {-1, 3, 4}, {-1, -1, 5}};   // [j][i - 1]
 #pragma unroll
-    for (int m = 1; m < NT; m *= 2) {
-        double s = scan[from][threadIdx.x];
-        if (threadIdx.x + m < NT) s += scan[from][threadIdx.x + m];
-        scan[from ^ 1][threadIdx.x] = s;
-        from ^= 1;
+            for (int j = 0; j < 3; ++j)
+#pragma unroll
+                for (int i = 1; i < 4; ++i)
+                    if (j <= tile && i > tile && i > j && i < held) within += p[place[j][i - 1]];
+        }
+        if (lane == 0) all_re[wv] = re_behind;
+        if (lane == 63) {
+            all_co[wv] = co_here;
+            all_l[wv] = l;
+        }
         __syncthreads();
+        double base = 0.0;
+        for (int k = NT / 64 - 1; k >= wv; --k) {  // e: q behind chunk k
+            if (static_cast<int64_t>(seg) * a.seglen + 64 * k >= min(n, a.L) || 64 * k >= a.seglen) continue;
+            base = all_l[k] < -24.0 * 0.6931471805599453 ? 0.0 : e - all_co[k];
+            e = base + all_re[k];
+        }
+        q = base + co_before + re_behind + within;
+    } else {
+        double w = 0.0;
+        if (live) {
+            for (int i = 0; i < (a.N + 63) / 64; ++i) w += f.w.row[i * blk + tok];
+            for (int i = 0; i < (a.P + 63) / 64; ++i) {
+                w -= f.w.col[i * blk + tok];
+                xdu += f.w.xdu[i * blk + tok];
+                dyx += f.w.dyx[i * blk + tok];
+            }
+        }
+        q = sum_behind<64>(w) + e;  // a segment of 64 tokens: the first wave's
     }
-    const double q = scan[from][threadIdx.x] + e;
     double dz = 0.0, dA = 0.0;
     if (live) {
-        const float z = io_traits<TIO>::load(static_cast<const TIO *>(a.dt.p), b * a.dt.sb + t * a.dt.st + h * a.dt.sh) +
-                        (a.dt_bias ? a.dt_bias[h] : 0.f);
-        dA = q * softplus_f(z);
-        dz = (a.A[h] * q + xdu) / (1.0 + exp(-static_cast<double>(z)));
+        dA = q * step;
+        dz = (a.A[h] * q + xdu) / (1.0 + exp(-z));
     }
     if (mine)
         io_traits<TIO>::store(static_cast<TIO *>(const_cast<void *>(f.g.ddt.p)),
@@ -113,12 +175,16 @@ __global__ __launch_bounds__(NT) void head_sums(FinishArgs f) {
     }
 }
 
-template <typename TIO> hipError_t finish(const FinishArgs &f, hipStream_t s) {
+template <typename TIO> hipError_t finish(const FinishArgs &f, bool sweeps, hipStream_t s) {
     const SsmArgs &a = f.g.f;
     const int64_t heads = static_cast<int64_t>(a.B) * a.H;
     hipError_t e = hipSuccess;
     if (heads) {
-        hipLaunchKernelGGL((decay_gradient<TIO>), dim3(static_cast<unsigned>(heads * a.nseg)), dim3(NT), 0, s, f);
+        const dim3 grid(static_cast<unsigned>(heads * a.nseg));
+        if (sweeps)
+            hipLaunchKernelGGL((decay_gradient<TIO, true>), grid, dim3(NT), 0, s, f);
+        else
+            hipLaunchKernelGGL((decay_gradient<TIO, false>), grid, dim3(NT), 0, s, f);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const int64_t n = static_cast<int64_t>(a.B) * a.G * a.L * a.N;
@@ -156,6 +222,7 @@ SsmBwdWs ssm_backward_ws(const SsmArgs &a) {
     w.col = take(2 * BH * a.L);
     w.xdu = take(2 * BH * a.L);
     w.dyx = take(2 * BH * a.L);
+    w.tiles = take(BH * ((static_cast<int64_t>(a.L) + 63) / 64) * 8);
     w.part = take(static_cast<int64_t>(a.B) * a.nseg * 3 * a.H);
     return w;
 }
@@ -172,10 +239,9 @@ size_t ssm_forward_floats(int B, int H, int P, int N, int nseg) {
 
 void ssm_segments(int B, int L, int H, int P, int N, bool mfma, bool backward, int *nseg, int *seglen) {
     (void)P;
-    (void)mfma;
     // as many workgroups as run at once (three a compute unit, two where N
     // takes more of its LDS and registers), segments of whole 64-token chunks;
-    // the backward's running sums over a segment hold at most 256 tokens
+    // the backward's sums over a segment hold 256 tokens, 64 after the walks
     const int64_t slots = N > 64 ? 512 : 768;
     const int64_t heads = static_cast<int64_t>(B) * H;
     const int64_t chunks = (static_cast<int64_t>(L) + 63) / 64;
@@ -183,15 +249,15 @@ void ssm_segments(int B, int L, int H, int P, int N, bool mfma, bool backward, i
     if (want > chunks) want = chunks;
     if (want < 1) want = 1;
     int64_t per = (chunks + want - 1) / want;
-    if (backward && per > 4) per = 4;
+    if (backward && per > (mfma ? 4 : 1)) per = mfma ? 4 : 1;
     if (per < 1) per = 1;
     *seglen = static_cast<int>(per * 64);
     *nseg = static_cast<int>(chunks > 0 ? (chunks + per - 1) / per : 1);
 }
 
-hipError_t launch_ssm_bwd_finish(const SsmBwdArgs &g, int blocks_row, int blocks_col, hipStream_t stream) {
-    const FinishArgs f{g, ssm_backward_ws(g.f), blocks_row, blocks_col};
-    return g.f.io == 1 ? finish<bf16_t>(f, stream) : finish<float>(f, stream);
+hipError_t launch_ssm_bwd_finish(const SsmBwdArgs &g, bool sweeps, hipStream_t stream) {
+    const FinishArgs f{g, ssm_backward_ws(g.f)};
+    return g.f.io == 1 ? finish<bf16_t>(f, sweeps, stream) : finish<float>(f, sweeps, stream);
 }
 
 }  // namespace ttt

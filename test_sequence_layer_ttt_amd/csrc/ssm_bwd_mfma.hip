@@ -5,9 +5,10 @@
 //     dC_i = sum_{j <= i} P_ij E_ij D_j B_j + exp(l_i) S dy_i
 //     dB_j = D_j (sum_{i >= j} P_ij E_ij C_i + exp(l_63 - l_j) R x_j)
 //     dx_j = D_j (sum_{i >= j} P_ij G_ij dy_i + exp(l_63 - l_j) B_j R) + D dy_j
-// and the two per-token products of the decay's gradient (ssm_bwd.hip)
-//     row_i = sum_{j < i} P_ij G_ij E_ij D_j + exp(l_i) C_i . (S dy_i)
-//     col_j = D_j (sum_{i > j} P_ij G_ij E_ij + exp(l_63 - l_j) B_j . (R x_j)).
+// and what the decay's gradient is made of (ssm_bwd.hip), W_ij = P_ij G_ij E_ij D_j,
+//     row_i = sum_{j < i} W_ij,   re_i = exp(l_i) C_i . (S dy_i)
+//     col_j = sum_{i > j} W_ij,   co_j = D_j exp(l_63 - l_j) B_j . (R x_j)
+// with the sums of W over the six pairs of different 16-token tiles.
 //
 // Two sweeps with one shape: forwards with S (own token i; rows X, B in LDS)
 // and backwards with R (own token j; rows dY, C in LDS). A wave makes the
@@ -37,6 +38,9 @@ template <int N> struct BwdSmem {
     uint16_t s[3][64 * NS];     // the state's (gradient's) three parts, [feature][n]
     ChunkDecay d[2];
 };
+
+// place of the sum over rows of tile i and columns of tile j < i (see ssm.hpp)
+__device__ __forceinline__ int pair_index(int i, int j) { return j == 0 ? i - 1 : j + i; }
 
 struct SweepArgs {
     SsmBwdArgs g;
@@ -82,7 +86,8 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
     const bf16_t *dp = static_cast<const bf16_t *>(a.dt.p) + b * a.dt.sb + h * a.dt.sh;
     bf16_t *dxp = static_cast<bf16_t *>(const_cast<void *>(ga.dx.p)) + b * ga.dx.sb + h * ga.dx.sh;
     float *ph = (REV ? w.w.dBh : w.w.dCh) + static_cast<int64_t>(bh) * a.L * N;
-    const int64_t tok0 = static_cast<int64_t>(bh) * a.L;
+    const int64_t tok0 = static_cast<int64_t>(bh) * a.L, inter = static_cast<int64_t>(a.B) * a.H * a.L;
+    const int64_t tiles0 = static_cast<int64_t>(bh) * ((a.L + Q - 1) / Q);
     const int nt0 = N >= 64 ? NT * wv : wv % 2, u0 = N >= 64 ? 0 : 2 * (wv / 2);
     constexpr int64_t NP = static_cast<int64_t>(N) * 64;
 
@@ -152,7 +157,7 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
         const float reach = REV ? d.tail[o] : fast_exp2(hi);  // decay between the token and the state
         // products with the tokens before (behind) this lane's: rows m = 4 g + r
         bf16x8 me[2], mg[2];
-        float strict = 0.f, diag = 0.f;
+        float strict = 0.f, diag = 0.f, apart[4] = {};
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             f32x4 pe[2], pg[2];
@@ -177,8 +182,12 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
                         const bool in = REV ? m + r >= o : m + r <= o, same = m + r == o;
                         const float e = in ? E[r] * p : 0.f;
                         const float ge = in ? G[r] * e : 0.f;
-                        strict += same ? 0.f : ge;
-                        diag += same ? ge : 0.f;
+                        if (mt == wv) {
+                            strict += same ? 0.f : ge;
+                            diag += same ? ge : 0.f;
+                        } else {
+                            apart[mt] += ge;
+                        }
                         E[r] = e;
                         G[r] = in ? G[r] * p : 0.f;
                     }
@@ -188,6 +197,15 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
             }
             me[kb] = pack8(pe[0], pe[1]);
             if constexpr (REV) mg[kb] = pack8(pg[0], pg[1]);
+        }
+        // a column's (row's) sum over the tiles, and the tiles' sums over the wave
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+            strict += apart[mt];
+            if (REV && mt > wv) {
+                const float s = rows4_sum(row16_sum(apart[mt] * step));
+                if (lane == 0) w.w.tiles[(tiles0 + t / Q) * 8 + pair_index(mt, wv)] = s;
+            }
         }
         // over n: the state times z, its product with q, and the tokens' part
         float qs = 0.f;
@@ -247,16 +265,19 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
             }
             yx = rows4_sum(yx);
         }
-        strict = rows4_sum(fmaf(reach, qs, strict));
+        strict = rows4_sum(strict);
         diag = rows4_sum(diag);
+        qs = reach * rows4_sum(qs);
         if (live && g == 0) {
             const int64_t tok = tok0 + t + o;
             if constexpr (REV) {
                 w.w.col[tok] = step * strict;
-                w.w.xdu[tok] = strict + diag;
+                w.w.col[inter + tok] = step * qs;
+                w.w.xdu[tok] = strict + diag + qs;
                 w.w.dyx[tok] = yx;
             } else {
                 w.w.row[tok] = strict;
+                w.w.row[inter + tok] = qs;
             }
         }
         if (more) {  // the state before the next chunk
@@ -300,15 +321,6 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
 #pragma unroll
         for (int i = 0; i < N / 8; ++i) ph[static_cast<int64_t>(t) * N + e * (N / 8) + i] = 0.f;
         if constexpr (REV) *reinterpret_cast<uint4 *>(dxp + static_cast<int64_t>(t) * ga.dx.st + 8 * e) = make_uint4(0, 0, 0, 0);
-        if (e == 0) {
-            if constexpr (REV) {
-                w.w.col[tok0 + t] = 0.f;
-                w.w.xdu[tok0 + t] = 0.f;
-                w.w.dyx[tok0 + t] = 0.f;
-            } else {
-                w.w.row[tok0 + t] = 0.f;
-            }
-        }
     }
 }
 
@@ -351,7 +363,7 @@ hipError_t launch_ssm_bwd_mfma(const SsmBwdArgs &g, hipStream_t stream) {
     else
         hipLaunchKernelGGL((sweeps<128>), grid, dim3(256), 0, stream, w);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    return launch_ssm_bwd_finish(g, 1, 1, stream);
+    return launch_ssm_bwd_finish(g, true, stream);
 }
 
 }  // namespace ttt

@@ -194,19 +194,12 @@ __global__ __launch_bounds__(512) void walk(WalkArgs w) {
     if (OUT) {
         for (int t = te + wv; t < t1; t += nw) {
             const int64_t tok = static_cast<int64_t>(bh) * a.L + t;
-            const int64_t blk = static_cast<int64_t>(vb) * a.B * a.H * a.L + tok;
             const SsmOperand &o = MODE == OUT_Y ? a.y : w.dx;
             if (vi < VD) {
                 if (MODE == OUT_Y || MODE == OUT_DU)
                     io_traits<TIO>::store(static_cast<TIO *>(const_cast<void *>(o.p)), b * o.sb + t * o.st + h * o.sh + vi, 0.f);
                 else
                     w.per_head[tok * a.N + vi] = 0.f;
-            }
-            if (lane == 0 && MODE == OUT_DC) w.row[blk] = 0.f;
-            if (lane == 0 && MODE == OUT_DU) {
-                w.col[blk] = 0.f;
-                w.xdu[blk] = 0.f;
-                w.dyx[blk] = 0.f;
             }
         }
     }
@@ -383,7 +376,7 @@ hipError_t launch_ssm_backward(const SsmBwdArgs &g, hipStream_t stream) {
     const int64_t NP = static_cast<int64_t>(a.N) * a.P;
     const SsmBwdWs s = ssm_backward_ws(a);
     hipError_t e;
-    if (!a.B) return launch_ssm_bwd_finish(g, 0, 0, stream);  // the sums over no tokens
+    if (!a.B) return launch_ssm_bwd_finish(g, false, stream);  // the sums over no tokens
     if (ssm_bwd_mfma_supported(g)) return launch_ssm_bwd_mfma(g, stream);
     if ((e = launch_ssm_states_valu(a, nullptr, s.sf, s.decay, stream)) != hipSuccess) return e;
     if ((e = launch_ssm_carry(a.B * a.H, static_cast<int>(NP), a.nseg, false, a.state, s.decay, s.sf, s.last,
@@ -409,7 +402,7 @@ hipError_t launch_ssm_backward(const SsmBwdArgs &g, hipStream_t stream) {
     if ((e = run_walk<OUT_DU>(w, stream)) != hipSuccess) return e;
     w.per_head = s.dBh;
     if ((e = run_walk<OUT_DB>(w, stream)) != hipSuccess) return e;
-    return launch_ssm_bwd_finish(g, (a.N + 63) / 64, (a.P + 63) / 64, stream);
+    return launch_ssm_bwd_finish(g, false, stream);
 }
 
 }  // namespace ttt
