@@ -10,6 +10,7 @@ and the call runs on the operands' device, whichever device is current. A
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -22,29 +23,32 @@ _ACT = {"none": _lib.TTT_ACT_NONE, "sigmoid": _lib.TTT_ACT_SIGMOID, "silu": _lib
 _S1, _S2, _S3 = (ctypes.c_int64 * n for n in (1, 2, 3))
 
 
-def _io(t, name: str) -> int:
+def _io(t, name: str):
+    """(storage type, device number) of an operand that sets both."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     io = _IO.get(t.dtype)
     if io is None:
         raise TypeError(f"{name} dtype {t.dtype} not supported")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor (got {t.device})")
-    return io
+    return io, t.get_device()
 
 
-def _check(t, name: str, shape, dtype, device, contiguous: bool = True) -> None:
+def _check(t, name: str, shape, dtype, index: int, contiguous: bool = True) -> None:
+    """`index`: the device's number (a tensor's own is quicker to ask than its device)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and (not contiguous or t.is_contiguous())):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if contiguous:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows(t, name: str, kind, skip: int = 1):
@@ -62,49 +66,75 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr() or None
 
 
-def _call(fn, device, stream, *args) -> None:
-    """The entry point on `device` and its current stream, or on `stream`."""
+def _call(fn, index: int, stream, *args) -> None:
+    """The entry point on device `index` and its current stream, or on `stream`."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif isinstance(stream, torch.cuda.Stream) and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the operands on {device}")
-    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if device.index == torch.cuda.current_device():
-        _lib.check(fn(*args, raw))
-        return
-    with torch.cuda.device(device):
-        _lib.check(fn(*args, raw))
+        raw = _raw_stream(index)
+    else:
+        if isinstance(stream, torch.cuda.Stream) and stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, the operands on cuda:{index}")
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index == _current_device():
+        code = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, raw)
+    if code:
+        _lib.check(code)
 
 
-def _lens(lens, B, device):
-    if lens is not None:
-        _check(lens, "lens", (B,), torch.int32, device)
+# The handle of a device's current stream and the current device's number,
+# without the objects that torch.cuda's functions make of them (2.5 us a call);
+# a tensor on the device exists, so it is initialised.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _lens(lens, B, index: int):
+    if lens is None:
+        return None
+    _check(lens, "lens", (B,), torch.int32, index)
     return _ptr(lens)
 
 
-def _workspace(workspace, need: int, device):
+def _workspace(workspace, need: int, index: int):
     if workspace is None:
-        workspace = torch.empty(max(need, 16), device=device, dtype=torch.uint8)
-    if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
+        if not need:
+            return None, 0
+        workspace = torch.empty(need, device=_device(index), dtype=torch.uint8)
+        return workspace, need
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the operands' device")
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _need(fn, *args) -> int:
+@functools.lru_cache(maxsize=4096)
+def _need(name: str, *args) -> int:
+    """A workspace query's answer, which goes by the sizes alone."""
     n = ctypes.c_size_t(0)
-    _lib.check(fn(*args, ctypes.byref(n)))
+    _lib.check(getattr(_lib.load(), name)(*args, ctypes.byref(n)))
     return n.value
 
 
-def _grads(grads, device, shapes: dict) -> dict:
+def _grads(grads, index: int, shapes: dict) -> dict:
     """The outputs of a backward: `grads` as given, or new contiguous ones."""
     if grads is None:
-        return {k: torch.empty(s, device=device, dtype=t) for k, (s, t) in shapes.items()}
+        return {k: _new(s, t, index) for k, (s, t) in shapes.items()}
     if set(grads) != set(shapes):
         raise ValueError(f"grads has {sorted(grads)}, expected {sorted(shapes)}")
     for k, (s, t) in shapes.items():
-        _check(grads[k], k, s, t, device, contiguous=False)
+        _check(grads[k], k, s, t, index, contiguous=False)
     return grads
+
+
+@functools.lru_cache(maxsize=None)
+def _device(index: int) -> torch.device:
+    return torch.device("cuda", index)
+
+
+def _new(shape, dtype, index: int):
+    return torch.empty(shape, device=_device(index), dtype=dtype)
 
 
 def _plain(g, name):
@@ -131,7 +161,7 @@ def ttt_conv_forward(x, weight, bias=None, state=None, activation: str = "silu",
     bias [C] fp32, state [B,K-1,C] the tokens before the first (zeros if
     None), activation "silu" or "none", lens [B] int32 optional lengths.
     Returns (y, state_out); state_out may be `state` itself."""
-    io, dev = _io(x, "x"), x.device
+    io, dev = _io(x, "x")
     B, L, C = x.shape
     K = weight.shape[-1]
     _check(weight, "weight", (C, K), torch.float32, dev)
@@ -140,9 +170,9 @@ def ttt_conv_forward(x, weight, bias=None, state=None, activation: str = "silu",
     if state is not None:
         _check(state, "state", (B, K - 1, C), x.dtype, dev)
     if y is None:
-        y = torch.empty((B, L, C), device=dev, dtype=x.dtype)
+        y = _new((B, L, C), x.dtype, dev)
     if state_out is None:
-        state_out = torch.empty((B, K - 1, C), device=dev, dtype=x.dtype)
+        state_out = _new((B, K - 1, C), x.dtype, dev)
     _check(y, "y", (B, L, C), x.dtype, dev, contiguous=False)
     _check(state_out, "state_out", (B, K - 1, C), x.dtype, dev)
     _call(_lib.load().ttt_conv_forward, dev, stream, B, L, C, K, io, _conv_act(activation), _ptr(x),
@@ -155,7 +185,7 @@ def ttt_conv_step(x, weight, state, bias=None, activation: str = "silu", y=None,
     """One token of ttt_conv_forward for each sequence: x [B,C] (a view with a
     contiguous last dimension allowed), state [B,K-1,C] updated in place.
     Returns y [B,C]."""
-    io, dev = _io(x, "x"), x.device
+    io, dev = _io(x, "x")
     B, C = x.shape
     K = weight.shape[-1]
     _check(weight, "weight", (C, K), torch.float32, dev)
@@ -163,7 +193,7 @@ def ttt_conv_step(x, weight, state, bias=None, activation: str = "silu", y=None,
         _check(bias, "bias", (C,), torch.float32, dev)
     _check(state, "state", (B, K - 1, C), x.dtype, dev)
     if y is None:
-        y = torch.empty((B, C), device=dev, dtype=x.dtype)
+        y = _new((B, C), x.dtype, dev)
     _check(y, "y", (B, C), x.dtype, dev)
     _call(_lib.load().ttt_conv_step, dev, stream, B, C, K, io, _conv_act(activation), _ptr(x),
           _rows(x, "x", _S1), _ptr(weight), _ptr(bias), _ptr(state), _ptr(y))
@@ -172,7 +202,7 @@ def ttt_conv_step(x, weight, state, bias=None, activation: str = "silu", y=None,
 
 def ttt_conv_backward_workspace(B: int, L: int, C: int, K: int) -> int:
     """Bytes of device workspace ttt_conv_backward needs."""
-    return _need(_lib.load().ttt_conv_backward_workspace, B, L, C, K)
+    return _need("ttt_conv_backward_workspace", B, L, C, K)
 
 
 def ttt_conv_backward(x, weight, dy, bias=None, state=None, dstate_out=None, activation: str = "silu",
@@ -181,7 +211,7 @@ def ttt_conv_backward(x, weight, dy, bias=None, state=None, dstate_out=None, act
     dx [B,L,C] in x's type, dweight [C,K] fp32, with a bias dbias [C] fp32 and
     with a state dstate [B,K-1,C] in x's type. `grads` may hold the outputs
     (a dict like the one returned; dx may be strided)."""
-    io, dev = _io(x, "x"), x.device
+    io, dev = _io(x, "x")
     B, L, C = x.shape
     K = weight.shape[-1]
     _check(weight, "weight", (C, K), torch.float32, dev)
@@ -209,7 +239,7 @@ def ttt_conv_backward(x, weight, dy, bias=None, state=None, dstate_out=None, act
 
 def _ssm_args(x, dt, A, B, C, D, dt_bias):
     """Checks and the operands' part of the argument list; B and C as given."""
-    io, dev = _io(x, "x"), x.device
+    io, dev = _io(x, "x")
     lead, (H, P) = x.shape[:-2], x.shape[-2:]
     G, N = B.shape[-2:]
     kind = _S2 if x.dim() == 3 else _S3
@@ -228,7 +258,7 @@ def _ssm_args(x, dt, A, B, C, D, dt_bias):
 
 def ttt_ssm_forward_workspace(B: int, L: int, H: int, P: int, G: int, N: int) -> int:
     """Bytes of device workspace ttt_ssm_forward needs."""
-    return _need(_lib.load().ttt_ssm_forward_workspace, B, L, H, P, G, N)
+    return _need("ttt_ssm_forward_workspace", B, L, H, P, G, N)
 
 
 def ttt_ssm_forward(x, dt, A, B, C, D=None, dt_bias=None, state=None, lens=None, y=None, state_out=None,
@@ -244,9 +274,9 @@ def ttt_ssm_forward(x, dt, A, B, C, D=None, dt_bias=None, state=None, lens=None,
     if state is not None:
         _check(state, "state", (Bn, H, N, P), torch.float32, dev)
     if y is None:
-        y = torch.empty((Bn, L, H, P), device=dev, dtype=x.dtype)
+        y = _new((Bn, L, H, P), x.dtype, dev)
     if state_out is None:
-        state_out = torch.empty((Bn, H, N, P), device=dev, dtype=torch.float32)
+        state_out = _new((Bn, H, N, P), torch.float32, dev)
     _check(y, "y", (Bn, L, H, P), x.dtype, dev, contiguous=False)
     _check(state_out, "state_out", (Bn, H, N, P), torch.float32, dev)
     workspace, nbytes = _workspace(workspace, ttt_ssm_forward_workspace(Bn, L, H, P, G, N), dev)
@@ -262,7 +292,7 @@ def ttt_ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, y=None, stream=Non
     dev, (Bn, H, P, G, N), args = _ssm_args(x, dt, A, B, C, D, dt_bias)
     _check(state, "state", (Bn, H, N, P), torch.float32, dev)
     if y is None:
-        y = torch.empty((Bn, H, P), device=dev, dtype=x.dtype)
+        y = _new((Bn, H, P), x.dtype, dev)
     _check(y, "y", (Bn, H, P), x.dtype, dev)
     _call(_lib.load().ttt_ssm_step, dev, stream, Bn, H, P, G, N, *args, _ptr(state), _ptr(y))
     return y
@@ -270,7 +300,7 @@ def ttt_ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, y=None, stream=Non
 
 def ttt_ssm_backward_workspace(B: int, L: int, H: int, P: int, G: int, N: int) -> int:
     """Bytes of device workspace ttt_ssm_backward needs."""
-    return _need(_lib.load().ttt_ssm_backward_workspace, B, L, H, P, G, N)
+    return _need("ttt_ssm_backward_workspace", B, L, H, P, G, N)
 
 
 def ttt_ssm_backward(x, dt, A, B, C, dy, D=None, dt_bias=None, state=None, dstate_out=None, lens=None,
@@ -309,9 +339,9 @@ def ttt_ssm_backward(x, dt, A, B, C, dy, D=None, dt_bias=None, state=None, dstat
 
 def _norm_args(resid, y, post_gamma, pre_gamma, gate, scale, post_beta, pre_beta, norm, gate_act, eps,
                lens):
-    io, dev = _io(y, "y"), y.device
+    io, dev = _io(y, "y")
     B, L, D = y.shape
-    rio = _io(resid, "resid")
+    rio, _ = _io(resid, "resid")
     _check(resid, "resid", (B, L, D), resid.dtype, dev, contiguous=False)
     if norm not in ("rms", "layer"):
         raise ValueError(f"norm {norm!r} is not 'rms' or 'layer'")
@@ -350,9 +380,9 @@ def ttt_block_norm(resid, y, post_gamma=None, pre_gamma=None, gate=None, scale=N
     dev, _, args = _norm_args(resid, y, post_gamma, pre_gamma, gate, scale, post_beta, pre_beta, norm,
                               gate_act, eps, lens)
     if resid_out is None:
-        resid_out = torch.empty(resid.shape, device=dev, dtype=resid.dtype)
+        resid_out = _new(resid.shape, resid.dtype, dev)
     if x is None:
-        x = torch.empty(y.shape, device=dev, dtype=y.dtype)
+        x = _new(y.shape, y.dtype, dev)
     _check(resid_out, "resid_out", resid.shape, resid.dtype, dev)
     _check(x, "x", y.shape, y.dtype, dev)
     _call(_lib.load().ttt_block_norm, dev, stream, *args, _ptr(resid_out), _ptr(x))
@@ -362,7 +392,7 @@ def ttt_block_norm(resid, y, post_gamma=None, pre_gamma=None, gate=None, scale=N
 def ttt_block_norm_backward_workspace(B: int, L: int, D: int, gate_dims: int = 0) -> int:
     """Bytes of device workspace ttt_block_norm_backward needs (gate_dims: the
     gate's number of dimensions, 0 without a gate)."""
-    return _need(_lib.load().ttt_block_norm_backward_workspace, B, L, D, gate_dims)
+    return _need("ttt_block_norm_backward_workspace", B, L, D, gate_dims)
 
 
 def ttt_block_norm_backward(resid, y, post_gamma, pre_gamma, dresid_out, dx, gate=None, scale=None,
