@@ -553,9 +553,9 @@ int ttt_conv_backward_workspace(int B, int L, int C, int K, size_t *bytes);
  *   B, C  : [B,L,G,N] io, strided (batch, token, group).
  *   state : [B,H,N,P] fp32 or NULL (zeros); state_out : the same or NULL; it
  *           may be exactly `state`.
- * The workspace holds ttt_ssm_forward_workspace's bytes (the states at the
- * borders of segments that run side by side; may be 0); calls that share one
- * must not overlap.
+ * The workspace holds ttt_ssm_forward_workspace's bytes (16 for each token and
+ * head, and the states at the borders of segments that run side by side);
+ * calls that share one must not overlap.
  * Numerics: state and sums in fp32. bf16 inputs with P = 64 and N = 32, 64 or
  * 128, in rows that allow 16-byte accesses, take MFMA products: the state's
  * update is exact to about 24 bits (its one unrounded operand is split into

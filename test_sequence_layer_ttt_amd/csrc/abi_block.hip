@@ -415,7 +415,7 @@ int ttt_ssm_forward_workspace(int B, int L, int H, int P, int G, int N, size_t *
     if ((st = ssm_common(B, L, H, P, G, N, TTT_F32)) || (st = ssm_plan(B, L, H, P, N))) return st;
     if (!bytes) return fail(TTT_E_NULL, "bytes is NULL");
     ttt::ssm_segments(B, L, H, P, N, false, false, &nseg, &seglen);
-    *bytes = ttt::ssm_forward_floats(B, H, P, N, nseg) * sizeof(float);
+    *bytes = ttt::ssm_forward_floats(B, L, H, P, N, nseg) * sizeof(float);
     return ok();
 }
 

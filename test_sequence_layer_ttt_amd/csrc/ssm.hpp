@@ -41,7 +41,7 @@ struct SsmBwdArgs {
 void ssm_segments(int B, int L, int H, int P, int N, bool mfma, bool backward, int *nseg, int *seglen);
 bool ssm_mfma_supported(const SsmArgs &a);
 // workspace floats
-size_t ssm_forward_floats(int B, int H, int P, int N, int nseg);
+size_t ssm_forward_floats(int B, int L, int H, int P, int N, int nseg);
 size_t ssm_backward_floats(int B, int L, int H, int P, int N, int nseg);
 
 hipError_t launch_ssm_step(const SsmArgs &a, hipStream_t stream);  // L = 1, state_out in place
@@ -72,6 +72,7 @@ struct SsmBwdWs {
     float *tiles;      // [B,H,ceil(L/64),8] sweeps: sums over pairs of 16-token tiles (i, j),
                        // (1,0) (2,0) (3,0) (2,1) (3,1) (3,2)
     float *part;       // [B*nseg][3][H]
+    float *prep;       // ssm_prep's chunks
     size_t floats;     // of all of them
 };
 SsmBwdWs ssm_backward_ws(const SsmArgs &a);
@@ -81,8 +82,11 @@ hipError_t launch_ssm_states_valu(const SsmArgs &a, const SsmOperand *dy, float 
                                   hipStream_t stream);
 hipError_t launch_ssm_mfma(const SsmArgs &a, hipStream_t stream);
 // the segments' shares of the states and of their gradients, one launch
-hipError_t launch_ssm_shares_mfma(const SsmArgs &a, const SsmOperand &dy, float *sf, float *sr, float *decay,
-                                  hipStream_t stream);
+hipError_t launch_ssm_shares_mfma(const SsmArgs &a, const SsmOperand &dy, const float *prep, float *sf, float *sr,
+                                  float *decay, hipStream_t stream);
+// the chunks' decays for the MFMA kernels
+size_t ssm_prep_floats(int B, int L, int H);
+hipError_t launch_ssm_prep(const SsmArgs &a, float *out, hipStream_t stream);
 bool ssm_bwd_mfma_supported(const SsmBwdArgs &g);
 hipError_t launch_ssm_bwd_mfma(const SsmBwdArgs &g, hipStream_t stream);
 

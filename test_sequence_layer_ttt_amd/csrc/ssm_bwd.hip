@@ -224,6 +224,7 @@ SsmBwdWs ssm_backward_ws(const SsmArgs &a) {
     w.dyx = take(2 * BH * a.L);
     w.tiles = take(BH * ((static_cast<int64_t>(a.L) + 63) / 64) * 8);
     w.part = take(static_cast<int64_t>(a.B) * a.nseg * 3 * a.H);
+    w.prep = take(static_cast<int64_t>(ssm_prep_floats(a.B, a.L, a.H)));
     return w;
 }
 
@@ -233,8 +234,9 @@ size_t ssm_backward_floats(int B, int L, int H, int P, int N, int nseg) {
     return ssm_backward_ws(a).floats;
 }
 
-size_t ssm_forward_floats(int B, int H, int P, int N, int nseg) {
-    return nseg > 1 ? static_cast<size_t>(B) * H * nseg * (static_cast<size_t>(N) * P + 1) : 0;
+size_t ssm_forward_floats(int B, int L, int H, int P, int N, int nseg) {
+    return ssm_prep_floats(B, L, H) +
+           (nseg > 1 ? static_cast<size_t>(B) * H * nseg * (static_cast<size_t>(N) * P + 1) : 0);
 }
 
 void ssm_segments(int B, int L, int H, int P, int N, bool mfma, bool backward, int *nseg, int *seglen) {

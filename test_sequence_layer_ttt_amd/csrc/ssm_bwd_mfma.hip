@@ -18,8 +18,9 @@
 // serve the dot products with those outputs.
 //  * The row and col sums are fp32: G and E are products of bf16 inputs summed
 //    in fp32, and S dy (R x) takes the state in three bf16 parts. They feed
-//    dA and ddt, where they are subtracted; dx, dB, dC are stored as bf16 and
-//    take the decayed products as bf16 operands.
+//    dA and ddt, where they are subtracted; dx, dB, dC are stored as bf16.
+//    dx takes the decayed products and R as bf16 operands, dB and dC take
+//    theirs in two bf16 parts (a group's heads add up their roundings).
 //  * dB and dC of each head go out in fp32 and are summed over the group's
 //    heads in a fixed order by ssm_bwd.hip.
 // Bound by issue and latency of the many small products; two workgroups share
@@ -39,6 +40,11 @@ template <int N> struct BwdSmem {
     ChunkDecay d[2];
 };
 
+// what rounding to bf16 leaves
+__device__ __forceinline__ f32x4 rest(f32x4 v) {
+    const uint2 p = __builtin_bit_cast(uint2, pack4(v));
+    return v - unpack4(p);
+}
 // place of the sum over rows of tile i and columns of tile j < i (see ssm.hpp)
 __device__ __forceinline__ int pair_index(int i, int j) { return j == 0 ? i - 1 : j + i; }
 
@@ -67,7 +73,7 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
     constexpr int NT = N >= 64 ? N / 64 : 1, UT = N >= 64 ? 4 : 2;  // the wave's part of the state
     const SsmBwdArgs &ga = w.g;
     const SsmArgs &a = ga.f;
-    const int lane = threadIdx.x % 64, wv = threadIdx.x / 64, g = lane / 16, c = lane % 16;
+    const int lane = threadIdx.x % 64, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), g = lane / 16, c = lane % 16;
     int bs, h;
     place(blockIdx.x, a.B * a.nseg, a.H, bs, h);
     const int b = bs / a.nseg, seg = bs % a.nseg, gr = h / (a.H / a.G), bh = b * a.H + h;
@@ -76,14 +82,14 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
     const int t0 = static_cast<int>(s0 < a.L ? s0 : a.L);
     const int t1 = static_cast<int>(s0 + a.seglen < a.L ? s0 + a.seglen : a.L);
     const int te = max(t0, min(t1, n));
-    const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
+    const float Dh = a.D ? a.D[h] : 0.f;
+    const float *prep = w.w.prep + static_cast<int64_t>(bh) * ((a.L + Q - 1) / Q) * 4 * Q;
     const SsmOperand &ov = REV ? ga.dy : a.x, &oz = REV ? a.x : ga.dy;
     const SsmOperand &ok = REV ? a.Cm : a.Bm, &oq = REV ? a.Bm : a.Cm;
     const bf16_t *vp = static_cast<const bf16_t *>(ov.p) + b * ov.sb + h * ov.sh;
     const bf16_t *zp = static_cast<const bf16_t *>(oz.p) + b * oz.sb + h * oz.sh;
     const bf16_t *kp = static_cast<const bf16_t *>(ok.p) + b * ok.sb + gr * ok.sh;
     const bf16_t *qp = static_cast<const bf16_t *>(oq.p) + b * oq.sb + gr * oq.sh;
-    const bf16_t *dp = static_cast<const bf16_t *>(a.dt.p) + b * a.dt.sb + h * a.dt.sh;
     bf16_t *dxp = static_cast<bf16_t *>(const_cast<void *>(ga.dx.p)) + b * ga.dx.sb + h * ga.dx.sh;
     float *ph = (REV ? w.w.dBh : w.w.dCh) + static_cast<int64_t>(bh) * a.L * N;
     const int64_t tok0 = static_cast<int64_t>(bh) * a.L, inter = static_cast<int64_t>(a.B) * a.H * a.L;
@@ -103,7 +109,7 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
     Stage<64> sv;
     Stage<N> sk;
     bf16x8 zn[2], qn[KB];
-    float dt = 0.f;
+    StageDecay sd;
     auto fetch = [&](int t) {
         const int count = min(Q, te - t);
         sv.fetch(vp + static_cast<int64_t>(t) * ov.st, ov.st, count);
@@ -113,12 +119,12 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
         for (int kb = 0; kb < 2; ++kb) zn[kb] = own_frag(zp + own * oz.st, kb, g);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) qn[kb] = own_frag(qp + own * oq.st, kb, g);
-        if (wv == 0 && lane < count) dt = bf16_to_f32(dp[static_cast<int64_t>(t + lane) * a.dt.st]);
+        sd.fetch(prep + static_cast<int64_t>(t / Q) * 4 * Q);
     };
-    auto put = [&](int t, int buf) {
+    auto put = [&](int buf) {
         sv.put(sm.v[buf], XS);
         sk.put(sm.k[buf], NS);
-        if (wv == 0) chunk_decay<bf16_t>(sm.d[buf], a, dt, bias, A, lane, min(Q, te - t));
+        sd.put(sm.d[buf]);
     };
     auto share_state = [&]() {
 #pragma unroll
@@ -137,12 +143,12 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
     auto chunk = [&](int i) { return t0 + (REV ? nc - 1 - i : i) * Q; };
     if (nc) {
         fetch(chunk(0));
-        put(chunk(0), 0);
+        put(0);
         share_state();
     }
     for (int ci = 0; ci < nc; ++ci) {
         const int t = chunk(ci), buf = ci % 2;
-        __syncthreads();
+        lds_barrier();
         bf16x8 z[2], q[KB];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) z[kb] = zn[kb];
@@ -156,7 +162,7 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
         const float hi = d.hi[o], lo = d.lo[o], step = d.step[o];
         const float reach = REV ? d.tail[o] : fast_exp2(hi);  // decay between the token and the state
         // products with the tokens before (behind) this lane's: rows m = 4 g + r
-        bf16x8 me[2], mg[2];
+        bf16x8 me[2][2], mg[2];
         float strict = 0.f, diag = 0.f, apart[4] = {};
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
@@ -195,7 +201,8 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
                 pe[k] = E;
                 pg[k] = G;
             }
-            me[kb] = pack8(pe[0], pe[1]);
+            me[kb][0] = pack8(pe[0], pe[1]);
+            me[kb][1] = pack8(rest(pe[0]), rest(pe[1]));
             if constexpr (REV) mg[kb] = pack8(pg[0], pg[1]);
         }
         // a column's (row's) sum over the tiles, and the tiles' sums over the wave
@@ -225,7 +232,11 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
             }
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
-                if (REV ? 2 * kb + 1 >= wv : 2 * kb <= wv) acc = mfma32(tokens_frag(kt, NS, kb, 16 * tn, g, c), me[kb], acc);
+                if (REV ? 2 * kb + 1 >= wv : 2 * kb <= wv) {
+                    const bf16x8 f = tokens_frag(kt, NS, kb, 16 * tn, g, c);
+                    acc = mfma32(f, me[kb][1], acc);
+                    acc = mfma32(f, me[kb][0], acc);
+                }
             }
             if (live) {
                 if (REV) {
@@ -281,7 +292,7 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
             }
         }
         if (more) {  // the state before the next chunk
-            const float whole = fast_exp2(d.total);
+            const float whole = fast_exp2(d.total());
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -302,7 +313,7 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     bf16x8 kw[3];
-                    weigh(tokens_frag(kt, NS, kb, 16 * (nt0 + i), g, c), w0, w1, kw);
+                    weigh<3>(tokens_frag(kt, NS, kb, 16 * (nt0 + i), g, c), w0, w1, kw);
 #pragma unroll
                     for (int k = 0; k < 3; ++k)
 #pragma unroll
@@ -310,8 +321,8 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
                             st[i][u] = mfma32(kw[k], N >= 64 || wv < 2 ? vf[kb][u] : vf[kb][2 + u % 2], st[i][u]);
                 }
             }
-            put(chunk(ci + 1), buf ^ 1);
-            __syncthreads();  // every wave has read the state's parts
+            put(buf ^ 1);
+            lds_barrier();  // every wave has read the state's parts
             share_state();
         }
     }
@@ -350,7 +361,8 @@ hipError_t launch_ssm_bwd_mfma(const SsmBwdArgs &g, hipStream_t stream) {
     const int NP = a.N * a.P;
     const SsmBwdWs s = ssm_backward_ws(a);
     hipError_t e;
-    if ((e = launch_ssm_shares_mfma(a, g.dy, s.sf, s.sr, s.decay, stream)) != hipSuccess) return e;
+    if ((e = launch_ssm_prep(a, s.prep, stream)) != hipSuccess) return e;
+    if ((e = launch_ssm_shares_mfma(a, g.dy, s.prep, s.sf, s.sr, s.decay, stream)) != hipSuccess) return e;
     if ((e = launch_ssm_carry(a.B * a.H, NP, a.nseg, false, a.state, s.decay, s.sf, s.last, stream)) != hipSuccess) return e;
     if ((e = launch_ssm_carry(a.B * a.H, NP, a.nseg, true, g.dstate_out, s.decay, s.sr, g.dstate, stream)) != hipSuccess)
         return e;

@@ -10,9 +10,12 @@
 //    X^T M^T as it stands (no trip through LDS); Y^T gives four adjacent
 //    features of one token to a lane.
 //  * The state lives in accumulators, fp32: wave w holds N / 4 of its rows
-//    (N = 32: half of the columns of 16). Its update takes X exactly as it is
-//    and B D exp(..) split into three bf16 parts, so the state is that of fp32
-//    arithmetic; only its copy for C S, in LDS, is rounded to bf16, as is M.
+//    (N = 32: half of the columns of 16). Where it goes on to the caller or to
+//    another segment, its update takes X exactly as it is and B D exp(..) split
+//    into three bf16 parts, so it is that of fp32 arithmetic; where it only
+//    feeds C S of its own segment, one rounded part. Its copy for C S, in LDS,
+//    is rounded to bf16, as is M: y is off by 1.9e-3 of its norm, of which
+//    the rounding of y itself is 1.7e-3.
 //  * X and B of the next chunk are fetched to registers while this one is
 //    worked on, C straight to the fragment that needs it; X^T and B^T are read
 //    from the row-major tiles by transposing LDS reads.
@@ -43,19 +46,20 @@ struct MfmaArgs {
     const float *init;    // [B,H,(nseg,)N,P]
     int64_t init_stride;  // as in WalkArgs
     float *fin, *decay;
+    const float *prep;    // ssm_prep's chunks
 };
 
 // OUT: outputs and the state's update. Otherwise the segment's share of the
 // state alone, or (REV) of the state's gradient: a walk from the segment's end
 // over S <- exp(l_63) S + (C diag(exp(l)))^T dY, with C in Bm and dY in x.
-template <int N, bool OUT, bool REV>
+template <int N, bool OUT, bool REV, int PARTS>
 __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
     constexpr int NS = Smem<N, OUT>::NS, KB = N / 32;
     constexpr int NT = N >= 64 ? N / 64 : 1;  // row tiles of the state in a wave
     constexpr int UT = N >= 64 ? 4 : 2;       // its feature tiles
     static_assert(!(OUT && REV), "outputs are made forwards");
     const SsmArgs &a = w.a;
-    const int lane = threadIdx.x % 64, wv = threadIdx.x / 64, g = lane / 16, c = lane % 16;
+    const int lane = threadIdx.x % 64, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), g = lane / 16, c = lane % 16;
     int bs, h;
     place(blockIdx.x, a.B * a.nseg, a.H, bs, h);
     const int b = bs / a.nseg, seg = bs % a.nseg, gr = h / (a.H / a.G), bh = b * a.H + h;
@@ -64,11 +68,11 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
     const int t0 = static_cast<int>(s0 < a.L ? s0 : a.L);
     const int t1 = static_cast<int>(s0 + a.seglen < a.L ? s0 + a.seglen : a.L);
     const int te = max(t0, min(t1, n));
-    const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
+    const float Dh = a.D ? a.D[h] : 0.f;
+    const float *prep = w.prep + static_cast<int64_t>(bh) * ((a.L + Q - 1) / Q) * 4 * Q;
     const bf16_t *xp = static_cast<const bf16_t *>(a.x.p) + b * a.x.sb + h * a.x.sh;
     const bf16_t *bp = static_cast<const bf16_t *>(a.Bm.p) + b * a.Bm.sb + gr * a.Bm.sh;
     const bf16_t *cp = static_cast<const bf16_t *>(a.Cm.p) + b * a.Cm.sb + gr * a.Cm.sh;
-    const bf16_t *dp = static_cast<const bf16_t *>(a.dt.p) + b * a.dt.sb + h * a.dt.sh;
     bf16_t *yp = static_cast<bf16_t *>(const_cast<void *>(a.y.p)) + b * a.y.sb + h * a.y.sh;
     const int nt0 = N >= 64 ? NT * wv : wv % 2, u0 = N >= 64 ? 0 : 2 * (wv / 2);
     constexpr int64_t NP = static_cast<int64_t>(N) * 64;
@@ -86,7 +90,7 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
     Stage<64> sx;
     Stage<N> sb;
     bf16x8 cf[KB], cn[KB];
-    float dt = 0.f;
+    StageDecay sd;
     auto fetch = [&](int t) {  // the chunk at token t < te
         const int count = min(Q, te - t);
         sx.fetch(xp + static_cast<int64_t>(t) * a.x.st, a.x.st, count);
@@ -96,12 +100,12 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) cn[kb] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4 *>(p + 32 * kb));
         }
-        if (wv == 0 && lane < count) dt = bf16_to_f32(dp[static_cast<int64_t>(t + lane) * a.dt.st]);
+        sd.fetch(prep + static_cast<int64_t>(t / Q) * 4 * Q);
     };
-    auto put = [&](int t, int buf) {
+    auto put = [&](int buf) {
         sx.put(sm.x[buf], XS);
         sb.put(sm.b[buf], NS);
-        if (wv == 0) chunk_decay<bf16_t>(sm.d[buf], a, dt, bias, A, lane, min(Q, te - t));
+        sd.put(sm.d[buf]);
     };
     auto share_state = [&]() {
 #pragma unroll
@@ -115,12 +119,12 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
     auto chunk = [&](int i) { return t0 + (REV ? nc - 1 - i : i) * Q; };
     if (nc) {
         fetch(chunk(0));
-        put(chunk(0), 0);
+        put(0);
         if constexpr (OUT) share_state();
     }
     for (int ci = 0; ci < nc; ++ci) {
         const int t = chunk(ci), buf = ci % 2;
-        __syncthreads();
+        lds_barrier();
         if constexpr (OUT) {
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) cf[kb] = cn[kb];
@@ -202,8 +206,8 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
                 }
             }
         }
-        const float whole = fast_exp2(d.total);
-        total += d.total;
+        const float whole = fast_exp2(d.total());
+        total += d.total();
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -234,19 +238,19 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
             }
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                bf16x8 bw[3];
-                weigh(tokens_frag(bt, NS, kb, 16 * (nt0 + i), g, c), w0, w1, bw);
+                bf16x8 bw[PARTS];
+                weigh<PARTS>(tokens_frag(bt, NS, kb, 16 * (nt0 + i), g, c), w0, w1, bw);
 #pragma unroll
-                for (int k = 0; k < 3; ++k)
+                for (int k = 0; k < PARTS; ++k)
 #pragma unroll
                     for (int u = 0; u < UT; ++u)
                         st[i][u] = mfma32(bw[k], N >= 64 || wv < 2 ? xf[kb][u] : xf[kb][2 + u % 2], st[i][u]);
             }
         }
-        if (more) put(chunk(ci + 1), buf ^ 1);
+        if (more) put(buf ^ 1);
         if constexpr (OUT) {
             if (more) {
-                __syncthreads();  // every wave has read the state's copy
+                lds_barrier();  // every wave has read the state's copy
                 share_state();
             }
         }
@@ -267,26 +271,30 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
     if (!OUT && threadIdx.x == 0) w.decay[static_cast<int64_t>(bh) * a.nseg + seg] = exp2f(total);
 }
 
-template <int N>
+// PARTS 3: the state goes on to the caller. 1: it does not (its exact value
+// comes from the shares) and only feeds the outputs, through a bf16 copy.
+template <int N, int PARTS>
 __global__ __launch_bounds__(256, N == 128 ? 2 : 3) void outputs(MfmaArgs w) {
     __shared__ Smem<N, true> sm;
-    chunks<N, true, false>(w, sm);
+    chunks<N, true, false, PARTS>(w, sm);
 }
 // blockIdx.y: the states' shares, then those of their gradients
 template <int N>
 __global__ __launch_bounds__(256, N == 128 ? 2 : 3) void shares(MfmaArgs f, MfmaArgs r) {
     __shared__ Smem<N, false> sm;
     if (blockIdx.y == 0)
-        chunks<N, false, false>(f, sm);
+        chunks<N, false, false, 3>(f, sm);
     else
-        chunks<N, false, true>(r, sm);
+        chunks<N, false, true, 3>(r, sm);
 }
 
 template <int N> hipError_t run(const MfmaArgs *out, const MfmaArgs *f, const MfmaArgs *r, hipStream_t s) {
     const SsmArgs &a = out ? out->a : f->a;
     const unsigned blocks = static_cast<unsigned>(a.B) * a.H * a.nseg;
-    if (out)
-        hipLaunchKernelGGL((outputs<N>), dim3(blocks), dim3(256), 0, s, *out);
+    if (out && out->fin)
+        hipLaunchKernelGGL((outputs<N, 3>), dim3(blocks), dim3(256), 0, s, *out);
+    else if (out)
+        hipLaunchKernelGGL((outputs<N, 1>), dim3(blocks), dim3(256), 0, s, *out);
     else
         hipLaunchKernelGGL((shares<N>), dim3(blocks, r ? 2 : 1), dim3(256), 0, s, *f, r ? *r : *f);
     return hipGetLastError();
@@ -304,12 +312,12 @@ bool wide(const SsmOperand &o) {  // rows of 16-byte accesses
 
 bool ssm_mfma_supported(const SsmArgs &a) {
     return a.io == 1 && a.P == 64 && (a.N == 32 || a.N == 64 || a.N == 128) && wide(a.x) && wide(a.Bm) &&
-           wide(a.Cm) && wide(a.y);
+           wide(a.Cm) && wide(a.y) && (reinterpret_cast<uintptr_t>(a.ws) & 15) == 0;
 }
 
-hipError_t launch_ssm_shares_mfma(const SsmArgs &a, const SsmOperand &dy, float *sf, float *sr, float *decay,
-                                  hipStream_t stream) {
-    MfmaArgs f{a, nullptr, 0, sf, decay}, r{a, nullptr, 0, sr, decay};
+hipError_t launch_ssm_shares_mfma(const SsmArgs &a, const SsmOperand &dy, const float *prep, float *sf, float *sr,
+                                  float *decay, hipStream_t stream) {
+    MfmaArgs f{a, nullptr, 0, sf, decay, prep}, r{a, nullptr, 0, sr, decay, prep};
     r.a.x = dy;
     r.a.Bm = a.Cm;
     return run(nullptr, &f, &r, stream);
@@ -317,11 +325,13 @@ hipError_t launch_ssm_shares_mfma(const SsmArgs &a, const SsmOperand &dy, float 
 
 hipError_t launch_ssm_mfma(const SsmArgs &a, hipStream_t stream) {
     const int64_t NP = static_cast<int64_t>(a.N) * a.P;
-    MfmaArgs w{a, a.state, 0, a.state_out, nullptr};
+    float *prep = a.ws, *seg = a.ws + ssm_prep_floats(a.B, a.L, a.H);
+    hipError_t e;
+    if ((e = launch_ssm_prep(a, prep, stream)) != hipSuccess) return e;
+    MfmaArgs w{a, a.state, 0, a.state_out, nullptr, prep};
     if (a.nseg > 1) {
-        float *seg = a.ws, *decay = a.ws + static_cast<int64_t>(a.B) * a.H * a.nseg * NP;
-        MfmaArgs p{a, nullptr, 0, seg, decay};
-        hipError_t e;
+        float *decay = seg + static_cast<int64_t>(a.B) * a.H * a.nseg * NP;
+        const MfmaArgs p{a, nullptr, 0, seg, decay, prep};
         if ((e = run(nullptr, &p, nullptr, stream)) != hipSuccess) return e;
         if ((e = launch_ssm_carry(a.B * a.H, static_cast<int>(NP), a.nseg, false, a.state, decay, seg, a.state_out,
                                   stream)) != hipSuccess)

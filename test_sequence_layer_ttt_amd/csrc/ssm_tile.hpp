@@ -42,49 +42,14 @@ __device__ __forceinline__ bf16x8 tokens_frag(const uint16_t *tile, int stride, 
     return join(read_tr(p), read_tr(p + 16 * stride));
 }
 
-template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_add64(double v) {
-    const uint64_t u = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, ROWS, 0xF, true);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, ROWS, 0xF, true);
-    return v + __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
-}
-// Inclusive sums over the lanes 0 .. lane: within rows of 16 lanes, then the
-// rows' totals.
-__device__ __forceinline__ double wave_scan(double v) {
-    v = dpp_add64<0x111, 0xF>(v);  // row_shr:1
-    v = dpp_add64<0x112, 0xF>(v);  // row_shr:2
-    v = dpp_add64<0x114, 0xF>(v);  // row_shr:4
-    v = dpp_add64<0x118, 0xF>(v);  // row_shr:8
-    v = dpp_add64<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
-    v = dpp_add64<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
-    return v;
-}
-
 // Per token of a chunk: log2 of the decay since the chunk's start, split into
 // two floats (their differences are decays between two tokens: one float would
-// lose up to |sum| 2^-24 of them), and D_t; the decay to the chunk's end.
+// lose up to |sum| 2^-24 of them), D_t, and the decay to the chunk's end.
 struct ChunkDecay {
     alignas(16) float hi[Q], lo[Q], step[Q], tail[Q];
-    float total;  // log2 of the whole chunk's decay
+    __device__ __forceinline__ float total() const { return hi[Q - 1]; }  // log2 of the whole chunk's
 };
-
-// One wave, lane = token. Tokens at and past `count` decay nothing and add
-// nothing. A factor below 2^-160 is zero in fp32 as it is, so the logarithms
-// are held above that.
-template <typename T>
-__device__ __forceinline__ void chunk_decay(ChunkDecay &d, const SsmArgs &a, float raw_dt, float bias, float A,
-                                            int lane, int count) {
-    const float step = lane < count ? softplus_f(raw_dt + bias) : 0.f;
-    const double l = lane < count ? fmax(static_cast<double>(step) * A * 1.4426950408889634, -160.0) : 0.0;
-    const double s = wave_scan(l);
-    const double all = __shfl(s, 63, 64);
-    const float hi = static_cast<float>(s);
-    d.hi[lane] = hi;
-    d.lo[lane] = static_cast<float>(s - hi);
-    d.step[lane] = step;
-    d.tail[lane] = exp2f(static_cast<float>(all - s));
-    if (lane == 0) d.total = static_cast<float>(all);
-}
+static_assert(sizeof(ChunkDecay) == 4 * Q * sizeof(float), "as ssm_prep writes it");
 
 // x = a + b + c to about 24 bits, each a bf16 (two floats at a time)
 __device__ __forceinline__ void split3(float x0, float x1, uint32_t &a, uint32_t &b, uint32_t &c) {
@@ -96,8 +61,10 @@ __device__ __forceinline__ void split3(float x0, float x1, uint32_t &a, uint32_t
 }
 
 // A fragment of a transposed read times one weight for each of its tokens
-// (w0: the first four, w1: the others), in three bf16 parts.
-__device__ __forceinline__ void weigh(bf16x8 f, f32x4 w0, f32x4 w1, bf16x8 (&out)[3]) {
+// (w0: the first four, w1: the others), in one or three bf16 parts.
+template <int PARTS>
+__device__ __forceinline__ void weigh(bf16x8 f, f32x4 w0, f32x4 w1, bf16x8 (&out)[PARTS]) {
+    static_assert(PARTS == 1 || PARTS == 3, "rounded, or to about 24 bits");
     const uint4 r = __builtin_bit_cast(uint4, f);
     const uint32_t in[4] = {r.x, r.y, r.z, r.w};
     uint32_t p[3][4];
@@ -105,10 +72,14 @@ __device__ __forceinline__ void weigh(bf16x8 f, f32x4 w0, f32x4 w1, bf16x8 (&out
     for (int i = 0; i < 4; ++i) {
         const float a = lo_bf(in[i]) * (i < 2 ? w0[2 * i] : w1[2 * i - 4]);
         const float b = hi_bf(in[i]) * (i < 2 ? w0[2 * i + 1] : w1[2 * i - 3]);
-        split3(a, b, p[0][i], p[1][i], p[2][i]);
+        if constexpr (PARTS == 1)
+            p[0][i] = pack2(a, b);
+        else
+            split3(a, b, p[0][i], p[1][i], p[2][i]);
     }
 #pragma unroll
-    for (int k = 0; k < 3; ++k) out[k] = __builtin_bit_cast(bf16x8, make_uint4(p[k][0], p[k][1], p[k][2], p[k][3]));
+    for (int k = 0; k < PARTS; ++k)
+        out[k] = __builtin_bit_cast(bf16x8, make_uint4(p[k][0], p[k][1], p[k][2], p[k][3]));
 }
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -134,6 +105,17 @@ template <int F> struct Stage {
         const int row = threadIdx.x / PER, f = threadIdx.x % PER * 8;
 #pragma unroll
         for (int i = 0; i < NP; ++i) *reinterpret_cast<uint4 *>(tile + (row + i * ROWS) * lds_stride + f) = r[i];
+    }
+};
+
+// A chunk's decays, which ssm_prep has laid out, to LDS by the first 64 threads.
+struct StageDecay {
+    uint4 r;
+    __device__ __forceinline__ void fetch(const float *base) {
+        if (threadIdx.x < Q) r = *reinterpret_cast<const uint4 *>(base + 4 * threadIdx.x);
+    }
+    __device__ __forceinline__ void put(ChunkDecay &d) const {
+        if (threadIdx.x < Q) *reinterpret_cast<uint4 *>(&d.hi[0] + 4 * threadIdx.x) = r;
     }
 };
 

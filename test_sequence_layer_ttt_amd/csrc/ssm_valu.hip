@@ -58,7 +58,7 @@ __global__ __launch_bounds__(512) void walk(WalkArgs w) {
     const int nw = blockDim.x / 64, kp = nw * KW;
     float *ks = lds, *qs = ks + T * kp, *vs = qs + (OUT ? T * kp : 0), *as = vs + T * 64, *ds = as + T;
     float *yp = ds + T, *kq = yp + (OUT ? nw * T * 64 : 0);  // [nw][T][64], [nw][T]
-    const int lane = threadIdx.x % 64, wv = threadIdx.x / 64;
+    const int lane = threadIdx.x % 64, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int vb = blockIdx.y, vi = vb * 64 + lane;
     const int seg = blockIdx.x % a.nseg;
     const int bh = blockIdx.x / a.nseg, b = bh / a.H, h = bh % a.H, gr = h / (a.H / a.G);
@@ -238,7 +238,7 @@ __global__ __launch_bounds__(CT) void carry(int NP, int nseg, int reverse, const
     float *p = seg + bh * nseg * NP + i;
     const float *d = decay + bh * nseg;
     float s = first ? first[bh * NP + i] : 0.f;
-    constexpr int U = 8;
+    constexpr int U = 16;  // segments in flight
     for (int k0 = 0; k0 < nseg; k0 += U) {
         float v[U];
 #pragma unroll
