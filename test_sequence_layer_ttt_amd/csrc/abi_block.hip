@@ -414,8 +414,13 @@ int ttt_ssm_forward_workspace(int B, int L, int H, int P, int G, int N, size_t *
     int st, nseg, seglen;
     if ((st = ssm_common(B, L, H, P, G, N, TTT_F32)) || (st = ssm_plan(B, L, H, P, N))) return st;
     if (!bytes) return fail(TTT_E_NULL, "bytes is NULL");
-    ttt::ssm_segments(B, L, H, P, N, false, false, &nseg, &seglen);
-    *bytes = ttt::ssm_forward_floats(B, L, H, P, N, nseg) * sizeof(float);
+    // either path's segments: which one runs goes by the operands' addresses
+    size_t most = 0;
+    for (int mfma = 0; mfma < 2; ++mfma) {
+        ttt::ssm_segments(B, L, H, P, N, mfma != 0, false, &nseg, &seglen);
+        most = std::max(most, ttt::ssm_forward_floats(B, L, H, P, N, nseg));
+    }
+    *bytes = most * sizeof(float);
     return ok();
 }
 
@@ -424,11 +429,10 @@ int ttt_ssm_forward(int B, int L, int H, int P, int G, int N, int io, const void
                     const int64_t *B_strides, const void *Cm, const int64_t *C_strides, const float *D,
                     const float *dt_bias, const float *state, const int *lens, void *y, const int64_t *y_strides,
                     float *state_out, void *workspace, size_t workspace_bytes, hipStream_t stream) {
-    int st, nseg, seglen;
+    int st;
     size_t need;
     if ((st = ssm_common(B, L, H, P, G, N, io)) || (st = ttt_ssm_forward_workspace(B, L, H, P, G, N, &need)))
         return st;
-    ttt::ssm_segments(B, L, H, P, N, false, false, &nseg, &seglen);
     const unsigned es = esize(io);
     const View vx = view(x, "x", B, L, H, P, x_strides, 3, es), vt = view(dt, "dt", B, L, H, 1, dt_strides, 3, es),
                vb = view(Bm, "B", B, L, G, N, B_strides, 3, es), vc = view(Cm, "C", B, L, G, N, C_strides, 3, es),
@@ -448,7 +452,8 @@ int ttt_ssm_forward(int B, int L, int H, int P, int G, int N, int io, const void
         return st;
     if (!B) return ok();
     ttt::SsmArgs a{B, L, H, P, G, N, io, operand(vx), operand(vt), operand(vb), operand(vc), A, D, dt_bias, state,
-                   lens, operand(vy), state_out, static_cast<float *>(workspace), nseg, seglen};
+                   lens, operand(vy), state_out, static_cast<float *>(workspace), 1, 64};
+    ttt::ssm_segments(B, L, H, P, N, ttt::ssm_mfma_supported(a), false, &a.nseg, &a.seglen);
     return launched(ttt::launch_ssm_forward(a, stream));
 }
 

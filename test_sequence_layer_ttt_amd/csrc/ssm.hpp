@@ -40,6 +40,9 @@ struct SsmBwdArgs {
 // segments of the forward and of the backward
 void ssm_segments(int B, int L, int H, int P, int N, bool mfma, bool backward, int *nseg, int *seglen);
 bool ssm_mfma_supported(const SsmArgs &a);
+// Values (of VD features) that a lane of the walks holds, 16 lanes side by side:
+// their blocks are of 16 times as many.
+int ssm_lane_values(int B, int L, int H, int VD);
 // workspace floats
 size_t ssm_forward_floats(int B, int L, int H, int P, int N, int nseg);
 size_t ssm_backward_floats(int B, int L, int H, int P, int N, int nseg);
@@ -64,11 +67,13 @@ struct SsmBwdWs {
     float *last;      // [B,H,N,P] state after the last segment
     float *decay;     // [B,H,nseg]
     float *dBh, *dCh; // [B,H,L,N] per head
-    // [2,B,H,L] per token. From the walks: two blocks of features' shares of
-    // the strict products. From the sweeps: the part within the 64-token
-    // chunk, then the part through the state before (behind) it.
+    // [blocks,B,H,L] per token. From the walks: the blocks of values' shares of
+    // the strict products (row: of N, col: of P). From the sweeps: the part
+    // within the 64-token chunk, then the part through the state before
+    // (behind) it.
     float *row, *col;
-    float *xdu, *dyx;  // [2,B,H,L] x . du and dy . x, by blocks of features (sweeps: the first)
+    float *xdu, *dyx;  // x . du and dy . x, by blocks of P (sweeps: the first)
+    int rows, cols;    // blocks of the walks
     float *tiles;      // [B,H,ceil(L/64),8] sweeps: sums over pairs of 16-token tiles (i, j),
                        // (1,0) (2,0) (3,0) (2,1) (3,1) (3,2)
     float *part;       // [B*nseg][3][H]

@@ -19,6 +19,8 @@
 //     ddt_t = (A q_t + x_t . du_t) sigma(dt_t + dt_bias),
 //     dA = sum D_t q_t,  dD = sum dy_t . x_t,  ddt_bias = sum ddt_t,
 // and dB, dC are summed over the heads of a group.
+#include <cmath>
+
 #include "block.hpp"
 #include "ssm.hpp"
 #include "vec.hpp"
@@ -127,8 +129,8 @@ __global__ __launch_bounds__(NT) void decay_gradient(FinishArgs f) {
     } else {
         double w = 0.0;
         if (live) {
-            for (int i = 0; i < (a.N + 63) / 64; ++i) w += f.w.row[i * blk + tok];
-            for (int i = 0; i < (a.P + 63) / 64; ++i) {
+            for (int i = 0; i < f.w.rows; ++i) w += f.w.row[i * blk + tok];
+            for (int i = 0; i < f.w.cols; ++i) {
                 w -= f.w.col[i * blk + tok];
                 xdu += f.w.xdu[i * blk + tok];
                 dyx += f.w.dyx[i * blk + tok];
@@ -218,10 +220,13 @@ SsmBwdWs ssm_backward_ws(const SsmArgs &a) {
     w.decay = take(BH * a.nseg);
     w.dBh = take(BH * a.L * a.N);
     w.dCh = take(BH * a.L * a.N);
-    w.row = take(2 * BH * a.L);
-    w.col = take(2 * BH * a.L);
-    w.xdu = take(2 * BH * a.L);
-    w.dyx = take(2 * BH * a.L);
+    const int rb = 16 * ssm_lane_values(a.B, a.L, a.H, a.N), cb = 16 * ssm_lane_values(a.B, a.L, a.H, a.P);
+    w.rows = (a.N + rb - 1) / rb;
+    w.cols = (a.P + cb - 1) / cb;
+    w.row = take((w.rows > 2 ? w.rows : 2) * BH * a.L);
+    w.col = take((w.cols > 2 ? w.cols : 2) * BH * a.L);
+    w.xdu = take(w.cols * BH * a.L);
+    w.dyx = take(w.cols * BH * a.L);
     w.tiles = take(BH * ((static_cast<int64_t>(a.L) + 63) / 64) * 8);
     w.part = take(static_cast<int64_t>(a.B) * a.nseg * 3 * a.H);
     w.prep = take(static_cast<int64_t>(ssm_prep_floats(a.B, a.L, a.H)));
@@ -241,20 +246,33 @@ size_t ssm_forward_floats(int B, int L, int H, int P, int N, int nseg) {
 
 void ssm_segments(int B, int L, int H, int P, int N, bool mfma, bool backward, int *nseg, int *seglen) {
     (void)P;
-    // as many workgroups as run at once (three a compute unit, two where N
-    // takes more of its LDS and registers), segments of whole 64-token chunks;
-    // the backward's sums over a segment hold 256 tokens, 64 after the walks
-    const int64_t slots = N > 64 ? 512 : 768;
     const int64_t heads = static_cast<int64_t>(B) * H;
-    const int64_t chunks = (static_cast<int64_t>(L) + 63) / 64;
-    int64_t want = heads > 0 ? slots / heads : 1;
-    if (want > chunks) want = chunks;
+    int64_t unit, want, most;  // tokens a segment is a multiple of, segments of a head, units of a segment
+    double least;              // where the walk of a segment and the carry over the segments cost the same
+    if (mfma) {
+        // as many workgroups as run at once (three a compute unit, two where N
+        // takes more of its LDS and registers), in whole 64-token chunks; the
+        // backward's sums over a segment hold 256 tokens
+        unit = 64;
+        want = (N > 64 ? 512 : 768) / (heads > 0 ? heads : 1);
+        most = backward ? 4 : INT64_MAX;
+        least = std::sqrt(L / 64.0 / 32.0);  // 2 us a chunk, 1 us for 16 segments
+    } else {
+        // three waves for each SIMD; the backward's sums hold 64 tokens
+        unit = 16;
+        want = 3072 / (heads > 0 ? heads : 1);
+        most = backward ? 4 : INT64_MAX;
+        least = std::fmax(2.0, std::sqrt(L / 6.0) / 16.0);  // 6 us for 16 tokens
+    }
+    const int64_t units = (static_cast<int64_t>(L) + unit - 1) / unit;
+    if (want > units) want = units;
     if (want < 1) want = 1;
-    int64_t per = (chunks + want - 1) / want;
-    if (backward && per > (mfma ? 4 : 1)) per = mfma ? 4 : 1;
+    int64_t per = (units + want - 1) / want;
+    if (per < static_cast<int64_t>(std::ceil(least)) && units > 1) per = static_cast<int64_t>(std::ceil(least));
+    if (per > most) per = most;
     if (per < 1) per = 1;
-    *seglen = static_cast<int>(per * 64);
-    *nseg = static_cast<int>(chunks > 0 ? (chunks + per - 1) / per : 1);
+    *seglen = static_cast<int>(per * unit);
+    *nseg = static_cast<int>(units > 0 ? (units + per - 1) / per : 1);
 }
 
 hipError_t launch_ssm_bwd_finish(const SsmBwdArgs &g, bool sweeps, hipStream_t stream) {

@@ -61,7 +61,7 @@ __global__ __launch_bounds__(64 * HB) void decays(SsmArgs a, int nch, float *out
         o[0] = hi;
         o[Q] = static_cast<float>(s - hi);
         o[2 * Q] = step;
-        o[3 * Q] = exp2f(static_cast<float>(all - s));
+        o[3 * Q] = __builtin_amdgcn_exp2f(static_cast<float>(all - s));
     }
 }
 

@@ -10,23 +10,27 @@
 //     y : k = B, v = u, q = C          dC : k = u, v = B, q = dy   (forwards)
 //     du: k = C, v = dy, q = B         dB : k = dy, v = C, q = u   (backwards)
 // so one kernel serves the four, with the state's two axes exchanged in dB
-// and dC. Lanes hold 64 values, each wave 16 keys of them in registers; a
-// token's reads of k and q are LDS broadcasts. The walk reads the state
-// before the token's own k_t v_t^T is added ("strict"); that last term is
-// (k_t . q_t) v_t and is added afterwards, which also leaves the strict part
-// to the gradient of the decay.
+// and dC. One wave holds a whole state of up to 128 keys and 64 values: lane
+// (g = lane / 16, c = lane % 16) has KPL = keys / 4 keys from g KPL on of
+// VPL = values / 16 values from c VPL on. A token's keys and queries are read
+// from LDS as 16-byte broadcasts that serve VPL products each; the sum over
+// the keys is in the lane's registers and then over the four lane rows. No
+// wave waits for another. The walk reads the state before the token's own
+// k_t v_t^T is added where the gradient of the decay needs it ("strict"; the
+// last term, (k_t . q_t) v_t, is added afterwards), else behind it.
 //
 // Vector bound: three fp32 operations for each token, key and value, one wave
-// instruction each four cycles. Segments of the sequence run side by side
-// (their states at the borders from a pass that does the update alone).
+// instruction each four cycles; tokens are staged T at a time, fetched to
+// registers while the T before are worked on. Segments of the sequence run
+// side by side (their states at the borders from a pass that does the update
+// alone).
 #include "ssm.hpp"
 #include "vec.hpp"
 
 namespace ttt {
 namespace {
 
-constexpr int T = 16;   // tokens staged at a time
-constexpr int KW = 16;  // keys of a wave
+constexpr int T = 16;  // tokens staged at a time
 
 enum Mode { STATES, STATES_REV, OUT_Y, OUT_DC, OUT_DU, OUT_DB };
 constexpr bool reversed(int m) { return m == STATES_REV || m == OUT_DU || m == OUT_DB; }
@@ -48,18 +52,17 @@ __device__ __forceinline__ float at(const SsmOperand &o, int b, int t, int h, in
     return io_traits<TIO>::load(static_cast<const TIO *>(o.p), b * o.sb + t * o.st + h * o.sh + i);
 }
 
-template <int MODE, typename TIO>
-__global__ __launch_bounds__(512) void walk(WalkArgs w) {
+template <int MODE, int KPL, int VPL, typename TIO>
+__global__ __launch_bounds__(64) void walk(WalkArgs w) {
     const SsmArgs &a = w.a;
-    extern __shared__ float lds[];
-    constexpr bool REV = reversed(MODE), EX = exchanged(MODE);
-    constexpr bool OUT = MODE >= OUT_Y;
+    constexpr bool REV = reversed(MODE), EX = exchanged(MODE), OUT = MODE >= OUT_Y;
+    constexpr bool STRICT = MODE == OUT_DC || MODE == OUT_DU;
+    constexpr int KP = 4 * KPL, VP = 16 * VPL, KN = T * KP / 64, VN = T * VP / 64;  // KN, VN: loads of T rows
+    __shared__ alignas(16) float ks[T][KP], qs[OUT ? T : 1][KP], vs[T][VP];
+    __shared__ float as[T], ds[T], dot[T];
     const int KD = EX ? a.P : a.N, VD = EX ? a.N : a.P;
-    const int nw = blockDim.x / 64, kp = nw * KW;
-    float *ks = lds, *qs = ks + T * kp, *vs = qs + (OUT ? T * kp : 0), *as = vs + T * 64, *ds = as + T;
-    float *yp = ds + T, *kq = yp + (OUT ? nw * T * 64 : 0);  // [nw][T][64], [nw][T]
-    const int lane = threadIdx.x % 64, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int vb = blockIdx.y, vi = vb * 64 + lane;
+    const int lane = threadIdx.x, g = lane / 16, c = lane % 16;
+    const int vb = blockIdx.y, v0 = vb * VP;
     const int seg = blockIdx.x % a.nseg;
     const int bh = blockIdx.x / a.nseg, b = bh / a.H, h = bh % a.H, gr = h / (a.H / a.G);
     const int n = a.lens ? max(0, min(a.lens[b], a.L)) : a.L;
@@ -67,122 +70,149 @@ __global__ __launch_bounds__(512) void walk(WalkArgs w) {
     const int t0 = static_cast<int>(s0 < a.L ? s0 : a.L);
     const int t1 = static_cast<int>(s0 + a.seglen < a.L ? s0 + a.seglen : a.L);
     const int te = max(t0, min(t1, n));  // tokens t0 .. te - 1 are walked
-    const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+    const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, Dh = a.D ? a.D[h] : 0.f;
     const int64_t NP = static_cast<int64_t>(a.N) * a.P;
+    // keys, queries and values: rows of x or dy (of the head), of B or C (of the group)
+    auto row = [&](const SsmOperand &o, int head) { return static_cast<const TIO *>(o.p) + b * o.sb + head * o.sh; };
+    const bool kx = MODE == OUT_DC, ky = MODE == OUT_DB, kc = MODE == STATES_REV || MODE == OUT_DU;
+    const SsmOperand &ok = kx ? a.x : ky ? w.dy : kc ? a.Cm : a.Bm;
+    const SsmOperand &oq = MODE == OUT_Y ? a.Cm : MODE == OUT_DU ? a.Bm : MODE == OUT_DC ? w.dy : a.x;
+    const SsmOperand &ov = MODE == OUT_DC ? a.Bm : MODE == OUT_DB ? a.Cm : REV ? w.dy : a.x;
+    const TIO *kp = row(ok, EX ? h : gr), *qp = row(oq, EX ? h : gr), *vp = row(ov, EX ? gr : h);
+    const TIO *dp = row(a.dt, h), *xp = row(a.x, h), *cp = row(a.Cm, gr);
     // element (key k, value v) of a state [N,P]
-    auto place = [&](int k) { return EX ? static_cast<int64_t>(vi) * a.P + k : static_cast<int64_t>(k) * a.P + vi; };
-    float st[KW];
+    auto place = [&](int k, int v) { return EX ? static_cast<int64_t>(v) * a.P + k : static_cast<int64_t>(k) * a.P + v; };
+    float st[KPL][VPL];
+    const float *init = w.init ? w.init + (w.init_stride ? w.init_stride * (static_cast<int64_t>(bh) * a.nseg + seg) : bh * NP) : nullptr;
 #pragma unroll
-    for (int i = 0; i < KW; ++i) {
-        const int k = wv * KW + i;
-        st[i] = 0.f;
-        if (w.init && k < KD && vi < VD)
-            st[i] = w.init[w.init_stride * (static_cast<int64_t>(bh) * a.nseg + seg) + (w.init_stride ? 0 : bh * NP) + place(k)];
-    }
+    for (int i = 0; i < KPL; ++i)
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const int k = g * KPL + i, v = v0 + c * VPL + j;
+            st[i][j] = init && k < KD && v < VD ? init[place(k, v)] : 0.f;
+        }
+    // the value whose sum over the keys this lane receives
+    const int vo = VPL == 4 ? 4 * c + g : VPL == 2 ? 2 * c + g / 2 : c;
+    const bool own = v0 + vo < VD && (VPL == 4 || (VPL == 2 ? g % 2 == 0 : g == 0));
     float total = 0.f;  // sum of D_t A over the segment
     const int chunks = (te - t0 + T - 1) / T;
+    float fk[KN], fq[OUT ? KN : 1], fv[VN], fd = 0.f;
+    auto fetch = [&](int ci) {  // rows and columns past the end are read from the last and not used
+        const int c0 = t0 + (REV ? chunks - 1 - ci : ci) * T, last = min(T, te - c0) - 1;
+        fd = io_traits<TIO>::load(dp, static_cast<int64_t>(c0 + min(lane, last)) * a.dt.st);
+#pragma unroll
+        for (int i = 0; i < KN; ++i) {
+            const int64_t at = c0 + min((64 * i + lane) / KP, last);
+            const int k = min((64 * i + lane) % KP, KD - 1);
+            fk[i] = io_traits<TIO>::load(kp, at * ok.st + k);
+            if (OUT) fq[i] = io_traits<TIO>::load(qp, at * oq.st + k);
+        }
+#pragma unroll
+        for (int i = 0; i < VN; ++i) {
+            const int64_t at = c0 + min((64 * i + lane) / VP, last);
+            fv[i] = io_traits<TIO>::load(vp, at * ov.st + min(v0 + (64 * i + lane) % VP, VD - 1));
+        }
+    };
+    if (chunks > 0) fetch(0);
     for (int ci = 0; ci < chunks; ++ci) {
         const int c0 = t0 + (REV ? chunks - 1 - ci : ci) * T, cn = min(T, te - c0);
-        __syncthreads();
-        if (threadIdx.x < T) {
-            float d = 0.f;
-            if (static_cast<int>(threadIdx.x) < cn) d = softplus_f(at<TIO>(a.dt, b, c0 + threadIdx.x, h, 0) + bias);
-            ds[threadIdx.x] = d;
-            as[threadIdx.x] = expf(d * A);
-        }
-        for (int i = threadIdx.x; i < T * kp; i += blockDim.x) {
-            const int t = i / kp, k = i % kp;
-            float kv = 0.f, qv = 0.f;
-            if (t < cn && k < KD) {
-                if (MODE == STATES || MODE == OUT_Y) kv = at<TIO>(a.Bm, b, c0 + t, gr, k);
-                if (MODE == STATES_REV || MODE == OUT_DU) kv = at<TIO>(a.Cm, b, c0 + t, gr, k);
-                if (MODE == OUT_DC) kv = at<TIO>(a.x, b, c0 + t, h, k);
-                if (MODE == OUT_DB) kv = at<TIO>(w.dy, b, c0 + t, h, k);
-                if (MODE == OUT_Y) qv = at<TIO>(a.Cm, b, c0 + t, gr, k);
-                if (MODE == OUT_DU) qv = at<TIO>(a.Bm, b, c0 + t, gr, k);
-                if (MODE == OUT_DC) qv = at<TIO>(w.dy, b, c0 + t, h, k);
-                if (MODE == OUT_DB) qv = at<TIO>(a.x, b, c0 + t, h, k);
-            }
-            ks[i] = kv;
-            if (OUT) qs[i] = qv;
-        }
-        for (int i = threadIdx.x; i < T * 64; i += blockDim.x) {
-            const int t = i / 64, v = vb * 64 + i % 64;
-            float x = 0.f;
-            if (t < cn && v < VD) {
-                if (MODE == STATES || MODE == OUT_Y) x = at<TIO>(a.x, b, c0 + t, h, v);
-                if (MODE == STATES_REV || MODE == OUT_DU) x = at<TIO>(w.dy, b, c0 + t, h, v);
-                if (MODE == OUT_DC) x = at<TIO>(a.Bm, b, c0 + t, gr, v);
-                if (MODE == OUT_DB) x = at<TIO>(a.Cm, b, c0 + t, gr, v);
-            }
-            vs[i] = x;
+        __syncthreads();  // the one wave has read what it staged before
+        if (lane < T) {
+            const float d = lane < cn ? softplus_f(fd + bias) : 0.f;
+            ds[lane] = d;
+            as[lane] = exp_f(fmaxf(d * A, -150.f));  // 0 below that
         }
         __syncthreads();
-        for (int i = 0; i < cn; ++i) {
-            const int t = REV ? cn - 1 - i : i;
+#pragma unroll
+        for (int i = 0; i < KN; ++i) {
+            const int t = (64 * i + lane) / KP, k = (64 * i + lane) % KP;
+            // u = D x wherever x enters as a key or a query
+            const float d = EX ? ds[t] : 1.f;
+            float kv = k < KD && t < cn ? fk[i] : 0.f, qv = OUT && k < KD ? fq[i] : 0.f;  // no key: adds nothing
+            if (MODE == OUT_DC) kv *= d;
+            if (MODE == OUT_DB) qv *= d;
+            ks[t][k] = kv;
+            if (OUT) qs[t][k] = qv;
+        }
+#pragma unroll
+        for (int i = 0; i < VN; ++i) {
+            const int t = (64 * i + lane) / VP, v = (64 * i + lane) % VP;
+            vs[t][v] = v0 + v < VD ? fv[i] : 0.f;
+        }
+        if (STRICT) {  // k . q of each token: four lanes a token
+            __syncthreads();
+            float p = 0.f;
+#pragma unroll 4
+            for (int k = lane % 4; k < KP; k += 4) p = fmaf(ks[lane / 4][k], qs[lane / 4][k], p);
+            p += __shfl_xor(p, 1, 64);
+            p += __shfl_xor(p, 2, 64);
+            if (lane % 4 == 0) dot[lane / 4] = p;
+        }
+        if (ci + 1 < chunks) fetch(ci + 1);
+        __syncthreads();
+        // all T, those past the end decay and add nothing: some tokens' LDS reads
+        // are under way while one is worked on
+#pragma unroll 2
+        for (int i = 0; i < T; ++i) {
+            const int t = REV ? T - 1 - i : i;
+            const bool in = t < cn;
             const float dcy = as[t], dv = ds[t];
             total = fmaf(dv, A, total);
-            // u = D x wherever x enters: as value, key or query
-            float v = vs[t * 64 + lane];
-            if (MODE == STATES || MODE == OUT_Y) v *= dv;
-            float o = 0.f, dot = 0.f;
+            float v[VPL], o[VPL] = {};
 #pragma unroll
-            for (int j = 0; j < KW; ++j) {
-                float k = ks[t * kp + wv * KW + j];
-                if (MODE == OUT_DC) k *= dv;
-                if (!REV) st[j] *= dcy;
-                if (OUT) {
-                    float q = qs[t * kp + wv * KW + j];
-                    if (MODE == OUT_DB) q *= dv;
-                    o = fmaf(q, st[j], o);
-                    dot = fmaf(q, k, dot);
+            for (int j = 0; j < VPL; ++j) {
+                v[j] = vs[t][c * VPL + j];
+                if (MODE == STATES || MODE == OUT_Y) v[j] *= dv;
+            }
+#pragma unroll
+            for (int k = 0; k < KPL; ++k) {
+                const float kk = ks[t][g * KPL + k], qq = OUT ? qs[t][g * KPL + k] : 0.f;
+#pragma unroll
+                for (int j = 0; j < VPL; ++j) {
+                    if (STRICT) {
+                        if (!REV) st[k][j] *= dcy;
+                        o[j] = fmaf(qq, st[k][j], o[j]);
+                        st[k][j] = fmaf(kk, v[j], st[k][j]);
+                    } else {
+                        st[k][j] = REV ? fmaf(kk, v[j], st[k][j]) : fmaf(kk, v[j], st[k][j] * dcy);
+                        if (OUT) o[j] = fmaf(qq, st[k][j], o[j]);
+                    }
+                    if (REV) st[k][j] *= dcy;
                 }
-                st[j] = fmaf(k, v, st[j]);
-                if (REV) st[j] *= dcy;
             }
             if (OUT) {
-                yp[(wv * T + t) * 64 + lane] = o;
-                if (lane == 0) kq[wv * T + t] = dot;
-            }
-        }
-        if (OUT) {
-            __syncthreads();
-            for (int t = wv; t < cn; t += nw) {
-                float strict = 0.f, dot = 0.f;
-                for (int i = 0; i < nw; ++i) {
-                    strict += yp[(i * T + t) * 64 + lane];
-                    dot += kq[i * T + t];
-                }
-                const float raw = vs[t * 64 + lane], dv = ds[t];
+                float out;
+                if constexpr (VPL == 4)
+                    out = tile::rows4_reduce4(o[0], o[1], o[2], o[3]);
+                else if constexpr (VPL == 2)
+                    out = tile::rows4_reduce2(o[0], o[1]);
+                else
+                    out = tile::rows4_sum(o[0]);
+                const float raw = vs[t][vo];
                 const int64_t tok = static_cast<int64_t>(bh) * a.L + c0 + t;
                 const int64_t blk = static_cast<int64_t>(vb) * a.B * a.H * a.L + tok;
-                const bool in = vi < VD;
-                if (MODE == OUT_Y) {
-                    const float y = fmaf(dot, dv * raw, strict) + (a.D ? a.D[h] * raw : 0.f);
-                    if (in)
-                        io_traits<TIO>::store(static_cast<TIO *>(const_cast<void *>(a.y.p)),
-                                              b * a.y.sb + (c0 + t) * a.y.st + h * a.y.sh + vi, y);
-                }
+                if (MODE == OUT_Y && own && in)
+                    io_traits<TIO>::store(static_cast<TIO *>(const_cast<void *>(a.y.p)),
+                                          b * a.y.sb + (c0 + t) * a.y.st + h * a.y.sh + v0 + vo, fmaf(Dh, raw, out));
+                if (MODE == OUT_DB && own && in) w.per_head[tok * a.N + v0 + vo] = out;
                 if (MODE == OUT_DC) {  // raw = B
-                    if (in) w.per_head[tok * a.N + vi] = fmaf(dot, raw, strict);
-                    const float s = tile::rows4_sum(tile::row16_sum(in ? at<TIO>(a.Cm, b, c0 + t, gr, vi) * strict : 0.f));
-                    if (lane == 0) w.row[blk] = s;
-                }
-                if (MODE == OUT_DB) {  // raw = C
-                    if (in) w.per_head[tok * a.N + vi] = fmaf(dot, raw, strict);
+                    const float cv = own && in ? io_traits<TIO>::load(cp, (c0 + t) * a.Cm.st + v0 + vo) : 0.f;
+                    if (own && in) w.per_head[tok * a.N + v0 + vo] = fmaf(dot[t], raw, out);
+                    const float s = tile::rows4_sum(tile::row16_sum(cv * out));
+                    if (lane == 0 && in) w.row[blk] = s;
                 }
                 if (MODE == OUT_DU) {  // raw = dy
-                    const float du = fmaf(dot, raw, strict);
-                    const float x = in ? at<TIO>(a.x, b, c0 + t, h, vi) : 0.f;
-                    if (in)
+                    const float du = fmaf(dot[t], raw, out);
+                    const float x = own && in ? io_traits<TIO>::load(xp, (c0 + t) * a.x.st + v0 + vo) : 0.f;
+                    if (own && in)
                         io_traits<TIO>::store(static_cast<TIO *>(const_cast<void *>(w.dx.p)),
-                                              b * w.dx.sb + (c0 + t) * w.dx.st + h * w.dx.sh + vi,
-                                              fmaf(dv, du, a.D ? a.D[h] * raw : 0.f));
-                    const float c = tile::rows4_sum(tile::row16_sum(x * strict));
+                                              b * w.dx.sb + (c0 + t) * w.dx.st + h * w.dx.sh + v0 + vo,
+                                              fmaf(dv, du, Dh * raw));
+                    const float s = tile::rows4_sum(tile::row16_sum(x * out));
                     const float xu = tile::rows4_sum(tile::row16_sum(x * du));
                     const float yx = tile::rows4_sum(tile::row16_sum(x * raw));
-                    if (lane == 0) {
-                        w.col[blk] = dv * c;
+                    if (lane == 0 && in) {
+                        w.col[blk] = dv * s;
                         w.xdu[blk] = xu;
                         w.dyx[blk] = yx;
                     }
@@ -191,41 +221,49 @@ __global__ __launch_bounds__(512) void walk(WalkArgs w) {
         }
     }
     // rows past the sequence's end are zeros
-    if (OUT) {
-        for (int t = te + wv; t < t1; t += nw) {
-            const int64_t tok = static_cast<int64_t>(bh) * a.L + t;
+    if (OUT && lane < VP && v0 + lane < VD) {
+        for (int t = te; t < t1; ++t) {
             const SsmOperand &o = MODE == OUT_Y ? a.y : w.dx;
-            if (vi < VD) {
-                if (MODE == OUT_Y || MODE == OUT_DU)
-                    io_traits<TIO>::store(static_cast<TIO *>(const_cast<void *>(o.p)), b * o.sb + t * o.st + h * o.sh + vi, 0.f);
-                else
-                    w.per_head[tok * a.N + vi] = 0.f;
-            }
+            if (MODE == OUT_Y || MODE == OUT_DU)
+                io_traits<TIO>::store(static_cast<TIO *>(const_cast<void *>(o.p)),
+                                      b * o.sb + static_cast<int64_t>(t) * o.st + h * o.sh + v0 + lane, 0.f);
+            else
+                w.per_head[(static_cast<int64_t>(bh) * a.L + t) * a.N + v0 + lane] = 0.f;
         }
     }
     if (w.fin) {
         float *f = w.fin + (static_cast<int64_t>(bh) * (OUT ? 1 : a.nseg) + (OUT ? 0 : seg)) * NP;
 #pragma unroll
-        for (int i = 0; i < KW; ++i) {
-            const int k = wv * KW + i;
-            if (k < KD && vi < VD) f[place(k)] = st[i];
-        }
+        for (int i = 0; i < KPL; ++i)
+#pragma unroll
+            for (int j = 0; j < VPL; ++j) {
+                const int k = g * KPL + i, v = v0 + c * VPL + j;
+                if (k < KD && v < VD) f[place(k, v)] = st[i][j];
+            }
     }
-    if (!OUT && vb == 0 && threadIdx.x == 0) w.decay[static_cast<int64_t>(bh) * a.nseg + seg] = expf(total);
+    if (!OUT && vb == 0 && lane == 0) w.decay[static_cast<int64_t>(bh) * a.nseg + seg] = exp_f(fmaxf(total, -150.f));
 }
 
-template <int MODE, typename TIO> hipError_t run_walk(const WalkArgs &w, hipStream_t s) {
+template <int MODE, int KPL, int VPL> hipError_t run_walk_kv(const WalkArgs &w, hipStream_t s) {
     const SsmArgs &a = w.a;
-    const int KD = exchanged(MODE) ? a.P : a.N, VD = exchanged(MODE) ? a.N : a.P;
-    const int nw = (KD + KW - 1) / KW, kp = nw * KW;
-    constexpr bool OUT = MODE >= OUT_Y;
-    const size_t floats = T * kp * (OUT ? 2 : 1) + T * 64 + 2 * T + (OUT ? nw * T * 64 + nw * T : 0);
-    hipLaunchKernelGGL((walk<MODE, TIO>), dim3(static_cast<unsigned>(a.B) * a.H * a.nseg, (VD + 63) / 64),
-                       dim3(64 * nw), floats * sizeof(float), s, w);
+    const int VD = exchanged(MODE) ? a.N : a.P;
+    const dim3 grid(static_cast<unsigned>(a.B) * a.H * a.nseg, (VD + 16 * VPL - 1) / (16 * VPL));
+    if (a.io == 1)
+        hipLaunchKernelGGL((walk<MODE, KPL, VPL, bf16_t>), grid, dim3(64), 0, s, w);
+    else
+        hipLaunchKernelGGL((walk<MODE, KPL, VPL, float>), grid, dim3(64), 0, s, w);
     return hipGetLastError();
 }
+template <int MODE, int KPL> hipError_t run_walk_k(const WalkArgs &w, hipStream_t s) {
+    const int v = ssm_lane_values(w.a.B, w.a.L, w.a.H, exchanged(MODE) ? w.a.N : w.a.P);
+    return v == 1 ? run_walk_kv<MODE, KPL, 1>(w, s) : v == 2 ? run_walk_kv<MODE, KPL, 2>(w, s) : run_walk_kv<MODE, KPL, 4>(w, s);
+}
 template <int MODE> hipError_t run_walk(const WalkArgs &w, hipStream_t s) {
-    return w.a.io == 1 ? run_walk<MODE, bf16_t>(w, s) : run_walk<MODE, float>(w, s);
+    const int KD = exchanged(MODE) ? w.a.P : w.a.N;
+    return KD <= 16   ? run_walk_k<MODE, 4>(w, s)
+           : KD <= 32 ? run_walk_k<MODE, 8>(w, s)
+           : KD <= 64 ? run_walk_k<MODE, 16>(w, s)
+                      : run_walk_k<MODE, 32>(w, s);
 }
 
 constexpr int CT = 256;
@@ -320,6 +358,16 @@ template <typename TIO> hipError_t step_t(const SsmArgs &a, hipStream_t s) {
 }
 
 }  // namespace
+
+// Values of a lane: as many as a row of LDS reads can serve, fewer where that
+// leaves SIMDs without a wave, as a lone wave is bound by its own instructions
+// (B = 3, H = 6, N = 24, P = 48, 517 tokens: outputs 16 us with 4 values a
+// lane, 9 us with 1). Goes by the sizes alone, as the workspace does.
+int ssm_lane_values(int B, int L, int H, int VD) {
+    const int64_t units = static_cast<int64_t>(B) * H * ((static_cast<int64_t>(L) + 63) / 64);
+    if (VD <= 16 || units * ((VD + 31) / 32) < 512) return 1;
+    return VD <= 32 || units * ((VD + 63) / 64) < 512 ? 2 : 4;
+}
 
 hipError_t launch_ssm_step(const SsmArgs &a, hipStream_t stream) {
     return a.io == 1 ? step_t<bf16_t>(a, stream) : step_t<float>(a, stream);

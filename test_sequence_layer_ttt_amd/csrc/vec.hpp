@@ -91,8 +91,28 @@ __device__ __forceinline__ void vec_load(const T *p, float (&x)[V]) {
 // quotient is then 0, which is the limit.
 __device__ __forceinline__ float sigmoid_f(float s) { return __builtin_amdgcn_rcpf(1.0f + __expf(-s)); }
 
-// log(1 + e^s) = max(s, 0) + log(1 + e^-|s|); the argument of log1p is in
-// (0, 1], so nothing overflows and small values keep their relative accuracy.
-__device__ __forceinline__ float softplus_f(float s) { return fmaxf(s, 0.f) + log1pf(expf(-fabsf(s))); }
+// e^x to about 1.5 steps of fp32: 2^t with t = x log2(e) rounded, times what
+// the rounding and the constant's own tail leave, 1 + r ln 2 (r is below 2^-20
+// for |x| < 10). Below -87 the result is 0 or a denormal and may be flushed.
+__device__ __forceinline__ float exp_f(float x) {
+    const float t = x * 1.44269504f;
+    const float r = fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;
+    return __builtin_amdgcn_exp2f(t) * fmaf(r, 0.693147181f, 1.0f);
+}
+
+// log(1 + e^s) = max(s, 0) + log(1 + e), e = e^-|s| in (0, 1], which is
+// 2 atanh(q), q = e / (2 + e) <= 1/3, by its series to q^15 (the next term is
+// below 2^-26): small results keep their relative accuracy, about 2 steps.
+__device__ __forceinline__ float softplus_f(float s) {
+    const float e = exp_f(-fminf(fabsf(s), 100.f));
+    const float q = e * __builtin_amdgcn_rcpf(2.0f + e), p = q * q;
+    float c = fmaf(p, 1.0f / 15, 1.0f / 13);
+    c = fmaf(p, c, 1.0f / 11);
+    c = fmaf(p, c, 1.0f / 9);
+    c = fmaf(p, c, 1.0f / 7);
+    c = fmaf(p, c, 1.0f / 5);
+    c = fmaf(p, c, 1.0f / 3);
+    return (s <= 0.f ? 0.f : s) + 2.0f * fmaf(q * p, c, q);  // NaN stays NaN
+}
 
 }  // namespace ttt
