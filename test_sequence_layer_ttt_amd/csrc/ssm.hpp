@@ -53,13 +53,17 @@ hipError_t launch_ssm_backward(const SsmBwdArgs &a, hipStream_t stream);
 
 // Parts of the launches above.
 //
-// The carry over segments, forward: S[0] = state, S[s+1] = decay[s] S[s] +
-// share[s]; on entry seg holds the shares [B,H,nseg,N,P], on return the state
-// before each segment. Reverse: S[nseg] = last, S[s] = decay[s] S[s+1] +
+// The carry over segments, forward: S[0] = first (or zeros), S[s+1] = decay[s]
+// S[s] + share[s]; on entry seg holds the shares [B,H,nseg,N,P], on return the
+// state before each segment. Reverse: S[nseg] = first, S[s] = decay[s] S[s+1] +
 // share[s]; on return seg[s] = S[s+1], the state's gradient behind segment s.
-// `out` (or null) receives what the walk ends with.
-hipError_t launch_ssm_carry(int BH, int NP, int nseg, bool reverse, const float *first, const float *decay,
-                            float *seg, float *out, hipStream_t stream);
+// `out` (or null) receives what the walk ends with. One or two in a launch.
+struct SsmCarry {
+    const float *first, *decay;
+    float *seg, *out;
+    int reverse;
+};
+hipError_t launch_ssm_carry(int BH, int NP, int nseg, const SsmCarry &c, const SsmCarry *other, hipStream_t stream);
 
 // What the backward's second half needs (ssm_bwd.hip).
 struct SsmBwdWs {

@@ -66,10 +66,10 @@ template <int W> __device__ __forceinline__ double sum_behind(double v) {
 
 // A workgroup takes a segment, a thread a token, a wave a 64-token chunk.
 template <typename TIO, bool SWEEPS>
-__global__ __launch_bounds__(NT) void decay_gradient(FinishArgs f) {
+__device__ __forceinline__ void decay_gradient(const FinishArgs &f, int block) {
     const SsmArgs &a = f.g.f;
     __shared__ double red[NT / 64], all_re[NT / 64], all_co[NT / 64], all_l[NT / 64];
-    const int seg = blockIdx.x % a.nseg, bh = blockIdx.x / a.nseg, b = bh / a.H, h = bh % a.H;
+    const int seg = block % a.nseg, bh = block / a.nseg, b = bh / a.H, h = bh % a.H;
     const int64_t NP = static_cast<int64_t>(a.N) * a.P;
     const int n = a.lens ? max(0, min(a.lens[b], a.L)) : a.L;
     const int64_t t = static_cast<int64_t>(seg) * a.seglen + threadIdx.x;
@@ -78,7 +78,17 @@ __global__ __launch_bounds__(NT) void decay_gradient(FinishArgs f) {
     const float *se = seg + 1 < a.nseg ? f.w.sf + (static_cast<int64_t>(bh) * a.nseg + seg + 1) * NP : f.w.last + bh * NP;
     const float *ge = f.w.sr + (static_cast<int64_t>(bh) * a.nseg + seg) * NP;
     double e = 0.0;
-    for (int64_t i = threadIdx.x; i < NP; i += NT) e += static_cast<double>(se[i]) * ge[i];
+    if (NP % 4 == 0) {  // the states lie at multiples of 16 bytes
+        const float4 *s4 = reinterpret_cast<const float4 *>(se), *g4 = reinterpret_cast<const float4 *>(ge);
+#pragma unroll 4
+        for (int i = threadIdx.x; i < static_cast<int>(NP / 4); i += NT) {
+            const float4 u = s4[i], v = g4[i];
+            e += (static_cast<double>(u.x) * v.x + static_cast<double>(u.y) * v.y) +
+                 (static_cast<double>(u.z) * v.z + static_cast<double>(u.w) * v.w);
+        }
+    } else {
+        for (int i = threadIdx.x; i < static_cast<int>(NP); i += NT) e += static_cast<double>(se[i]) * ge[i];
+    }
     e = block_sum(e, red);
     const int64_t tok = static_cast<int64_t>(bh) * a.L + t, blk = static_cast<int64_t>(a.B) * a.H * a.L;
     double xdu = 0.0, dyx = 0.0, z = 0.0, step = 0.0, q;
@@ -156,44 +166,57 @@ __global__ __launch_bounds__(NT) void decay_gradient(FinishArgs f) {
     }
 }
 
-// dB and dC from the heads' parts, a group's heads in order
-template <typename TIO>
-__global__ __launch_bounds__(NT) void head_sums(FinishArgs f) {
+// dB (second: dC) from the heads' parts, a group's heads in order: V adjacent
+// values of a thread, ROWS tokens of one sequence and group to a workgroup.
+constexpr int ROWS = 32;
+template <typename TIO, int V>
+__device__ __forceinline__ void head_sums(const FinishArgs &f, int64_t block, bool second) {
     const SsmArgs &a = f.g.f;
-    const int64_t LN = static_cast<int64_t>(a.L) * a.N, all = a.B * a.G * LN;
-    const int R = a.H / a.G;
-    const bool second = blockIdx.y;
+    const int runs = (a.L + ROWS - 1) / ROWS, R = a.H / a.G;
+    const int run = static_cast<int>(block % runs), bg = static_cast<int>(block / runs), b = bg / a.G, g = bg % a.G;
+    const int64_t LN = static_cast<int64_t>(a.L) * a.N;
+    const int t0 = run * ROWS, nv = a.N / V, count = min(ROWS, a.L - t0) * nv;
+    const float *part = (second ? f.w.dCh : f.w.dBh) + (static_cast<int64_t>(b) * a.H + static_cast<int64_t>(g) * R) * LN +
+                        static_cast<int64_t>(t0) * a.N;
     const SsmOperand &o = second ? f.g.dC : f.g.dB;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x; i < all;
-         i += static_cast<int64_t>(gridDim.x) * NT) {  // (b, g, t, n)
-        const int n = static_cast<int>(i % a.N), t = static_cast<int>(i / a.N % a.L);
-        const int g = static_cast<int>(i / LN % a.G), b = static_cast<int>(i / LN / a.G);
-        const float *p = (second ? f.w.dCh : f.w.dBh) +
-                         (static_cast<int64_t>(b) * a.H + static_cast<int64_t>(g) * R) * LN +
-                         static_cast<int64_t>(t) * a.N + n;
-        float s = 0.f;
-        for (int r = 0; r < R; ++r) s += p[r * LN];
-        io_traits<TIO>::store(static_cast<TIO *>(const_cast<void *>(o.p)), b * o.sb + t * o.st + g * o.sh + n, s);
+    TIO *out = static_cast<TIO *>(const_cast<void *>(o.p)) + b * o.sb + g * o.sh;
+    for (int i = threadIdx.x; i < count; i += NT) {
+        float s[V] = {};
+#pragma unroll 4
+        for (int r = 0; r < R; ++r) {
+            float v[V];
+            vec_load<float, V>(part + r * LN + static_cast<int64_t>(i) * V, v);
+#pragma unroll
+            for (int k = 0; k < V; ++k) s[k] += v[k];
+        }
+        const int t = i / nv;
+        VecIO<TIO, V>::store(out + (t0 + t) * o.st + (i - t * nv) * V, s);
     }
 }
 
-template <typename TIO> hipError_t finish(const FinishArgs &f, bool sweeps, hipStream_t s) {
+// One launch: workgroups of the decay's gradient, then those of dB, of dC.
+template <typename TIO, bool SWEEPS, int V>
+__global__ __launch_bounds__(NT) void last(FinishArgs f, int decays, int sums) {
+    const int64_t i = blockIdx.x;
+    if (i < decays)
+        decay_gradient<TIO, SWEEPS>(f, static_cast<int>(i));
+    else
+        head_sums<TIO, V>(f, (i - decays) % sums, i - decays >= sums);
+}
+
+template <typename TIO, bool SWEEPS> hipError_t finish(const FinishArgs &f, hipStream_t s) {
     const SsmArgs &a = f.g.f;
-    const int64_t heads = static_cast<int64_t>(a.B) * a.H;
+    const int decays = a.B * a.H * a.nseg, sums = a.B * a.G * ((a.L + ROWS - 1) / ROWS);
     hipError_t e = hipSuccess;
-    if (heads) {
-        const dim3 grid(static_cast<unsigned>(heads * a.nseg));
-        if (sweeps)
-            hipLaunchKernelGGL((decay_gradient<TIO, true>), grid, dim3(NT), 0, s, f);
+    if (decays + sums > 0) {
+        auto wide = [&](const SsmOperand &o) {
+            return (reinterpret_cast<uintptr_t>(o.p) & (4 * sizeof(TIO) - 1)) == 0 && o.sb % 4 == 0 && o.st % 4 == 0 && o.sh % 4 == 0;
+        };
+        const dim3 grid(static_cast<unsigned>(decays) + 2u * sums);
+        if (a.N % 4 == 0 && wide(f.g.dB) && wide(f.g.dC) && (reinterpret_cast<uintptr_t>(a.ws) & 15) == 0)
+            hipLaunchKernelGGL((last<TIO, SWEEPS, 4>), grid, dim3(NT), 0, s, f, decays, sums);
         else
-            hipLaunchKernelGGL((decay_gradient<TIO, false>), grid, dim3(NT), 0, s, f);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    const int64_t n = static_cast<int64_t>(a.B) * a.G * a.L * a.N;
-    if (n) {
-        const int64_t blocks = (n + NT - 1) / NT;
-        hipLaunchKernelGGL((head_sums<TIO>), dim3(static_cast<unsigned>(blocks < (1 << 20) ? blocks : 1 << 20), 2),
-                           dim3(NT), 0, s, f);
+            hipLaunchKernelGGL((last<TIO, SWEEPS, 1>), grid, dim3(NT), 0, s, f, decays, sums);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     ColumnSums c{f.w.part, 3 * static_cast<int64_t>(a.H), a.B * a.nseg};
@@ -255,8 +278,26 @@ void ssm_segments(int B, int L, int H, int P, int N, bool mfma, bool backward, i
         // backward's sums over a segment hold 256 tokens
         unit = 64;
         want = (N > 64 ? 512 : 768) / (heads > 0 ? heads : 1);
-        most = backward ? 4 : INT64_MAX;
+        most = INT64_MAX;
         least = std::sqrt(L / 64.0 / 32.0);  // 2 us a chunk, 1 us for 16 segments
+        if (backward) {
+            // two sweeps of workgroups of which 512 (256) run at once: the
+            // fewest chunk times over all rounds, a border's states counted as
+            // half a chunk (B=4 L=2048 H=12 N=64: sweeps 49 us with segments
+            // of four chunks, two rounds; 40 us with two, three rounds)
+            const int64_t chunks = (static_cast<int64_t>(L) + 63) / 64, slots = N > 64 ? 256 : 512;
+            double best = 0;
+            for (int64_t p = 1; p <= 4; ++p) {
+                const int64_t blocks = 2 * heads * ((chunks + p - 1) / p);
+                const double cost = static_cast<double>((blocks + slots - 1) / slots) * (p + 0.5);
+                if (p == 1 || cost < best) {
+                    best = cost;
+                    most = p;
+                }
+            }
+            want = 1;
+            least = 1;
+        }
     } else {
         // three waves for each SIMD; the backward's sums hold 64 tokens
         unit = 16;
@@ -277,7 +318,8 @@ void ssm_segments(int B, int L, int H, int P, int N, bool mfma, bool backward, i
 
 hipError_t launch_ssm_bwd_finish(const SsmBwdArgs &g, bool sweeps, hipStream_t stream) {
     const FinishArgs f{g, ssm_backward_ws(g.f)};
-    return g.f.io == 1 ? finish<bf16_t>(f, sweeps, stream) : finish<float>(f, sweeps, stream);
+    if (sweeps) return finish<bf16_t, true>(f, stream);  // bf16 alone
+    return g.f.io == 1 ? finish<bf16_t, false>(f, stream) : finish<float, false>(f, stream);
 }
 
 }  // namespace ttt

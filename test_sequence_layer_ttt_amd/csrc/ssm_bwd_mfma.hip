@@ -363,9 +363,8 @@ hipError_t launch_ssm_bwd_mfma(const SsmBwdArgs &g, hipStream_t stream) {
     hipError_t e;
     if ((e = launch_ssm_prep(a, s.prep, stream)) != hipSuccess) return e;
     if ((e = launch_ssm_shares_mfma(a, g.dy, s.prep, s.sf, s.sr, s.decay, stream)) != hipSuccess) return e;
-    if ((e = launch_ssm_carry(a.B * a.H, NP, a.nseg, false, a.state, s.decay, s.sf, s.last, stream)) != hipSuccess) return e;
-    if ((e = launch_ssm_carry(a.B * a.H, NP, a.nseg, true, g.dstate_out, s.decay, s.sr, g.dstate, stream)) != hipSuccess)
-        return e;
+    const SsmCarry cf{a.state, s.decay, s.sf, s.last, 0}, cr{g.dstate_out, s.decay, s.sr, g.dstate, 1};
+    if ((e = launch_ssm_carry(a.B * a.H, NP, a.nseg, cf, &cr, stream)) != hipSuccess) return e;
     const SweepArgs w{g, s};
     const dim3 grid(static_cast<unsigned>(a.B) * a.H * a.nseg, 2);
     if (a.N == 32)

@@ -333,9 +333,8 @@ hipError_t launch_ssm_mfma(const SsmArgs &a, hipStream_t stream) {
         float *decay = seg + static_cast<int64_t>(a.B) * a.H * a.nseg * NP;
         const MfmaArgs p{a, nullptr, 0, seg, decay, prep};
         if ((e = run(nullptr, &p, nullptr, stream)) != hipSuccess) return e;
-        if ((e = launch_ssm_carry(a.B * a.H, static_cast<int>(NP), a.nseg, false, a.state, decay, seg, a.state_out,
-                                  stream)) != hipSuccess)
-            return e;
+        const SsmCarry c{a.state, decay, seg, a.state_out, 0};
+        if ((e = launch_ssm_carry(a.B * a.H, static_cast<int>(NP), a.nseg, c, nullptr, stream)) != hipSuccess) return e;
         w.init = seg;
         w.init_stride = NP;
         w.fin = nullptr;

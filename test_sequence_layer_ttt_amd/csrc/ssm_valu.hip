@@ -268,31 +268,32 @@ template <int MODE> hipError_t run_walk(const WalkArgs &w, hipStream_t s) {
 
 constexpr int CT = 256;
 
-__global__ __launch_bounds__(CT) void carry(int NP, int nseg, int reverse, const float *first,
-                                            const float *decay, float *seg, float *out) {
+// blockIdx.z: one walk over a head's segments, or a second one
+__global__ __launch_bounds__(CT) void carry(int NP, int nseg, SsmCarry c0, SsmCarry c1) {
+    const SsmCarry &c = blockIdx.z ? c1 : c0;
     const int i = blockIdx.x * CT + threadIdx.x;
     const int64_t bh = blockIdx.y;
     if (i >= NP) return;
-    float *p = seg + bh * nseg * NP + i;
-    const float *d = decay + bh * nseg;
-    float s = first ? first[bh * NP + i] : 0.f;
+    float *p = c.seg + bh * nseg * NP + i;
+    const float *d = c.decay + bh * nseg;
+    float s = c.first ? c.first[bh * NP + i] : 0.f;
     constexpr int U = 16;  // segments in flight
     for (int k0 = 0; k0 < nseg; k0 += U) {
         float v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = min(k0 + u, nseg - 1);
-            v[u] = p[static_cast<int64_t>(reverse ? nseg - 1 - k : k) * NP];
+            v[u] = p[static_cast<int64_t>(c.reverse ? nseg - 1 - k : k) * NP];
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (k0 + u >= nseg) break;
-            const int k = reverse ? nseg - 1 - (k0 + u) : k0 + u;
+            const int k = c.reverse ? nseg - 1 - (k0 + u) : k0 + u;
             p[static_cast<int64_t>(k) * NP] = s;
             s = fmaf(d[k], s, v[u]);
         }
     }
-    if (out) out[bh * NP + i] = s;
+    if (c.out) c.out[bh * NP + i] = s;
 }
 
 // one token: the state is read, updated and written in place
@@ -373,14 +374,19 @@ hipError_t launch_ssm_step(const SsmArgs &a, hipStream_t stream) {
     return a.io == 1 ? step_t<bf16_t>(a, stream) : step_t<float>(a, stream);
 }
 
-hipError_t launch_ssm_carry(int BH, int NP, int nseg, bool reverse, const float *first, const float *decay,
-                            float *seg, float *out, hipStream_t stream) {
+hipError_t launch_ssm_carry(int BH, int NP, int nseg, const SsmCarry &c, const SsmCarry *other, hipStream_t stream) {
     for (int h0 = 0; h0 < BH; h0 += 65535) {  // a grid has at most 65535 rows
         const int nh = BH - h0 < 65535 ? BH - h0 : 65535;
-        const int64_t o = static_cast<int64_t>(h0) * NP;
-        hipLaunchKernelGGL(carry, dim3((NP + CT - 1) / CT, nh), dim3(CT), 0, stream, NP, nseg, reverse ? 1 : 0,
-                           first ? first + o : nullptr, decay + static_cast<int64_t>(h0) * nseg, seg + o * nseg,
-                           out ? out + o : nullptr);
+        auto from = [&](SsmCarry x) {
+            const int64_t o = static_cast<int64_t>(h0) * NP;
+            x.first = x.first ? x.first + o : nullptr;
+            x.out = x.out ? x.out + o : nullptr;
+            x.decay += static_cast<int64_t>(h0) * nseg;
+            x.seg += o * nseg;
+            return x;
+        };
+        hipLaunchKernelGGL(carry, dim3((NP + CT - 1) / CT, nh, other ? 2 : 1), dim3(CT), 0, stream, NP, nseg,
+                           from(c), from(other ? *other : c));
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -407,9 +413,8 @@ hipError_t launch_ssm_forward(const SsmArgs &a, hipStream_t stream) {
     if (a.nseg > 1) {
         float *seg = a.ws, *decay = a.ws + static_cast<int64_t>(a.B) * a.H * a.nseg * NP;
         if ((e = launch_ssm_states_valu(a, nullptr, seg, decay, stream)) != hipSuccess) return e;
-        if ((e = launch_ssm_carry(a.B * a.H, static_cast<int>(NP), a.nseg, false, a.state, decay, seg,
-                                  a.state_out, stream)) != hipSuccess)
-            return e;
+        const SsmCarry c{a.state, decay, seg, a.state_out, 0};
+        if ((e = launch_ssm_carry(a.B * a.H, static_cast<int>(NP), a.nseg, c, nullptr, stream)) != hipSuccess) return e;
         w.init = seg;
         w.init_stride = NP;
     } else {
@@ -427,13 +432,9 @@ hipError_t launch_ssm_backward(const SsmBwdArgs &g, hipStream_t stream) {
     if (!a.B) return launch_ssm_bwd_finish(g, false, stream);  // the sums over no tokens
     if (ssm_bwd_mfma_supported(g)) return launch_ssm_bwd_mfma(g, stream);
     if ((e = launch_ssm_states_valu(a, nullptr, s.sf, s.decay, stream)) != hipSuccess) return e;
-    if ((e = launch_ssm_carry(a.B * a.H, static_cast<int>(NP), a.nseg, false, a.state, s.decay, s.sf, s.last,
-                              stream)) != hipSuccess)
-        return e;
     if ((e = launch_ssm_states_valu(a, &g.dy, s.sr, s.decay, stream)) != hipSuccess) return e;
-    if ((e = launch_ssm_carry(a.B * a.H, static_cast<int>(NP), a.nseg, true, g.dstate_out, s.decay, s.sr,
-                              g.dstate, stream)) != hipSuccess)
-        return e;
+    const SsmCarry cf{a.state, s.decay, s.sf, s.last, 0}, cr{g.dstate_out, s.decay, s.sr, g.dstate, 1};
+    if ((e = launch_ssm_carry(a.B * a.H, static_cast<int>(NP), a.nseg, cf, &cr, stream)) != hipSuccess) return e;
     WalkArgs w{};
     w.a = a;
     w.dy = g.dy;
