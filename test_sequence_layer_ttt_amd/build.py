@@ -1,10 +1,12 @@
-"""Build libttt.so (HIP, gfx950) in-tree with hipcc."""
+"""Build libttt.so (HIP, gfx950) in-tree with hipcc, and _block.so, the native
+Python binding of the operators around the layer, with g++."""
 from __future__ import annotations
 
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -12,6 +14,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libttt.so")
+BINDING = os.path.join(PKG, "_block.so")
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -45,7 +48,23 @@ def build(verbose: bool = False, extra=()) -> str:
             objs = list(pool.map(compile_one, sources()))
         run([hipcc, "--offload-arch=gfx950", "-shared", "-o", LIB + ".tmp", *objs])
     os.replace(LIB + ".tmp", LIB)
+    run(binding_command())
+    os.replace(BINDING + ".tmp", BINDING)
     return LIB
+
+
+def binding_command():
+    """g++ on csrc/binding.cpp against torch and libttt.so (host code only)."""
+    import torch
+    from torch.utils import cpp_extension
+    inc = [a for p in cpp_extension.include_paths("cuda") for a in ("-isystem", p)]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", os.path.join(ROOT, "include"), *inc, "-I", sysconfig.get_paths()["include"],
+            os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp", "-L", PKG, "-l:libttt.so",
+            "-L", lib, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
 
 
 if __name__ == "__main__":
