@@ -40,6 +40,8 @@ struct SsmBwdArgs {
 // segments of the forward and of the backward
 void ssm_segments(int B, int L, int H, int P, int N, bool mfma, bool backward, int *nseg, int *seglen);
 bool ssm_mfma_supported(const SsmArgs &a);
+// how x, B, C, p and q lie in the MFMA kernels' tiles (ssm_tile.hpp, Fit)
+int ssm_fit(const SsmArgs &a, const SsmOperand &p, const SsmOperand &q);
 // Values (of VD features) that a lane of the walks holds, 16 lanes side by side:
 // their blocks are of 16 times as many.
 int ssm_lane_values(int B, int L, int H, int VD);

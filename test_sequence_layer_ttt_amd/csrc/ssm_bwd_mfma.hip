@@ -1,5 +1,5 @@
-// The state space scan's gradients on the matrix cores: bf16 features, P = 64,
-// N = 32, 64 or 128. With the notation of ssm_mfma.hip, P_ij = exp(l_i - l_j),
+// The state space scan's gradients on the matrix cores: bf16 features, P <= 64,
+// N <= 128. With the notation of ssm_mfma.hip, P_ij = exp(l_i - l_j),
 // G_ij = C_i . B_j, E_ij = dy_i . x_j, S the state before a chunk and R the
 // loss's gradient in the state behind it,
 //     dC_i = sum_{j <= i} P_ij E_ij D_j B_j + exp(l_i) S dy_i
@@ -61,13 +61,26 @@ __device__ __forceinline__ bf16x8 own_frag(const T *row, int kb, int g) {
     const uint2 b = *reinterpret_cast<const uint2 *>(row + 32 * kb + 16 + 4 * g);
     return __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, b.x, b.y));
 }
+// the same from a row of `cols` in global memory
+template <Fit FIT> __device__ __forceinline__ bf16x8 own_frag(const bf16_t *row, int kb, int g, int cols) {
+    if constexpr (FIT == FULL) return own_frag(row, kb, g);
+    if constexpr (FIT == WIDE) {
+        const int f0 = 32 * kb + 4 * g, f1 = f0 + 16;
+        const uint2 a = *reinterpret_cast<const uint2 *>(row + min(f0, cols - 4));
+        const uint2 b = *reinterpret_cast<const uint2 *>(row + min(f1, cols - 4));
+        return __builtin_bit_cast(bf16x8, make_uint4(f0 < cols ? a.x : 0u, f0 < cols ? a.y : 0u, f1 < cols ? b.x : 0u,
+                                                     f1 < cols ? b.y : 0u));
+    }
+    const uint2 a = four(row, 32 * kb + 4 * g, cols), b = four(row, 32 * kb + 16 + 4 * g, cols);
+    return __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, b.x, b.y));
+}
 // values of output tile t (16 t + 4 g .. + 3) from such fragments
 template <int KB> __device__ __forceinline__ f32x4 own_quad(const bf16x8 (&f)[KB], int t) {
     const uint4 r = __builtin_bit_cast(uint4, f[t / 2]);
     return t % 2 ? unpack4(make_uint2(r.z, r.w)) : unpack4(make_uint2(r.x, r.y));
 }
 
-template <int N, bool REV>
+template <int N, Fit FIT, bool REV>
 __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
     constexpr int NS = BwdSmem<N>::NS, KB = N / 32, TN = N / 16;
     constexpr int NT = N >= 64 ? N / 64 : 1, UT = N >= 64 ? 4 : 2;  // the wave's part of the state
@@ -91,11 +104,12 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
     const bf16_t *kp = static_cast<const bf16_t *>(ok.p) + b * ok.sb + gr * ok.sh;
     const bf16_t *qp = static_cast<const bf16_t *>(oq.p) + b * oq.sb + gr * oq.sh;
     bf16_t *dxp = static_cast<bf16_t *>(const_cast<void *>(ga.dx.p)) + b * ga.dx.sb + h * ga.dx.sh;
-    float *ph = (REV ? w.w.dBh : w.w.dCh) + static_cast<int64_t>(bh) * a.L * N;
+    const int Nn = FIT == FULL ? N : a.N, P = FIT == FULL ? 64 : a.P;  // the tile's rest is zeros
+    float *ph = (REV ? w.w.dBh : w.w.dCh) + static_cast<int64_t>(bh) * a.L * Nn;
     const int64_t tok0 = static_cast<int64_t>(bh) * a.L, inter = static_cast<int64_t>(a.B) * a.H * a.L;
     const int64_t tiles0 = static_cast<int64_t>(bh) * ((a.L + Q - 1) / Q);
     const int nt0 = N >= 64 ? NT * wv : wv % 2, u0 = N >= 64 ? 0 : 2 * (wv / 2);
-    constexpr int64_t NP = static_cast<int64_t>(N) * 64;
+    const int64_t NP = static_cast<int64_t>(Nn) * P;
 
     f32x4 st[NT][UT];
     const float *init = (REV ? w.w.sr : w.w.sf) + (static_cast<int64_t>(bh) * a.nseg + seg) * NP;
@@ -104,26 +118,33 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
 #pragma unroll
         for (int u = 0; u < UT; ++u)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) st[i][u][r] = init[(16 * (nt0 + i) + 4 * g + r) * 64 + 16 * (u0 + u) + c];
+            for (int r = 0; r < 4; ++r) {
+                const int k = 16 * (nt0 + i) + 4 * g + r, p = 16 * (u0 + u) + c;
+                st[i][u][r] = FIT == FULL || (k < Nn && p < P) ? init[k * P + p] : 0.f;
+            }
 
-    Stage<64> sv;
-    Stage<N> sk;
+    Stage<64, FIT> sv;
+    Stage<N, FIT> sk;
     bf16x8 zn[2], qn[KB];
     StageDecay sd;
+    auto fetch_own = [&](int t) {
+        const int64_t own = t + min(16 * wv + c, min(Q, te - t) - 1);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) zn[kb] = own_frag<FIT>(zp + own * oz.st, kb, g, P);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) qn[kb] = own_frag<FIT>(qp + own * oq.st, kb, g, Nn);
+    };
     auto fetch = [&](int t) {
         const int count = min(Q, te - t);
-        sv.fetch(vp + static_cast<int64_t>(t) * ov.st, ov.st, count);
-        sk.fetch(kp + static_cast<int64_t>(t) * ok.st, ok.st, count);
-        const int64_t own = t + min(16 * wv + c, count - 1);
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) zn[kb] = own_frag(zp + own * oz.st, kb, g);
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) qn[kb] = own_frag(qp + own * oq.st, kb, g);
+        sv.fetch(vp + static_cast<int64_t>(t) * ov.st, ov.st, count, P);
+        sk.fetch(kp + static_cast<int64_t>(t) * ok.st, ok.st, count, Nn);
+        if (FIT != SINGLE) fetch_own(t);
         sd.fetch(prep + static_cast<int64_t>(t / Q) * 4 * Q);
     };
-    auto put = [&](int buf) {
-        sv.put(sm.v[buf], XS);
-        sk.put(sm.k[buf], NS);
+    auto put = [&](int t, int buf) {
+        if (FIT == SINGLE) fetch_own(t);
+        sv.put(sm.v[buf], XS, P);
+        sk.put(sm.k[buf], NS, Nn);
         sd.put(sm.d[buf]);
     };
     auto share_state = [&]() {
@@ -143,7 +164,7 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
     auto chunk = [&](int i) { return t0 + (REV ? nc - 1 - i : i) * Q; };
     if (nc) {
         fetch(chunk(0));
-        put(0);
+        put(chunk(0), 0);
         share_state();
     }
     for (int ci = 0; ci < nc; ++ci) {
@@ -243,7 +264,14 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) acc[r] *= step;
                 }
-                *reinterpret_cast<f32x4 *>(ph + static_cast<int64_t>(t + o) * N + 16 * tn + 4 * g) = acc;
+                float *out = ph + static_cast<int64_t>(t + o) * Nn + 16 * tn + 4 * g;
+                if constexpr (FIT != SINGLE) {
+                    if (FIT == FULL || 16 * tn + 4 * g < Nn) *reinterpret_cast<f32x4 *>(out) = acc;
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * tn + 4 * g + r < Nn) out[r] = acc[r];
+                }
             }
         }
         bf16x8 vf[2][4];
@@ -272,7 +300,7 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
                     yx = fmaf(xv[r], dyv[r], yx);
                     out[r] = fmaf(step, acc[r], Dh * dyv[r]);
                 }
-                if (live) VecIO<bf16_t, 4>::store(dxp + static_cast<int64_t>(t + o) * ga.dx.st + 16 * u + 4 * g, out);
+                if (live) store4<FIT>(dxp + static_cast<int64_t>(t + o) * ga.dx.st, 16 * u + 4 * g, P, out);
             }
             yx = rows4_sum(yx);
         }
@@ -321,40 +349,44 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
                             st[i][u] = mfma32(kw[k], N >= 64 || wv < 2 ? vf[kb][u] : vf[kb][2 + u % 2], st[i][u]);
                 }
             }
-            put(buf ^ 1);
+            put(chunk(ci + 1), buf ^ 1);
             lds_barrier();  // every wave has read the state's parts
             share_state();
         }
     }
     // rows past the sequence's end are zeros
-    for (int t = te + static_cast<int>(threadIdx.x) / 8; t < t1; t += 32) {
-        const int e = threadIdx.x % 8;
-#pragma unroll
-        for (int i = 0; i < N / 8; ++i) ph[static_cast<int64_t>(t) * N + e * (N / 8) + i] = 0.f;
-        if constexpr (REV) *reinterpret_cast<uint4 *>(dxp + static_cast<int64_t>(t) * ga.dx.st + 8 * e) = make_uint4(0, 0, 0, 0);
+    const float zero[4] = {};
+    for (int t = te + static_cast<int>(threadIdx.x) / 16; t < t1; t += 16) {
+        const int e = threadIdx.x % 16;
+        for (int k = e; k < Nn; k += 16) ph[static_cast<int64_t>(t) * Nn + k] = 0.f;
+        if constexpr (REV) store4<FIT>(dxp + static_cast<int64_t>(t) * ga.dx.st, 4 * e, P, zero);
     }
 }
 
 // blockIdx.y: the sweep backwards (the longer one) first
-template <int N> __global__ __launch_bounds__(256, N == 128 ? 1 : 2) void sweeps(SweepArgs w) {
+template <int N, Fit FIT> __global__ __launch_bounds__(256, N == 128 ? 1 : 2) void sweeps(SweepArgs w) {
     __shared__ BwdSmem<N> sm;
     if (blockIdx.y == 0)
-        sweep<N, true>(w, sm);
+        sweep<N, FIT, true>(w, sm);
     else
-        sweep<N, false>(w, sm);
+        sweep<N, FIT, false>(w, sm);
 }
 
-bool wide(const SsmOperand &o) {  // rows of 16-byte accesses
-    return (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && o.sb % 8 == 0 && o.st % 8 == 0 && o.sh % 8 == 0;
+template <Fit FIT> hipError_t run(const SweepArgs &w, hipStream_t s) {
+    const SsmArgs &a = w.g.f;
+    const dim3 grid(static_cast<unsigned>(a.B) * a.H * a.nseg, 2);
+    if (a.N <= 32)
+        hipLaunchKernelGGL((sweeps<32, FIT>), grid, dim3(256), 0, s, w);
+    else if (a.N <= 64)
+        hipLaunchKernelGGL((sweeps<64, FIT>), grid, dim3(256), 0, s, w);
+    else
+        hipLaunchKernelGGL((sweeps<128, FIT>), grid, dim3(256), 0, s, w);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-bool ssm_bwd_mfma_supported(const SsmBwdArgs &g) {
-    const SsmArgs &a = g.f;
-    return a.io == 1 && a.P == 64 && (a.N == 32 || a.N == 64 || a.N == 128) && wide(a.x) && wide(a.Bm) &&
-           wide(a.Cm) && wide(g.dy) && wide(g.dx) && (reinterpret_cast<uintptr_t>(a.ws) & 15) == 0;
-}
+bool ssm_bwd_mfma_supported(const SsmBwdArgs &g) { return ssm_mfma_supported(g.f); }
 
 hipError_t launch_ssm_bwd_mfma(const SsmBwdArgs &g, hipStream_t stream) {
     const SsmArgs &a = g.f;
@@ -366,14 +398,8 @@ hipError_t launch_ssm_bwd_mfma(const SsmBwdArgs &g, hipStream_t stream) {
     const SsmCarry cf{a.state, s.decay, s.sf, s.last, 0}, cr{g.dstate_out, s.decay, s.sr, g.dstate, 1};
     if ((e = launch_ssm_carry(a.B * a.H, NP, a.nseg, cf, &cr, stream)) != hipSuccess) return e;
     const SweepArgs w{g, s};
-    const dim3 grid(static_cast<unsigned>(a.B) * a.H * a.nseg, 2);
-    if (a.N == 32)
-        hipLaunchKernelGGL((sweeps<32>), grid, dim3(256), 0, stream, w);
-    else if (a.N == 64)
-        hipLaunchKernelGGL((sweeps<64>), grid, dim3(256), 0, stream, w);
-    else
-        hipLaunchKernelGGL((sweeps<128>), grid, dim3(256), 0, stream, w);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const int fit = ssm_fit(a, g.dy, g.dx);
+    if ((e = fit == FULL ? run<FULL>(w, stream) : fit == WIDE ? run<WIDE>(w, stream) : run<SINGLE>(w, stream)) != hipSuccess) return e;
     return launch_ssm_bwd_finish(g, true, stream);
 }
 

@@ -1,5 +1,5 @@
-// The selective state space scan on the matrix cores: bf16 features, P = 64,
-// N = 32, 64 or 128 (formulas in ttt.h). A workgroup of four waves walks over
+// The selective state space scan on the matrix cores: bf16 features, P <= 64,
+// N <= 128 in tiles of 64 x 32, 64 or 128 (formulas in ttt.h). A workgroup of four waves walks over
 // the 64-token chunks of one head's segment. With l_i the sum of D_t A over
 // the chunk's tokens up to i and S the state before the chunk, a chunk is
 //     M_ij = (C_i . B_j) exp(l_i - l_j) D_j  for j <= i, else 0
@@ -52,7 +52,7 @@ struct MfmaArgs {
 // OUT: outputs and the state's update. Otherwise the segment's share of the
 // state alone, or (REV) of the state's gradient: a walk from the segment's end
 // over S <- exp(l_63) S + (C diag(exp(l)))^T dY, with C in Bm and dY in x.
-template <int N, bool OUT, bool REV, int PARTS>
+template <int N, Fit FIT, bool OUT, bool REV, int PARTS>
 __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
     constexpr int NS = Smem<N, OUT>::NS, KB = N / 32;
     constexpr int NT = N >= 64 ? N / 64 : 1;  // row tiles of the state in a wave
@@ -75,7 +75,8 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
     const bf16_t *cp = static_cast<const bf16_t *>(a.Cm.p) + b * a.Cm.sb + gr * a.Cm.sh;
     bf16_t *yp = static_cast<bf16_t *>(const_cast<void *>(a.y.p)) + b * a.y.sb + h * a.y.sh;
     const int nt0 = N >= 64 ? NT * wv : wv % 2, u0 = N >= 64 ? 0 : 2 * (wv / 2);
-    constexpr int64_t NP = static_cast<int64_t>(N) * 64;
+    const int Nn = FIT == FULL ? N : a.N, P = FIT == FULL ? 64 : a.P;  // the tile's rest is zeros
+    const int64_t NP = static_cast<int64_t>(Nn) * P;
 
     f32x4 st[NT][UT];
     const float *init = w.init ? w.init + (w.init_stride ? (static_cast<int64_t>(bh) * a.nseg + seg) * NP : bh * NP) : nullptr;
@@ -85,26 +86,33 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
         for (int u = 0; u < UT; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                st[i][u][r] = init ? init[(16 * (nt0 + i) + 4 * g + r) * 64 + 16 * (u0 + u) + c] : 0.f;
+            {
+                const int k = 16 * (nt0 + i) + 4 * g + r, p = 16 * (u0 + u) + c;
+                st[i][u][r] = init && (FIT == FULL || (k < Nn && p < P)) ? init[k * P + p] : 0.f;
+            }
 
-    Stage<64> sx;
-    Stage<N> sb;
+    Stage<64, FIT> sx;
+    Stage<N, FIT> sb;
     bf16x8 cf[KB], cn[KB];
     StageDecay sd;
+    auto fetch_own = [&](int t) {
+        if constexpr (OUT) {
+            const bf16_t *p = cp + static_cast<int64_t>(t + min(16 * wv + c, min(Q, te - t) - 1)) * a.Cm.st;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) cn[kb] = __builtin_bit_cast(bf16x8, eight<FIT>(p, 32 * kb + 8 * g, Nn));
+        }
+    };
     auto fetch = [&](int t) {  // the chunk at token t < te
         const int count = min(Q, te - t);
-        sx.fetch(xp + static_cast<int64_t>(t) * a.x.st, a.x.st, count);
-        sb.fetch(bp + static_cast<int64_t>(t) * a.Bm.st, a.Bm.st, count);
-        if constexpr (OUT) {
-            const bf16_t *p = cp + static_cast<int64_t>(t + min(16 * wv + c, count - 1)) * a.Cm.st + 8 * g;
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) cn[kb] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4 *>(p + 32 * kb));
-        }
+        sx.fetch(xp + static_cast<int64_t>(t) * a.x.st, a.x.st, count, P);
+        sb.fetch(bp + static_cast<int64_t>(t) * a.Bm.st, a.Bm.st, count, Nn);
+        if (FIT != SINGLE) fetch_own(t);
         sd.fetch(prep + static_cast<int64_t>(t / Q) * 4 * Q);
     };
-    auto put = [&](int buf) {
-        sx.put(sm.x[buf], XS);
-        sb.put(sm.b[buf], NS);
+    auto put = [&](int t, int buf) {
+        if (FIT == SINGLE) fetch_own(t);
+        sx.put(sm.x[buf], XS, P);
+        sb.put(sm.b[buf], NS, Nn);
         sd.put(sm.d[buf]);
     };
     auto share_state = [&]() {
@@ -119,7 +127,7 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
     auto chunk = [&](int i) { return t0 + (REV ? nc - 1 - i : i) * Q; };
     if (nc) {
         fetch(chunk(0));
-        put(0);
+        put(chunk(0), 0);
         if constexpr (OUT) share_state();
     }
     for (int ci = 0; ci < nc; ++ci) {
@@ -202,7 +210,7 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
                     vec_load<bf16_t, 4>(&x[i * XS + 16 * u + 4 * g], xv);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) o[r] = fmaf(Dh, xv[r], y[u][r]);
-                    VecIO<bf16_t, 4>::store(yp + static_cast<int64_t>(t + i) * a.y.st + 16 * u + 4 * g, o);
+                    store4<FIT>(yp + static_cast<int64_t>(t + i) * a.y.st, 16 * u + 4 * g, P, o);
                 }
             }
         }
@@ -247,7 +255,7 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
                         st[i][u] = mfma32(bw[k], N >= 64 || wv < 2 ? xf[kb][u] : xf[kb][2 + u % 2], st[i][u]);
             }
         }
-        if (more) put(buf ^ 1);
+        if (more) put(chunk(ci + 1), buf ^ 1);
         if constexpr (OUT) {
             if (more) {
                 lds_barrier();  // every wave has read the state's copy
@@ -256,8 +264,9 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
         }
     }
     if constexpr (OUT) {  // rows past the sequence's end are zeros
-        for (int t = te + threadIdx.x / 8; t < t1; t += 32)
-            *reinterpret_cast<uint4 *>(yp + static_cast<int64_t>(t) * a.y.st + threadIdx.x % 8 * 8) = make_uint4(0, 0, 0, 0);
+        const float zero[4] = {};
+        for (int t = te + threadIdx.x / 16; t < t1; t += 16)
+            store4<FIT>(yp + static_cast<int64_t>(t) * a.y.st, threadIdx.x % 16 * 4, P, zero);
     }
     if (w.fin) {
         float *f = w.fin + (static_cast<int64_t>(bh) * (OUT ? 1 : a.nseg) + (OUT ? 0 : seg)) * NP;
@@ -266,42 +275,49 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
 #pragma unroll
             for (int u = 0; u < UT; ++u)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) f[(16 * (nt0 + i) + 4 * g + r) * 64 + 16 * (u0 + u) + c] = st[i][u][r];
+                for (int r = 0; r < 4; ++r) {
+                    const int k = 16 * (nt0 + i) + 4 * g + r, p = 16 * (u0 + u) + c;
+                    if (FIT == FULL || (k < Nn && p < P)) f[k * P + p] = st[i][u][r];
+                }
     }
     if (!OUT && threadIdx.x == 0) w.decay[static_cast<int64_t>(bh) * a.nseg + seg] = exp2f(total);
 }
 
 // PARTS 3: the state goes on to the caller. 1: it does not (its exact value
 // comes from the shares) and only feeds the outputs, through a bf16 copy.
-template <int N, int PARTS>
+template <int N, Fit FIT, int PARTS>
 __global__ __launch_bounds__(256, N == 128 ? 2 : 3) void outputs(MfmaArgs w) {
     __shared__ Smem<N, true> sm;
-    chunks<N, true, false, PARTS>(w, sm);
+    chunks<N, FIT, true, false, PARTS>(w, sm);
 }
 // blockIdx.y: the states' shares, then those of their gradients
-template <int N>
+template <int N, Fit FIT>
 __global__ __launch_bounds__(256, N == 128 ? 2 : 3) void shares(MfmaArgs f, MfmaArgs r) {
     __shared__ Smem<N, false> sm;
     if (blockIdx.y == 0)
-        chunks<N, false, false, 3>(f, sm);
+        chunks<N, FIT, false, false, 3>(f, sm);
     else
-        chunks<N, false, true, 3>(r, sm);
+        chunks<N, FIT, false, true, 3>(r, sm);
 }
 
-template <int N> hipError_t run(const MfmaArgs *out, const MfmaArgs *f, const MfmaArgs *r, hipStream_t s) {
+template <int N, Fit FIT> hipError_t run(const MfmaArgs *out, const MfmaArgs *f, const MfmaArgs *r, hipStream_t s) {
     const SsmArgs &a = out ? out->a : f->a;
     const unsigned blocks = static_cast<unsigned>(a.B) * a.H * a.nseg;
     if (out && out->fin)
-        hipLaunchKernelGGL((outputs<N, 3>), dim3(blocks), dim3(256), 0, s, *out);
+        hipLaunchKernelGGL((outputs<N, FIT, 3>), dim3(blocks), dim3(256), 0, s, *out);
     else if (out)
-        hipLaunchKernelGGL((outputs<N, 1>), dim3(blocks), dim3(256), 0, s, *out);
+        hipLaunchKernelGGL((outputs<N, FIT, 1>), dim3(blocks), dim3(256), 0, s, *out);
     else
-        hipLaunchKernelGGL((shares<N>), dim3(blocks, r ? 2 : 1), dim3(256), 0, s, *f, r ? *r : *f);
+        hipLaunchKernelGGL((shares<N, FIT>), dim3(blocks, r ? 2 : 1), dim3(256), 0, s, *f, r ? *r : *f);
     return hipGetLastError();
 }
-hipError_t run(const MfmaArgs *out, const MfmaArgs *f, const MfmaArgs *r, hipStream_t s) {
+template <Fit FIT> hipError_t run(const MfmaArgs *out, const MfmaArgs *f, const MfmaArgs *r, hipStream_t s) {
     const int N = out ? out->a.N : f->a.N;
-    return N == 32 ? run<32>(out, f, r, s) : N == 64 ? run<64>(out, f, r, s) : run<128>(out, f, r, s);
+    return N <= 32 ? run<32, FIT>(out, f, r, s) : N <= 64 ? run<64, FIT>(out, f, r, s) : run<128, FIT>(out, f, r, s);
+}
+
+hipError_t run(int fit, const MfmaArgs *out, const MfmaArgs *f, const MfmaArgs *r, hipStream_t s) {
+    return fit == FULL ? run<FULL>(out, f, r, s) : fit == WIDE ? run<WIDE>(out, f, r, s) : run<SINGLE>(out, f, r, s);
 }
 
 bool wide(const SsmOperand &o) {  // rows of 16-byte accesses
@@ -310,9 +326,14 @@ bool wide(const SsmOperand &o) {  // rows of 16-byte accesses
 
 }  // namespace
 
+// FULL, WIDE or SINGLE for x, B, C and up to two more operands of P features
+int ssm_fit(const SsmArgs &a, const SsmOperand &p, const SsmOperand &q) {
+    if (a.P % 8 || a.N % 8 || !wide(a.x) || !wide(a.Bm) || !wide(a.Cm) || !wide(p) || !wide(q)) return SINGLE;
+    return a.P == 64 && (a.N == 32 || a.N == 64 || a.N == 128) ? FULL : WIDE;
+}
+
 bool ssm_mfma_supported(const SsmArgs &a) {
-    return a.io == 1 && a.P == 64 && (a.N == 32 || a.N == 64 || a.N == 128) && wide(a.x) && wide(a.Bm) &&
-           wide(a.Cm) && wide(a.y) && (reinterpret_cast<uintptr_t>(a.ws) & 15) == 0;
+    return a.io == 1 && a.P <= 64 && a.N <= 128 && (reinterpret_cast<uintptr_t>(a.ws) & 15) == 0;
 }
 
 hipError_t launch_ssm_shares_mfma(const SsmArgs &a, const SsmOperand &dy, const float *prep, float *sf, float *sr,
@@ -320,11 +341,12 @@ hipError_t launch_ssm_shares_mfma(const SsmArgs &a, const SsmOperand &dy, const 
     MfmaArgs f{a, nullptr, 0, sf, decay, prep}, r{a, nullptr, 0, sr, decay, prep};
     r.a.x = dy;
     r.a.Bm = a.Cm;
-    return run(nullptr, &f, &r, stream);
+    return run(ssm_fit(a, dy, dy), nullptr, &f, &r, stream);
 }
 
 hipError_t launch_ssm_mfma(const SsmArgs &a, hipStream_t stream) {
     const int64_t NP = static_cast<int64_t>(a.N) * a.P;
+    const int fit = ssm_fit(a, a.y, a.y);
     float *prep = a.ws, *seg = a.ws + ssm_prep_floats(a.B, a.L, a.H);
     hipError_t e;
     if ((e = launch_ssm_prep(a, prep, stream)) != hipSuccess) return e;
@@ -332,14 +354,14 @@ hipError_t launch_ssm_mfma(const SsmArgs &a, hipStream_t stream) {
     if (a.nseg > 1) {
         float *decay = seg + static_cast<int64_t>(a.B) * a.H * a.nseg * NP;
         const MfmaArgs p{a, nullptr, 0, seg, decay, prep};
-        if ((e = run(nullptr, &p, nullptr, stream)) != hipSuccess) return e;
+        if ((e = run(fit, nullptr, &p, nullptr, stream)) != hipSuccess) return e;
         const SsmCarry c{a.state, decay, seg, a.state_out, 0};
         if ((e = launch_ssm_carry(a.B * a.H, static_cast<int>(NP), a.nseg, c, nullptr, stream)) != hipSuccess) return e;
         w.init = seg;
         w.init_stride = NP;
         w.fin = nullptr;
     }
-    return run(&w, nullptr, nullptr, stream);
+    return run(fit, &w, nullptr, nullptr, stream);
 }
 
 }  // namespace ttt

@@ -84,27 +84,85 @@ __device__ __forceinline__ void weigh(bf16x8 f, f32x4 w0, f32x4 w1, bf16x8 (&out
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Feature f of a row of `cols`, 0 behind them (which are not read).
+__device__ __forceinline__ uint32_t feature_or_zero(const bf16_t *row, int f, int cols) {
+    const uint32_t v = row[min(f, cols - 1)];
+    return f < cols ? v : 0u;
+}
+__device__ __forceinline__ uint2 four(const bf16_t *row, int f, int cols) {
+    return make_uint2(feature_or_zero(row, f, cols) | feature_or_zero(row, f + 1, cols) << 16,
+                      feature_or_zero(row, f + 2, cols) | feature_or_zero(row, f + 3, cols) << 16);
+}
+// How a kernel's operands lie in its tiles of 64 x 32, 64 or 128 features.
+// FULL: they fill them, in 16-byte accesses. WIDE: multiples of eight features
+// in such accesses, the rest of a tile is zeros. SINGLE: any number in any
+// place, read one by one.
+enum Fit { SINGLE, WIDE, FULL };
+
+// Eight adjacent features of a row.
+template <Fit FIT> __device__ __forceinline__ uint4 eight(const bf16_t *row, int f, int cols) {
+    if constexpr (FIT == FULL) return *reinterpret_cast<const uint4 *>(row + f);
+    if constexpr (FIT == WIDE) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(row + min(f, cols - 8));
+        return f < cols ? v : make_uint4(0, 0, 0, 0);
+    }
+    const uint2 a = four(row, f, cols), b = four(row, f + 4, cols);
+    return make_uint4(a.x, a.y, b.x, b.y);
+}
+
+// Four adjacent features f .. f + 3 to a row of `cols`.
+template <Fit FIT> __device__ __forceinline__ void store4(bf16_t *row, int f, int cols, const float (&v)[4]) {
+    if constexpr (FIT != SINGLE) {
+        if (FIT == FULL || f < cols) VecIO<bf16_t, 4>::store(row + f, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (f + i < cols) row[f + i] = f32_to_bf16(v[i]);
+    }
+}
+
 // 64 rows of F features (F = 32, 64, 128) from global memory to LDS by 256
-// threads, 16 bytes each, through registers: fetched while the chunk before is
-// worked on. Rows at and past `count` are zeros and are not read.
-template <int F> struct Stage {
+// threads: 16 bytes each, through registers, fetched while the chunk before is
+// worked on; single elements are read when they are put (they would take four
+// times the registers). Rows at and past `count` are zeros and are
+// not read.
+template <int F, Fit FIT> struct Stage {
     static constexpr int PER = F / 8;         // accesses of a row
     static constexpr int ROWS = 256 / PER;    // rows of a pass
     static constexpr int NP = Q / ROWS;       // passes
-    uint4 r[NP];
-    __device__ __forceinline__ void fetch(const bf16_t *base, int64_t stride, int count) {
+    uint4 r[FIT == SINGLE ? 1 : NP];
+    const bf16_t *base;
+    int64_t stride;
+    int count;
+    __device__ __forceinline__ void fetch(const bf16_t *from, int64_t row_stride, int rows, int cols) {
+        if constexpr (FIT != SINGLE) {
+            const int row = threadIdx.x / PER, f = threadIdx.x % PER * 8;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int t = row + i * ROWS;
+                r[i] = make_uint4(0, 0, 0, 0);
+                if (t < rows && (FIT == FULL || f < cols)) r[i] = *reinterpret_cast<const uint4 *>(from + t * row_stride + f);
+            }
+        } else {
+            base = from;
+            stride = row_stride;
+            count = rows;
+        }
+    }
+    __device__ __forceinline__ void put(uint16_t *tile, int lds_stride, int cols) const {
         const int row = threadIdx.x / PER, f = threadIdx.x % PER * 8;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int t = row + i * ROWS;
-            r[i] = make_uint4(0, 0, 0, 0);
-            if (t < count) r[i] = *reinterpret_cast<const uint4 *>(base + t * stride + f);
+            uint4 v;
+            if constexpr (FIT != SINGLE) {
+                v = r[i];
+            } else {
+                v = make_uint4(0, 0, 0, 0);
+                if (t < count) v = eight<SINGLE>(base + t * stride, f, cols);
+            }
+            *reinterpret_cast<uint4 *>(tile + t * lds_stride + f) = v;
         }
-    }
-    __device__ __forceinline__ void put(uint16_t *tile, int lds_stride) const {
-        const int row = threadIdx.x / PER, f = threadIdx.x % PER * 8;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) *reinterpret_cast<uint4 *>(tile + (row + i * ROWS) * lds_stride + f) = r[i];
     }
 };
 
