@@ -8,7 +8,7 @@
 //             consecutive channels (16 bytes) and walks over T tokens with the
 //             last K - 1 of them in registers, so a token is read again only
 //             at the T-token borders (from the chip's caches). Rows are loaded
-//             U at a time before any of them is used.
+//             U at a time, while the U before are worked on.
 //  conv_step  one token: the state is read, shifted and written in place.
 //  conv_bwd   with g_t = dy_t act'(z_t):
 //                 dx_t = sum_k w_k g_{t+K-1-k},   dw_k = sum_t g_t x_{t-K+1+k}.
@@ -63,10 +63,17 @@ __global__ __launch_bounds__(NT) void conv_fwd(ConvArgs a, int tokens) {
     for (int k = 0; k < K - 1; ++k) {
         if (t0 < te) IO::unpack(full_row<K, V>(x, a.xt, st, a.C, t0 + k), win[k]);
     }
+    typename IO::Raw next[U];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) next[u] = IO::raw(x + static_cast<int64_t>(min(t + u, te - 1)) * a.xt);
+    };
+    if (t0 < te) fetch(t0);
     for (int t = t0; t < te; t += U) {
         typename IO::Raw r[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) r[u] = IO::raw(x + static_cast<int64_t>(min(t + u, te - 1)) * a.xt);
+        for (int u = 0; u < U; ++u) r[u] = next[u];
+        if (t + U < te) fetch(t + U);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             IO::unpack(r[u], win[K - 1]);
@@ -167,17 +174,24 @@ __global__ __launch_bounds__(NT) void conv_bwd(ConvBwdArgs g) {
         }
         const int t1 = min(t0 + BT, a.L);   // dx rows t0 .. t1 - 1 are this thread's
         const int te = t1 + K - 1;          // the walk
+        const int tn = min(te, n) - 1;      // the last row that is read
+        typename IO::Raw nx[U], nd[U];
+        auto fetch = [&](int t) {  // rows behind the last are read from it and count as zeros
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                nx[u] = IO::raw(x + static_cast<int64_t>(min(t + u, tn)) * a.xt);
+                nd[u] = IO::raw(dy + static_cast<int64_t>(min(t + u, tn)) * g.dyt);
+            }
+        };
+        if (t0 <= tn) fetch(t0);
         for (int tb = t0; tb < te; tb += U) {
             typename IO::Raw rx[U], rd[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                rx[u] = IO::zero();
-                rd[u] = IO::zero();
-                if (tb + u < n && tb + u < te) {
-                    rx[u] = IO::raw(x + static_cast<int64_t>(tb + u) * a.xt);
-                    rd[u] = IO::raw(dy + static_cast<int64_t>(tb + u) * g.dyt);
-                }
+                rx[u] = tb + u <= tn ? nx[u] : IO::zero();
+                rd[u] = tb + u <= tn ? nd[u] : IO::zero();
             }
+            if (tb + U <= tn) fetch(tb + U);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int t = tb + u;
