@@ -151,9 +151,9 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
             const float hi = d.hi[i];
             // decay from a token j of an earlier tile to the end of the tile
             // before this wave's, times D_j (one exp a lane), and from there
-            // to token i: neither is above 1
+            // to token i: with A < 0 neither is above 1
             const float edge = wv ? d.hi[16 * wv - 1] : 0.f;
-            sm.f[wv][lane] = fast_exp2(fminf(edge - d.hi[lane], 0.f)) * d.step[lane];
+            sm.f[wv][lane] = lane < 16 * wv ? fast_exp2(edge - d.hi[lane]) * d.step[lane] : 0.f;
             const float ef = fast_exp2(hi - edge);
             bf16x8 mf[2];
 #pragma unroll

@@ -205,3 +205,23 @@ def test_decay_that_forgets_everything_and_one_that_forgets_nothing(dt):
     d["dt"] = torch.full((B, L, H), -200.0, device="cuda").to(dt)
     gy, gs = _call(ttt.ttt_ssm_forward, d, state=d["state"])
     assert torch.equal(gs, d["state"])
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_states_that_grow(dt):
+    """A > 0: factors above 1 between tokens of one chunk, of two and of two segments."""
+    B, L, H, P, G, N = 1, 200, 2, 64, 1, 64
+    d, dy, dso, _ = _inputs(B, L, H, P, G, N, dt, 6)
+    d["A"] = torch.tensor([0.3, 1.0], device="cuda")
+    ref = {k: R.t64(v) for k, v in d.items()}
+    y, so = R.scan(**ref, lens=None)
+    my, ms = R.scan(**_absolute(ref), lens=None)
+    gy, gs = _call(ttt.ttt_ssm_forward, d, state=d["state"])
+    R.check(gy, y, "y", 4 * L + 128, my, 2.0 if dt is BF else 0.0)
+    R.check(gs, so, "state_out", 4 * L + 128, ms)
+    want = R.gradients(lambda **v: R.scan(**v, lens=None), ref, (R.t64(dy), R.t64(dso)))
+    mag = R.gradients(lambda **v: R.scan(**v, lens=None), _absolute(ref), (R.t64(dy).abs(), R.t64(dso).abs()))
+    got = _call(ttt.ttt_ssm_backward, d, dy, state=d["state"], dstate_out=dso)
+    for k, n in (("x", "dx"), ("Bm", "dB"), ("Cm", "dC")):
+        R.check(got[n], want[k], n, 4 * L + 128, mag[k], 2.0 if dt is BF else 0.0)
+    R.check(got["dstate"], want["state"], "dstate", 4 * L + 128, mag["state"])
