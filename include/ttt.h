@@ -549,7 +549,8 @@ int ttt_conv_backward_workspace(int B, int L, int C, int K, size_t *bytes);
  *   B*H*ceil(L/64) at most TTT_SSM_MAX_HEADS.
  *   x, y  : [B,L,H,P] io, strided (batch, token, head).
  *   dt    : [B,L,H] io, strided (batch, token, head).
- *   A     : [H] fp32 (decays where negative); D, dt_bias : [H] fp32 or NULL (0).
+ *   A     : [H] fp32 (a state decays where it is negative, grows where it is
+ *           not); D, dt_bias : [H] fp32 or NULL (0).
  *   B, C  : [B,L,G,N] io, strided (batch, token, group).
  *   state : [B,H,N,P] fp32 or NULL (zeros); state_out : the same or NULL; it
  *           may be exactly `state`.
@@ -564,7 +565,7 @@ int ttt_conv_backward_workspace(int B, int L, int C, int K, size_t *bytes);
  * vector arithmetic, token by token.
  */
 #define TTT_SSM_MAX_DIM 128
-#define TTT_SSM_MAX_HEADS (1 << 22)
+#define TTT_SSM_MAX_HEADS ((1 << 22) - 1)
 int ttt_ssm_forward(int B, int L, int H, int P, int G, int N, int io, const void *x,
                     const int64_t *x_strides, const void *dt, const int64_t *dt_strides,
                     const float *A, const void *Bm, const int64_t *B_strides, const void *Cm,

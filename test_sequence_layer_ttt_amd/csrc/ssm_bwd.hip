@@ -33,6 +33,7 @@ constexpr int NT = 256;
 struct FinishArgs {
     SsmBwdArgs g;
     SsmBwdWs w;
+    int rows;  // tokens of a workgroup of head_sums
 };
 
 __device__ __forceinline__ double block_sum(double v, double (&red)[NT / 64]) {
@@ -78,7 +79,7 @@ __device__ __forceinline__ void decay_gradient(const FinishArgs &f, int block) {
     const float *se = seg + 1 < a.nseg ? f.w.sf + (static_cast<int64_t>(bh) * a.nseg + seg + 1) * NP : f.w.last + bh * NP;
     const float *ge = f.w.sr + (static_cast<int64_t>(bh) * a.nseg + seg) * NP;
     double e = 0.0;
-    if (NP % 4 == 0) {  // the states lie at multiples of 16 bytes
+    if (NP % 4 == 0 && (reinterpret_cast<uintptr_t>(a.ws) & 15) == 0) {
         const float4 *s4 = reinterpret_cast<const float4 *>(se), *g4 = reinterpret_cast<const float4 *>(ge);
 #pragma unroll 4
         for (int i = threadIdx.x; i < static_cast<int>(NP / 4); i += NT) {
@@ -167,15 +168,14 @@ __device__ __forceinline__ void decay_gradient(const FinishArgs &f, int block) {
 }
 
 // dB (second: dC) from the heads' parts, a group's heads in order: V adjacent
-// values of a thread, ROWS tokens of one sequence and group to a workgroup.
-constexpr int ROWS = 32;
+// values of a thread, f.rows tokens of one sequence and group to a workgroup.
 template <typename TIO, int V>
 __device__ __forceinline__ void head_sums(const FinishArgs &f, int64_t block, bool second) {
     const SsmArgs &a = f.g.f;
-    const int runs = (a.L + ROWS - 1) / ROWS, R = a.H / a.G;
+    const int runs = (a.L + f.rows - 1) / f.rows, R = a.H / a.G;
     const int run = static_cast<int>(block % runs), bg = static_cast<int>(block / runs), b = bg / a.G, g = bg % a.G;
     const int64_t LN = static_cast<int64_t>(a.L) * a.N;
-    const int t0 = run * ROWS, nv = a.N / V, count = min(ROWS, a.L - t0) * nv;
+    const int t0 = run * f.rows, nv = a.N / V, count = min(f.rows, a.L - t0) * nv;
     const float *part = (second ? f.w.dCh : f.w.dBh) + (static_cast<int64_t>(b) * a.H + static_cast<int64_t>(g) * R) * LN +
                         static_cast<int64_t>(t0) * a.N;
     const SsmOperand &o = second ? f.g.dC : f.g.dB;
@@ -204,9 +204,11 @@ __global__ __launch_bounds__(NT) void last(FinishArgs f, int decays, int sums) {
         head_sums<TIO, V>(f, (i - decays) % sums, i - decays >= sums);
 }
 
-template <typename TIO, bool SWEEPS> hipError_t finish(const FinishArgs &f, hipStream_t s) {
+template <typename TIO, bool SWEEPS> hipError_t finish(FinishArgs f, hipStream_t s) {
     const SsmArgs &a = f.g.f;
-    const int decays = a.B * a.H * a.nseg, sums = a.B * a.G * ((a.L + ROWS - 1) / ROWS);
+    // a grid's threads are counted in 32 bits: at most 12 million workgroups here
+    f.rows = static_cast<int64_t>(a.B) * a.G * a.L < (1 << 24) ? 32 : 256;
+    const int decays = a.B * a.H * a.nseg, sums = a.B * a.G * ((a.L + f.rows - 1) / f.rows);
     hipError_t e = hipSuccess;
     if (decays + sums > 0) {
         auto wide = [&](const SsmOperand &o) {
@@ -317,7 +319,7 @@ void ssm_segments(int B, int L, int H, int P, int N, bool mfma, bool backward, i
 }
 
 hipError_t launch_ssm_bwd_finish(const SsmBwdArgs &g, bool sweeps, hipStream_t stream) {
-    const FinishArgs f{g, ssm_backward_ws(g.f)};
+    const FinishArgs f{g, ssm_backward_ws(g.f), 0};
     if (sweeps) return finish<bf16_t, true>(f, stream);  // bf16 alone
     return g.f.io == 1 ? finish<bf16_t, false>(f, stream) : finish<float, false>(f, stream);
 }

@@ -181,6 +181,15 @@ def test_workspace_of_a_segmented_prompt(lib):
     assert call(lib, "ttt_ssm_forward", SSM_F, B=1, L=8192, G=1, N=64, bytes=n.value - 1) == SHAPE
 
 
+def test_the_scan_refuses_grids_that_32_bits_do_not_count(lib):
+    """B*H*ceil(L/64) has to stay below 2^22."""
+    n = ctypes.c_size_t(0)
+    for q in (lib.ttt_ssm_forward_workspace, lib.ttt_ssm_backward_workspace):
+        assert q(1, 64 * ((1 << 22) - 1), 1, 1, 1, 1, ctypes.byref(n)) == _lib.TTT_OK
+        assert q(1, 64 << 22, 1, 1, 1, 1, ctypes.byref(n)) == SHAPE
+        assert q(1 << 11, 64, 1 << 11, 1, 1, 1, ctypes.byref(n)) == SHAPE
+
+
 def test_empty_batches_launch_nothing(lib):
     z = dict(B=0)
     assert call(lib, "ttt_conv_forward", CONV_F, **z) == _lib.TTT_OK
