@@ -417,7 +417,7 @@ int ttt_ssm_forward_workspace(int B, int L, int H, int P, int G, int N, size_t *
     // either path's segments: which one runs goes by the operands' addresses
     size_t most = 0;
     for (int mfma = 0; mfma < 2; ++mfma) {
-        ttt::ssm_segments(B, L, H, P, N, mfma != 0, false, &nseg, &seglen);
+        ttt::ssm_segments(B, L, H, N, mfma != 0, false, &nseg, &seglen);
         most = std::max(most, ttt::ssm_forward_floats(B, L, H, P, N, nseg));
     }
     *bytes = most * sizeof(float);
@@ -453,7 +453,7 @@ int ttt_ssm_forward(int B, int L, int H, int P, int G, int N, int io, const void
     if (!B) return ok();
     ttt::SsmArgs a{B, L, H, P, G, N, io, operand(vx), operand(vt), operand(vb), operand(vc), A, D, dt_bias, state,
                    lens, operand(vy), state_out, static_cast<float *>(workspace), 1, 64};
-    ttt::ssm_segments(B, L, H, P, N, ttt::ssm_mfma_supported(a), false, &a.nseg, &a.seglen);
+    ttt::ssm_segments(B, L, H, N, ttt::ssm_mfma_supported(a), false, &a.nseg, &a.seglen);
     return launched(ttt::launch_ssm_forward(a, stream));
 }
 
@@ -485,7 +485,7 @@ int ttt_ssm_backward_workspace(int B, int L, int H, int P, int G, int N, size_t 
     if ((st = ssm_common(B, L, H, P, G, N, TTT_F32)) || (st = ssm_plan(B, L, H, P, N))) return st;
     if (!bytes) return fail(TTT_E_NULL, "bytes is NULL");
     // the walks' segments, which are the shorter: the call takes them or the sweeps'
-    ttt::ssm_segments(B, L, H, P, N, false, true, &nseg, &seglen);
+    ttt::ssm_segments(B, L, H, N, false, true, &nseg, &seglen);
     *bytes = ttt::ssm_backward_floats(B, L, H, P, N, nseg) * sizeof(float);
     return ok();
 }
@@ -530,7 +530,7 @@ int ttt_ssm_backward(int B, int L, int H, int P, int G, int N, int io, const voi
                        state, lens, {nullptr, 0, 0, 0}, nullptr, static_cast<float *>(workspace), 1, 64},
                       operand(vdy), dstate_out, operand(vdx), operand(vdt), operand(vdb), operand(vdc), dA, dD,
                       ddt_bias, dstate};
-    ttt::ssm_segments(B, L, H, P, N, ttt::ssm_bwd_mfma_supported(g), true, &g.f.nseg, &g.f.seglen);
+    ttt::ssm_segments(B, L, H, N, ttt::ssm_bwd_mfma_supported(g), true, &g.f.nseg, &g.f.seglen);
     return launched(ttt::launch_ssm_backward(g, stream));
 }
 

@@ -38,7 +38,7 @@ struct SsmBwdArgs {
 };
 
 // segments of the forward and of the backward
-void ssm_segments(int B, int L, int H, int P, int N, bool mfma, bool backward, int *nseg, int *seglen);
+void ssm_segments(int B, int L, int H, int N, bool mfma, bool backward, int *nseg, int *seglen);
 bool ssm_mfma_supported(const SsmArgs &a);
 // how x, B, C, p and q lie in the MFMA kernels' tiles (ssm_tile.hpp, Fit)
 int ssm_fit(const SsmArgs &a, const SsmOperand &p, const SsmOperand &q);

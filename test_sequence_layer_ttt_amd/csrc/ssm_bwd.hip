@@ -11,7 +11,8 @@
 //    state before and behind the chunk, and W (row_i = sum_j W_ij, col_j =
 //    sum_i W_ij) what passes within it,
 //        q_t = base + sum_{j < t} co_j + sum_{i >= t} re_i + sum_{i >= t > j} W_ij,
-//    where base passes the whole chunk: q at its end less all of co, and
+//    where base passes the whole chunk: q at its end less all of co, or in
+//    the segment's first half q at its start less all of re, and
 //    taken as 0 where the chunk's decay is below 2^-24 and that difference is
 //    nothing but rounding. The last sum is known at the borders of the
 //    16-token tiles from the tiles' sums and runs within a tile.
@@ -65,6 +66,23 @@ template <int W> __device__ __forceinline__ double sum_behind(double v) {
     return v;
 }
 
+// a thread's part of the product of two arrays of n
+__device__ __forceinline__ double dot(const float *s, const float *g, int64_t n) {
+    double e = 0.0;
+    if (n % 4 == 0 && ((reinterpret_cast<uintptr_t>(s) | reinterpret_cast<uintptr_t>(g)) & 15) == 0) {
+        const float4 *s4 = reinterpret_cast<const float4 *>(s), *g4 = reinterpret_cast<const float4 *>(g);
+#pragma unroll 4
+        for (int i = threadIdx.x; i < static_cast<int>(n / 4); i += NT) {
+            const float4 u = s4[i], v = g4[i];
+            e += (static_cast<double>(u.x) * v.x + static_cast<double>(u.y) * v.y) +
+                 (static_cast<double>(u.z) * v.z + static_cast<double>(u.w) * v.w);
+        }
+    } else {
+        for (int i = threadIdx.x; i < static_cast<int>(n); i += NT) e += static_cast<double>(s[i]) * g[i];
+    }
+    return e;
+}
+
 // A workgroup takes a segment, a thread a token, a wave a 64-token chunk.
 template <typename TIO, bool SWEEPS>
 __device__ __forceinline__ void decay_gradient(const FinishArgs &f, int block) {
@@ -75,21 +93,12 @@ __device__ __forceinline__ void decay_gradient(const FinishArgs &f, int block) {
     const int n = a.lens ? max(0, min(a.lens[b], a.L)) : a.L;
     const int64_t t = static_cast<int64_t>(seg) * a.seglen + threadIdx.x;
     const bool mine = static_cast<int>(threadIdx.x) < a.seglen && t < a.L, live = mine && t < n;
-    // <state, its gradient> at the segment's end
+    // <state, its gradient> at the segment's end, and at its start where that is known
     const float *se = seg + 1 < a.nseg ? f.w.sf + (static_cast<int64_t>(bh) * a.nseg + seg + 1) * NP : f.w.last + bh * NP;
     const float *ge = f.w.sr + (static_cast<int64_t>(bh) * a.nseg + seg) * NP;
-    double e = 0.0;
-    if (NP % 4 == 0 && (reinterpret_cast<uintptr_t>(a.ws) & 15) == 0) {
-        const float4 *s4 = reinterpret_cast<const float4 *>(se), *g4 = reinterpret_cast<const float4 *>(ge);
-#pragma unroll 4
-        for (int i = threadIdx.x; i < static_cast<int>(NP / 4); i += NT) {
-            const float4 u = s4[i], v = g4[i];
-            e += (static_cast<double>(u.x) * v.x + static_cast<double>(u.y) * v.y) +
-                 (static_cast<double>(u.z) * v.z + static_cast<double>(u.w) * v.w);
-        }
-    } else {
-        for (int i = threadIdx.x; i < static_cast<int>(NP); i += NT) e += static_cast<double>(se[i]) * ge[i];
-    }
+    const bool both = SWEEPS && seg > 0;
+    double e = dot(se, ge, NP), e0 = 0.0;
+    if (both) e0 = block_sum(dot(f.w.sf + (static_cast<int64_t>(bh) * a.nseg + seg) * NP, ge - NP, NP), red);
     e = block_sum(e, red);
     const int64_t tok = static_cast<int64_t>(bh) * a.L + t, blk = static_cast<int64_t>(a.B) * a.H * a.L;
     double xdu = 0.0, dyx = 0.0, z = 0.0, step = 0.0, q;
@@ -131,10 +140,20 @@ __device__ __forceinline__ void decay_gradient(const FinishArgs &f, int block) {
         }
         __syncthreads();
         double base = 0.0;
-        for (int k = NT / 64 - 1; k >= wv; --k) {  // e: q behind chunk k
-            if (static_cast<int64_t>(seg) * a.seglen + 64 * k >= min(n, a.L) || 64 * k >= a.seglen) continue;
-            base = all_l[k] < -24.0 * 0.6931471805599453 ? 0.0 : e - all_co[k];
-            e = base + all_re[k];
+        const int held = static_cast<int>((max(0, min(a.seglen, n - seg * a.seglen)) + 63) / 64);  // chunks with tokens
+        auto passes = [&](int k, double q_border, double own) {
+            return all_l[k] < -24.0 * 0.6931471805599453 ? 0.0 : q_border - own;
+        };
+        if (both && wv < held / 2) {
+            for (int k = 0; k <= wv; ++k) {  // e0: q before chunk k
+                base = passes(k, e0, all_re[k]);
+                e0 = base + all_co[k];
+            }
+        } else {
+            for (int k = held - 1; k >= wv; --k) {  // e: q behind chunk k
+                base = passes(k, e, all_co[k]);
+                e = base + all_re[k];
+            }
         }
         q = base + co_before + re_behind + within;
     } else {
@@ -269,8 +288,7 @@ size_t ssm_forward_floats(int B, int L, int H, int P, int N, int nseg) {
            (nseg > 1 ? static_cast<size_t>(B) * H * nseg * (static_cast<size_t>(N) * P + 1) : 0);
 }
 
-void ssm_segments(int B, int L, int H, int P, int N, bool mfma, bool backward, int *nseg, int *seglen) {
-    (void)P;
+void ssm_segments(int B, int L, int H, int N, bool mfma, bool backward, int *nseg, int *seglen) {
     const int64_t heads = static_cast<int64_t>(B) * H;
     int64_t unit, want, most;  // tokens a segment is a multiple of, segments of a head, units of a segment
     double least;              // where the walk of a segment and the carry over the segments cost the same
@@ -283,20 +301,15 @@ void ssm_segments(int B, int L, int H, int P, int N, bool mfma, bool backward, i
         most = INT64_MAX;
         least = std::sqrt(L / 64.0 / 32.0);  // 2 us a chunk, 1 us for 16 segments
         if (backward) {
-            // two sweeps of workgroups of which 512 (256) run at once: the
-            // fewest chunk times over all rounds, a border's states counted as
-            // half a chunk (B=4 L=2048 H=12 N=64: sweeps 49 us with segments
-            // of four chunks, two rounds; 40 us with two, three rounds)
-            const int64_t chunks = (static_cast<int64_t>(L) + 63) / 64, slots = N > 64 ? 256 : 512;
-            double best = 0;
-            for (int64_t p = 1; p <= 4; ++p) {
-                const int64_t blocks = 2 * heads * ((chunks + p - 1) / p);
-                const double cost = static_cast<double>((blocks + slots - 1) / slots) * (p + 0.5);
-                if (p == 1 || cost < best) {
-                    best = cost;
-                    most = p;
-                }
-            }
+            // the longest segments, of four chunks at most, that leave the
+            // two sweeps 384 workgroups, 1.5 a compute unit: a border costs a
+            // share, a carry and its states' product. Whole backward, segments
+            // of 1 / 2 / 4 chunks, N = 64: 768 workgroups of four (B=4 L=2048
+            // H=12) 107 / 99 / 94 us, 384 (B=2) 69 / 60 / 59, 192 (B=1) 50 /
+            // 48 / 54; N = 128, B=4: 228 / 183 / 164
+            const int64_t chunks = (static_cast<int64_t>(L) + 63) / 64;
+            most = 4;
+            while (most > 1 && 2 * heads * ((chunks + most - 1) / most) < 384) --most;
             want = 1;
             least = 1;
         }

@@ -362,8 +362,8 @@ template <typename TIO> hipError_t step_t(const SsmArgs &a, hipStream_t s) {
 
 // Values of a lane: as many as a row of LDS reads can serve, fewer where that
 // leaves SIMDs without a wave, as a lone wave is bound by its own instructions
-// (B = 3, H = 6, N = 24, P = 48, 517 tokens: outputs 16 us with 4 values a
-// lane, 9 us with 1). Goes by the sizes alone, as the workspace does.
+// (B = 3, H = 6, N = 24, P = 48, 517 tokens: outputs 15.9 us with 4 values a
+// lane, 10.4 us with 1). Goes by the sizes alone, as the workspace does.
 int ssm_lane_values(int B, int L, int H, int VD) {
     const int64_t units = static_cast<int64_t>(B) * H * ((static_cast<int64_t>(L) + 63) / 64);
     if (VD <= 16 || units * ((VD + 31) / 32) < 512) return 1;
