@@ -281,6 +281,7 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
             for (int u = 0; u < 4; ++u) vf[kb][u] = tokens_frag(v, XS, kb, 16 * u, g, c);
         float yx = 0.f;
         if constexpr (REV) {
+            float out[4][4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -293,15 +294,15 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
                     if (2 * kb + 1 >= wv) acc = mfma32(vf[kb][u], mg[kb], acc);
                 }
                 const f32x4 xv = own_quad(z, u);
-                float dyv[4], out[4];
+                float dyv[4];
                 vec_load<bf16_t, 4>(&v[o * XS + 16 * u + 4 * g], dyv);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     yx = fmaf(xv[r], dyv[r], yx);
-                    out[r] = fmaf(step, acc[r], Dh * dyv[r]);
+                    out[u][r] = fmaf(step, acc[r], Dh * dyv[r]);
                 }
-                if (live) store4<FIT>(dxp + static_cast<int64_t>(t + o) * ga.dx.st, 16 * u + 4 * g, P, out);
             }
+            store_row<FIT>(dxp + static_cast<int64_t>(t + o) * ga.dx.st, live, out, g, P);
             yx = rows4_sum(yx);
         }
         strict = rows4_sum(strict);

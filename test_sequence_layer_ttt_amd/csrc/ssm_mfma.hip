@@ -203,16 +203,15 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
                     for (int u = 0; u < 4; ++u) y[u] = mfma32(xf[kb][u], mf[kb], y[u]);
                 }
             }
-            if (t + i < te) {
+            float o[4][4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    float xv[4], o[4];
-                    vec_load<bf16_t, 4>(&x[i * XS + 16 * u + 4 * g], xv);
+            for (int u = 0; u < 4; ++u) {
+                float xv[4];
+                vec_load<bf16_t, 4>(&x[i * XS + 16 * u + 4 * g], xv);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) o[r] = fmaf(Dh, xv[r], y[u][r]);
-                    store4<FIT>(yp + static_cast<int64_t>(t + i) * a.y.st, 16 * u + 4 * g, P, o);
-                }
+                for (int r = 0; r < 4; ++r) o[u][r] = fmaf(Dh, xv[r], y[u][r]);
             }
+            store_row<FIT>(yp + static_cast<int64_t>(t + i) * a.y.st, t + i < te, o, g, P);
         }
         const float whole = fast_exp2(d.total());
         total += d.total();
