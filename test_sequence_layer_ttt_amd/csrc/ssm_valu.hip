@@ -23,7 +23,11 @@
 // instruction each four cycles; tokens are staged T at a time, fetched to
 // registers while the T before are worked on. Segments of the sequence run
 // side by side (their states at the borders from a pass that does the update
-// alone).
+// alone). B=3 L=517 H=6 P=48 N=24 fp32: outputs 10.4 us, the update alone 8.4 us,
+// the carry between them 5.3 us; few waves, so latency of a token's chain.
+//
+// A single token (step) is bound by the state's bytes: 64 sequences of 32 heads
+// of 64 x 64 read and write 67 MB in 12.7 us, 5.3 TB/s.
 #include "ssm.hpp"
 #include "vec.hpp"
 
