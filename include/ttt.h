@@ -594,6 +594,10 @@ int ttt_ssm_step(int B, int H, int P, int G, int N, int io, const void *x,
  * workspace holds ttt_ssm_backward_workspace's bytes (states at segment
  * borders, dB and dC of each head in fp32, per-token sums); calls that share
  * one must not overlap.
+ * Numerics as the forward's: on the MFMA path dx takes the decayed products and
+ * the state's gradient as bf16 operands, dB and dC theirs in two bf16 parts,
+ * the decay's gradient comes from sums exact to fp32, and a value that is not
+ * finite reaches every gradient of its 64-token chunk.
  */
 int ttt_ssm_backward(int B, int L, int H, int P, int G, int N, int io, const void *x,
                      const int64_t *x_strides, const void *dt, const int64_t *dt_strides,
