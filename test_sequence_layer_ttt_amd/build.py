@@ -64,7 +64,7 @@ def binding_command():
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             "-I", os.path.join(ROOT, "include"), *inc, "-I", sysconfig.get_paths()["include"],
             os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp", "-L", PKG, "-l:libttt.so",
-            "-L", lib, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+            "-L", lib, "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
 
 
 if __name__ == "__main__":

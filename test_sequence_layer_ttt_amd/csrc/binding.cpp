@@ -1,14 +1,15 @@
 // Python binding of the operators around the layer (_block.so): argument
 // marshalling only. It checks type, shape, layout and device of torch tensors,
 // makes the outputs and workspaces that are not given, and calls libttt.so's
-// C ABI on the operands' device and its current stream. A call costs about
-// 3 us here; the same checks in Python through ctypes cost 9 to 13 us, more
-// than the kernels of a single token take. block.py documents the functions.
+// C ABI on the operands' device and its current stream. A call costs 3 to 4 us,
+// 2.7 of them the launch and 0.4 each output; the same checks in Python through
+// ctypes cost 9 to 13 us, more than the kernels of a single token take. block.py
+// documents the functions.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
@@ -121,8 +122,10 @@ struct Operand {
     Operand(const Operand &) = delete;
 };
 
+// straight from the caching allocator, on the device's current stream: past the
+// dispatcher, which takes as long again
 Tensor make(at::IntArrayRef shape, at::ScalarType dt, const Kind &k) {
-    return at::empty(shape, at::TensorOptions().dtype(dt).device(at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(k.index))));
+    return at::detail::empty_cuda(shape, dt, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(k.index)), std::nullopt);
 }
 // an output: as given (checked) or new
 Tensor output(PyObject *o, const char *name, at::IntArrayRef shape, at::ScalarType dt, const Kind &k, bool contiguous = true) {
