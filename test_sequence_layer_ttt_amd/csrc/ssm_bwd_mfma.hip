@@ -24,9 +24,10 @@
 //  * dB and dC of each head go out in fp32 and are summed over the group's
 //    heads in a fixed order by ssm_bwd.hip.
 // Bound by issue and latency of the many small products; two workgroups share
-// a compute unit (N = 128: one, its LDS holds the state's three parts). 51 us
-// for B=4 L=2048 H=12 N=64, both sweeps: about 800 vector instructions for a
-// wave and chunk, waves waiting 43 % of their time.
+// a compute unit (N = 128: one, its LDS holds the state's three parts). 43 us
+// for B=4 L=2048 H=12 N=64, both sweeps.
+#include <type_traits>
+
 #include "ssm_tile.hpp"
 
 namespace ttt {
@@ -185,128 +186,149 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
         const float hi = d.hi[o], lo = d.lo[o], step = d.step[o];
         const float reach = REV ? d.tail[o] : fast_exp2(hi);  // decay between the token and the state
         // products with the tokens before (behind) this lane's: rows m = 4 g + r
-        bf16x8 me[2][2], mg[2];
-        float strict = 0.f, diag = 0.f, apart[4] = {};
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            f32x4 pe[2], pg[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int mt = 2 * kb + k;
-                f32x4 G = {0.f, 0.f, 0.f, 0.f}, E = {0.f, 0.f, 0.f, 0.f};
-                if (REV ? mt >= wv : mt <= wv) {
-#pragma unroll
-                    for (int f = 0; f < KB; ++f) G = mfma32(own_frag(&kt[(16 * mt + c) * NS], f, g), q[f], G);
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) E = mfma32(own_frag(&v[(16 * mt + c) * XS], f, g), z[f], E);
-                    const int m = 16 * mt + 4 * g;
-                    const f32x4 hm = *reinterpret_cast<const f32x4 *>(&d.hi[m]);
-                    const f32x4 lm = *reinterpret_cast<const f32x4 *>(&d.lo[m]);
-                    const f32x4 sm4 = *reinterpret_cast<const f32x4 *>(&d.step[m]);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float l = (hm[r] - hi) + (lm[r] - lo);  // log2 P_{m,own} (REV), its negative else
-                        float p = fast_exp2(REV ? l : -l);
-                        if (!REV) p *= sm4[r];
-                        const bool in = REV ? m + r >= o : m + r <= o, same = m + r == o;
-                        const float e = in ? E[r] * p : 0.f;
-                        const float ge = in ? G[r] * e : 0.f;
-                        if (mt == wv) {
-                            strict += same ? 0.f : ge;
-                            diag += same ? ge : 0.f;
-                        } else {
-                            apart[mt] += ge;
-                        }
-                        E[r] = e;
-                        G[r] = in ? G[r] * p : 0.f;
-                    }
-                }
-                pe[k] = E;
-                pg[k] = G;
-            }
-            me[kb][0] = pack8(pe[0], pe[1]);
-            me[kb][1] = pack8(rest(pe[0]), rest(pe[1]));
-            if constexpr (REV) mg[kb] = pack8(pg[0], pg[1]);
-        }
-        // a column's (row's) sum over the tiles, and the tiles' sums over the wave
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-            strict += apart[mt];
-            if (REV && mt > wv) {
-                const float s = rows4_sum(row16_sum(apart[mt] * step));
-                if (lane == 0) w.w.tiles[(tiles0 + t / Q) * 8 + pair_index(mt, wv)] = s;
-            }
-        }
-        // over n: the state times z, its product with q, and the tokens' part
-        float qs = 0.f;
+        float strict = 0.f, diag = 0.f, qs = 0.f, yx = 0.f;
         const bool live = t + o < te;
+        bf16x8 vf[2][4];
+        // straight-line code for each wave, tiles side by side, so that no product
+        // waits at a branch or for the one before (51 -> 43 us)
+        auto pairs = [&](auto wave) {
+            constexpr int W = decltype(wave)::value;
+            bf16x8 me[2][2], mg[2];
+            float apart[4] = {};
 #pragma unroll
-        for (int tn = 0; tn < TN; ++tn) {
-            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            for (int kb = 0; kb < 2; ++kb) {
+                f32x4 pe[2], pg[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int mt = 2 * kb + k;
+                    f32x4 G = {0.f, 0.f, 0.f, 0.f}, E = {0.f, 0.f, 0.f, 0.f};
+                    if (REV ? mt >= W : mt <= W) {
+#pragma unroll
+                        for (int f = 0; f < KB; ++f) G = mfma32(own_frag(&kt[(16 * mt + c) * NS], f, g), q[f], G);
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) E = mfma32(own_frag(&v[(16 * mt + c) * XS], f, g), z[f], E);
+                        const int m = 16 * mt + 4 * g;
+                        const f32x4 hm = *reinterpret_cast<const f32x4 *>(&d.hi[m]);
+                        const f32x4 lm = *reinterpret_cast<const f32x4 *>(&d.lo[m]);
+                        const f32x4 sm4 = *reinterpret_cast<const f32x4 *>(&d.step[m]);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float l = (hm[r] - hi) + (lm[r] - lo);  // log2 P_{m,own} (REV), its negative else
+                            float p = fast_exp2(REV ? l : -l);
+                            if (!REV) p *= sm4[r];
+                            const bool in = mt != W || (REV ? 4 * g + r >= c : 4 * g + r <= c), same = 4 * g + r == c;
+                            const float e = in ? E[r] * p : 0.f;
+                            const float ge = in ? G[r] * e : 0.f;
+                            if (mt == W) {
+                                strict += same ? 0.f : ge;
+                                diag += same ? ge : 0.f;
+                            } else {
+                                apart[mt] += ge;
+                            }
+                            E[r] = e;
+                            G[r] = in ? G[r] * p : 0.f;
+                        }
+                    }
+                    pe[k] = E;
+                    pg[k] = G;
+                }
+                me[kb][0] = pack8(pe[0], pe[1]);
+                me[kb][1] = pack8(rest(pe[0]), rest(pe[1]));
+                if constexpr (REV) mg[kb] = pack8(pg[0], pg[1]);
+            }
+            // a column's (row's) sum over the tiles, and the tiles' sums over the wave
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+                strict += apart[mt];
+                if (REV && mt > W) {
+                    const float s = rows4_sum(row16_sum(apart[mt] * step));
+                    if (lane == 0) w.w.tiles[(tiles0 + t / Q) * 8 + pair_index(mt, W)] = s;
+                }
+            }
+            // over n: the state times z, its product with q, and the tokens' part
+            f32x4 acc[TN];
+#pragma unroll
+            for (int tn = 0; tn < TN; ++tn) acc[tn] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int part = 2; part >= 0; --part)
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb) acc = mfma32(tokens_frag(sm.s[part], NS, kb, 16 * tn, g, c), z[kb], acc);
-            const f32x4 qv = own_quad(q, tn);
+                for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                qs = fmaf(qv[r], acc[r], qs);
-                acc[r] *= reach;
+                    for (int tn = 0; tn < TN; ++tn)
+                        acc[tn] = mfma32(tokens_frag(sm.s[part], NS, kb, 16 * tn, g, c), z[kb], acc[tn]);
+#pragma unroll
+            for (int tn = 0; tn < TN; ++tn) {
+                const f32x4 qv = own_quad(q, tn);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    qs = fmaf(qv[r], acc[tn][r], qs);
+                    acc[tn][r] *= reach;
+                }
             }
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
-                if (REV ? 2 * kb + 1 >= wv : 2 * kb <= wv) {
-                    const bf16x8 f = tokens_frag(kt, NS, kb, 16 * tn, g, c);
-                    acc = mfma32(f, me[kb][1], acc);
-                    acc = mfma32(f, me[kb][0], acc);
+                if (REV ? 2 * kb + 1 >= W : 2 * kb <= W) {
+#pragma unroll
+                    for (int tn = 0; tn < TN; ++tn) {
+                        const bf16x8 f = tokens_frag(kt, NS, kb, 16 * tn, g, c);
+                        acc[tn] = mfma32(f, me[kb][1], acc[tn]);
+                        acc[tn] = mfma32(f, me[kb][0], acc[tn]);
+                    }
                 }
+            }
+            if (REV) {
+#pragma unroll
+                for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[tn][r] *= step;
             }
             if (live) {
-                if (REV) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[r] *= step;
-                }
-                float *out = ph + static_cast<int64_t>(t + o) * Nn + 16 * tn + 4 * g;
-                if constexpr (FIT != SINGLE) {
-                    if (FIT == FULL || 16 * tn + 4 * g < Nn) *reinterpret_cast<f32x4 *>(out) = acc;
-                } else {
+                for (int tn = 0; tn < TN; ++tn) {
+                    float *out = ph + static_cast<int64_t>(t + o) * Nn + 16 * tn + 4 * g;
+                    if constexpr (FIT != SINGLE) {
+                        if (FIT == FULL || 16 * tn + 4 * g < Nn) *reinterpret_cast<f32x4 *>(out) = acc[tn];
+                    } else {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (16 * tn + 4 * g + r < Nn) out[r] = acc[r];
-                }
-            }
-        }
-        bf16x8 vf[2][4];
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) vf[kb][u] = tokens_frag(v, XS, kb, 16 * u, g, c);
-        float yx = 0.f;
-        if constexpr (REV) {
-            float out[4][4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int f = 0; f < KB; ++f) acc = mfma32(own_frag(&sm.s[0][(16 * u + c) * NS], f, g), q[f], acc);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[r] *= reach;
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    if (2 * kb + 1 >= wv) acc = mfma32(vf[kb][u], mg[kb], acc);
-                }
-                const f32x4 xv = own_quad(z, u);
-                float dyv[4];
-                vec_load<bf16_t, 4>(&v[o * XS + 16 * u + 4 * g], dyv);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    yx = fmaf(xv[r], dyv[r], yx);
-                    out[u][r] = fmaf(step, acc[r], Dh * dyv[r]);
+                        for (int r = 0; r < 4; ++r)
+                            if (16 * tn + 4 * g + r < Nn) out[r] = acc[tn][r];
+                    }
                 }
             }
-            store_row<FIT>(dxp + static_cast<int64_t>(t + o) * ga.dx.st, live, out, g, P);
-            yx = rows4_sum(yx);
-        }
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) vf[kb][u] = tokens_frag(v, XS, kb, 16 * u, g, c);
+            if constexpr (REV) {
+                float out[4][4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int f = 0; f < KB; ++f) acc = mfma32(own_frag(&sm.s[0][(16 * u + c) * NS], f, g), q[f], acc);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[r] *= reach;
+#pragma unroll
+                    for (int kb = 0; kb < 2; ++kb) {
+                        if (2 * kb + 1 >= W) acc = mfma32(vf[kb][u], mg[kb], acc);
+                    }
+                    const f32x4 xv = own_quad(z, u);
+                    float dyv[4];
+                    vec_load<bf16_t, 4>(&v[o * XS + 16 * u + 4 * g], dyv);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        yx = fmaf(xv[r], dyv[r], yx);
+                        out[u][r] = fmaf(step, acc[r], Dh * dyv[r]);
+                    }
+                }
+                store_row<FIT>(dxp + static_cast<int64_t>(t + o) * ga.dx.st, live, out, g, P);
+                yx = rows4_sum(yx);
+            }
+        };
+        if (wv == 0) pairs(std::integral_constant<int, 0>());
+        else if (wv == 1) pairs(std::integral_constant<int, 1>());
+        else if (wv == 2) pairs(std::integral_constant<int, 2>());
+        else pairs(std::integral_constant<int, 3>());
         strict = rows4_sum(strict);
         diag = rows4_sum(diag);
         qs = reach * rows4_sum(qs);
@@ -335,7 +357,8 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
                 const int j0 = 32 * kb + 4 * g, j1 = j0 + 16;
                 f32x4 w0 = *reinterpret_cast<const f32x4 *>(REV ? &d.hi[j0] : &d.tail[j0]);
                 f32x4 w1 = *reinterpret_cast<const f32x4 *>(REV ? &d.hi[j1] : &d.tail[j1]);
-                const f32x4 p0 = *reinterpret_cast<const f32x4 *>(&d.step[j0]), p1 = *reinterpret_cast<const f32x4 *>(&d.step[j1]);
+                const f32x4 p0 = *reinterpret_cast<const f32x4 *>(&d.step[j0]);
+                const f32x4 p1 = *reinterpret_cast<const f32x4 *>(&d.step[j1]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     w0[r] = REV ? fast_exp2(w0[r]) : w0[r] * p0[r];
@@ -402,7 +425,8 @@ hipError_t launch_ssm_bwd_mfma(const SsmBwdArgs &g, hipStream_t stream) {
     if ((e = launch_ssm_carry(a.B * a.H, NP, a.nseg, cf, &cr, stream)) != hipSuccess) return e;
     const SweepArgs w{g, s};
     const int fit = ssm_fit(a, g.dy, g.dx);
-    if ((e = fit == FULL ? run<FULL>(w, stream) : fit == WIDE ? run<WIDE>(w, stream) : run<SINGLE>(w, stream)) != hipSuccess) return e;
+    e = fit == FULL ? run<FULL>(w, stream) : fit == WIDE ? run<WIDE>(w, stream) : run<SINGLE>(w, stream);
+    if (e != hipSuccess) return e;
     return launch_ssm_bwd_finish(g, true, stream);
 }
 
