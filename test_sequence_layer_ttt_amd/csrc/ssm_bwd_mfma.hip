@@ -346,12 +346,8 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
         }
         if (more) {  // the state before the next chunk
             const float whole = fast_exp2(d.total());
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int u = 0; u < UT; ++u)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) st[i][u][r] *= whole;
+            // the chunk's share is summed by itself, as those at the segments' borders are
+            f32x4 share[NT][UT] = {};
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
                 const int j0 = 32 * kb + 4 * g, j1 = j0 + 16;
@@ -369,12 +365,18 @@ __device__ __forceinline__ void sweep(const SweepArgs &w, BwdSmem<N> &sm) {
                     bf16x8 kw[3];
                     weigh<3>(tokens_frag(kt, NS, kb, 16 * (nt0 + i), g, c), w0, w1, kw);
 #pragma unroll
-                    for (int k = 0; k < 3; ++k)
+                    for (int k = 2; k >= 0; --k)
 #pragma unroll
                         for (int u = 0; u < UT; ++u)
-                            st[i][u] = mfma32(kw[k], N >= 64 || wv < 2 ? vf[kb][u] : vf[kb][2 + u % 2], st[i][u]);
+                            share[i][u] = mfma32(kw[k], N >= 64 || wv < 2 ? vf[kb][u] : vf[kb][2 + u % 2], share[i][u]);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int u = 0; u < UT; ++u)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) st[i][u][r] = fmaf(st[i][u][r], whole, share[i][u][r]);
             put(chunk(ci + 1), buf ^ 1);
             lds_barrier();  // every wave has read the state's parts
             share_state();

@@ -254,8 +254,9 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
             for (int i = 0; i < NT; ++i) {
                 bf16x8 bw[PARTS];
                 weigh<PARTS>(tokens_frag(bt, NS, kb, 16 * (nt0 + i), g, c), w0, w1, bw);
+                // the smallest part first: the state off 9.6e-8, 1.15e-7 the other way
 #pragma unroll
-                for (int k = 0; k < PARTS; ++k)
+                for (int k = PARTS - 1; k >= 0; --k)
 #pragma unroll
                     for (int u = 0; u < UT; ++u)
                         st[i][u] = mfma32(bw[k], N >= 64 || wv < 2 ? xf[kb][u] : xf[kb][2 + u % 2], st[i][u]);
