@@ -7,7 +7,8 @@ outputs and workspaces that are not given and calls libttt.so. Unlike the
 layer's own entry points, these take strided views (innermost dimension
 contiguous) and run on the operands' device, whichever device is current, on
 its current stream. A `stream` that is given is made the current one for the
-call, so what the call allocates belongs to it.
+call, so what the call allocates belongs to it. Autograd does not see these
+calls: gradients come from the _backward functions.
 """
 from __future__ import annotations
 
