@@ -317,7 +317,7 @@ void ssm_segments(int B, int L, int H, int N, bool mfma, bool backward, int *nse
     } else {
         // three waves for each SIMD; the backward's sums hold 64 tokens
         unit = 16;
-        want = 3072 / (heads > 0 ? heads : 1);
+        want = 3 * 1024 / (heads > 0 ? heads : 1);
         most = backward ? 4 : INT64_MAX;
         least = std::fmax(2.0, std::sqrt(L / 6.0) / 16.0);  // 6 us for 16 tokens
     }
