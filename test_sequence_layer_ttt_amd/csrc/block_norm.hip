@@ -27,11 +27,11 @@ template <class C, typename TIO, typename TR> struct RowIn {
 };
 
 template <int TPR, int VEC, int NV, typename TIO, typename TR>
-__global__ __launch_bounds__(NT) void block_norm_fwd(NormArgs a, int rows) {
+__global__ __launch_bounds__(threads(TPR)) void block_norm_fwd(NormArgs a, int rows) {
     typedef Cols<TPR, VEC, NV> C;
-    constexpr int E = C::E, RPW = NT / TPR;
+    constexpr int E = C::E, RPW = threads(TPR) / TPR;
     constexpr bool HOLD = E <= 16;  // parameters in registers over all rows
-    __shared__ float red[4][NT / 64];
+    __shared__ float red[4][threads(TPR) / 64];
     RowSum<TPR> sum{red};
     const C c{a.D, static_cast<int>(threadIdx.x % TPR)};
     const float inv_d = 1.0f / static_cast<float>(a.D);
@@ -106,10 +106,10 @@ __global__ __launch_bounds__(NT) void block_norm_fwd(NormArgs a, int rows) {
 
 template <int TPR, int VEC, int NV, typename TIO, typename TR> struct Fwd {
     static hipError_t run(const NormArgs &a, hipStream_t s) {
-        const int rows = a.B * a.L, rpw = NT / TPR;
+        const int rows = a.B * a.L, rpw = threads(TPR) / TPR;
         const int64_t need = (static_cast<int64_t>(rows) + rpw - 1) / rpw;
         const int grid = static_cast<int>(need < 2048 ? need : 2048);
-        hipLaunchKernelGGL((block_norm_fwd<TPR, VEC, NV, TIO, TR>), dim3(grid), dim3(NT), 0, s, a, rows);
+        hipLaunchKernelGGL((block_norm_fwd<TPR, VEC, NV, TIO, TR>), dim3(grid), dim3(threads(TPR)), 0, s, a, rows);
         return hipGetLastError();
     }
 };
@@ -118,7 +118,7 @@ template <int TPR, int VEC, int NV, typename TIO, typename TR> struct Fwd {
 
 hipError_t launch_block_norm(const NormArgs &a, hipStream_t stream) {
     const bool out = aligned(a.resid_out, 16) && aligned(a.x, 16);
-    return by_type<Fwd, 8>(a, a, out && vec_ok(a, 4), out && vec_ok(a, 8), stream);
+    return by_type<Fwd, 8, false>(a, a, out && vec_ok(a, 4), out && vec_ok(a, 8), stream);
 }
 
 }  // namespace ttt

@@ -10,21 +10,29 @@
 namespace ttt {
 namespace norm {
 
-constexpr int NT = 256;
+// threads of a workgroup: four rows of 64, or one row
+constexpr int threads(int tpr) { return tpr > 256 ? tpr : 256; }
 
 __device__ __forceinline__ float wave_sum(float v) { return tile::rows4_sum(tile::row16_sum(v)); }
 
 // Sum over the TPR threads of a row; every thread receives it. The LDS slots
 // alternate from call to call, so one barrier a call is enough.
 template <int TPR> struct RowSum {
-    float (*red)[NT / 64];
+    static constexpr int NW = threads(TPR) / 64;
+    float (*red)[NW];
     int slot = 0;
+    __device__ __forceinline__ static float over_waves(const float (&p)[NW]) {
+        float s = (p[0] + p[1]) + (p[2] + p[3]);
+#pragma unroll
+        for (int k = 4; k < NW; k += 4) s += (p[k] + p[k + 1]) + (p[k + 2] + p[k + 3]);
+        return s;
+    }
     __device__ __forceinline__ float operator()(float v) {
         v = wave_sum(v);
         if constexpr (TPR > 64) {
             red[slot][threadIdx.x / 64] = v;
             __syncthreads();
-            v = (red[slot][0] + red[slot][1]) + (red[slot][2] + red[slot][3]);
+            v = over_waves(red[slot]);
             slot ^= 1;
         }
         return v;
@@ -36,8 +44,8 @@ template <int TPR> struct RowSum {
             red[slot][threadIdx.x / 64] = u;
             red[slot + 2][threadIdx.x / 64] = v;
             __syncthreads();
-            u = (red[slot][0] + red[slot][1]) + (red[slot][2] + red[slot][3]);
-            v = (red[slot + 2][0] + red[slot + 2][1]) + (red[slot + 2][2] + red[slot + 2][3]);
+            u = over_waves(red[slot]);
+            v = over_waves(red[slot + 2]);
             slot ^= 1;
         }
     }
@@ -167,8 +175,13 @@ inline bool vec_ok(const NormArgs &a, int v) {
 
 // A row of up to 1024 columns is one wave's (no barriers), a longer one a
 // workgroup's. Columns go in vectors of 4 (8 for the forward's long rows),
-// one by one where the width or an address does not allow vectors.
-template <template <int, int, int, typename, typename> class K, int WIDE, typename TIO, typename TR, typename A>
+// one by one where the width or an address does not allow vectors. The backward
+// (BWD) holds seven values and up to six sums of a column in registers: eight
+// columns of a thread are two waves a SIMD, so its rows of 2049 to 4096 columns
+// go to 512 threads (D = 2560, 2457 rows: 47 us, 54 with sixteen columns; D =
+// 4096, 1536 rows: 42 and 44). Longer rows spill either way and stay with 256,
+// which may spill to more registers (D = 8192 with betas: 150 us, 169 with 512).
+template <template <int, int, int, typename, typename> class K, int WIDE, bool BWD, typename TIO, typename TR, typename A>
 hipError_t by_width(const A &a, int D, bool vec4, bool wide, hipStream_t s) {
     if (vec4 && D <= 1024) {
         if (D <= 256) return K<64, 4, 1, TIO, TR>::run(a, s);
@@ -178,7 +191,7 @@ hipError_t by_width(const A &a, int D, bool vec4, bool wide, hipStream_t s) {
     }
     if (wide && vec4) {
         if (D <= 2048) return K<256, WIDE, 8 / WIDE, TIO, TR>::run(a, s);
-        if (D <= 4096) return K<256, WIDE, 16 / WIDE, TIO, TR>::run(a, s);
+        if (D <= 4096) return K<BWD ? 512 : 256, WIDE, (BWD ? 8 : 16) / WIDE, TIO, TR>::run(a, s);
         return K<256, WIDE, 32 / WIDE, TIO, TR>::run(a, s);
     }
     if (D <= 256) return K<64, 1, 4, TIO, TR>::run(a, s);
@@ -187,11 +200,11 @@ hipError_t by_width(const A &a, int D, bool vec4, bool wide, hipStream_t s) {
     return K<256, 1, 32, TIO, TR>::run(a, s);
 }
 
-template <template <int, int, int, typename, typename> class K, int WIDE, typename A>
+template <template <int, int, int, typename, typename> class K, int WIDE, bool BWD, typename A>
 hipError_t by_type(const A &a, const NormArgs &f, bool vec4, bool wide, hipStream_t s) {
-    if (f.io == TTT_F32) return by_width<K, WIDE, float, float>(a, f.D, vec4, wide, s);
-    return f.rio == TTT_F32 ? by_width<K, WIDE, bf16_t, float>(a, f.D, vec4, wide, s)
-                            : by_width<K, WIDE, bf16_t, bf16_t>(a, f.D, vec4, wide, s);
+    if (f.io == TTT_F32) return by_width<K, WIDE, BWD, float, float>(a, f.D, vec4, wide, s);
+    return f.rio == TTT_F32 ? by_width<K, WIDE, BWD, bf16_t, float>(a, f.D, vec4, wide, s)
+                            : by_width<K, WIDE, BWD, bf16_t, bf16_t>(a, f.D, vec4, wide, s);
 }
 
 }  // namespace norm

@@ -23,10 +23,10 @@ enum { Q_POST_G, Q_PRE_G, Q_SCALE, Q_POST_B, Q_PRE_B, Q_GATE, Q_N };
 
 // BETAS: the betas' column sums too
 template <int TPR, int VEC, int NV, bool BETAS, typename TIO, typename TR>
-__global__ __launch_bounds__(NT, VEC * NV <= 12 ? 2 : 1) void block_norm_bwd(NormBwdArgs ga) {
+__global__ __launch_bounds__(threads(TPR), VEC * NV <= 12 ? 2 : 1) void block_norm_bwd(NormBwdArgs ga) {
     typedef Cols<TPR, VEC, NV> C;
-    constexpr int E = C::E, RPW = NT / TPR;
-    __shared__ float red[4][NT / 64];
+    constexpr int E = C::E, RPW = threads(TPR) / TPR;
+    __shared__ float red[4][threads(TPR) / 64];
     __shared__ float comb[RPW > 1 ? RPW * TPR * E : 1];
     const NormArgs &a = ga.f;
     RowSum<TPR> sum{red};
@@ -183,9 +183,9 @@ template <int TPR, int VEC, int NV, typename TIO, typename TR> struct Bwd {
         const int outer = a.gmode == TTT_GATE_SEQUENCE ? a.B : 1;
         const dim3 grid(static_cast<unsigned>(groups / outer), outer);
         if (g.dpost_beta || g.dpre_beta)
-            hipLaunchKernelGGL((block_norm_bwd<TPR, VEC, NV, true, TIO, TR>), grid, dim3(NT), 0, s, g);
+            hipLaunchKernelGGL((block_norm_bwd<TPR, VEC, NV, true, TIO, TR>), grid, dim3(threads(TPR)), 0, s, g);
         else
-            hipLaunchKernelGGL((block_norm_bwd<TPR, VEC, NV, false, TIO, TR>), grid, dim3(NT), 0, s, g);
+            hipLaunchKernelGGL((block_norm_bwd<TPR, VEC, NV, false, TIO, TR>), grid, dim3(threads(TPR)), 0, s, g);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         ColumnSums c{g.ws, static_cast<int64_t>(nq) * a.D, static_cast<int>(groups)};
@@ -204,7 +204,7 @@ template <int TPR, int VEC, int NV, typename TIO, typename TR> struct Bwd {
 }  // namespace
 
 void block_norm_backward_partials(int B, int L, int D, int gmode, int64_t *groups, int *quantities) {
-    const int rpw = D <= 1024 ? NT / 64 : 1;  // rows a workgroup holds at a time
+    const int rpw = D <= 1024 ? 4 : 1;  // rows a workgroup holds at a time
     const int64_t outer = gmode == TTT_GATE_SEQUENCE ? B : 1;
     const int64_t rows = gmode == TTT_GATE_SEQUENCE ? L : static_cast<int64_t>(B) * L;
     int64_t per = (rows + rpw - 1) / rpw;
@@ -219,7 +219,7 @@ hipError_t launch_block_norm_backward(const NormBwdArgs &g, hipStream_t stream) 
     const bool out = aligned(g.dresid_out, 16) && aligned(g.dx, 16) && aligned(g.dresid, 16) &&
                      aligned(g.dy, 16) && aligned(g.dgate, 16) && aligned(g.ws, 16);
     const bool v = out && vec_ok(g.f, 4);
-    return by_type<Bwd, 4>(g, g.f, v, v, stream);
+    return by_type<Bwd, 4, true>(g, g.f, v, v, stream);
 }
 
 }  // namespace ttt

@@ -51,6 +51,12 @@ CASES = [  # B, L, D, dtype, resid dtype, norm, gate dims, act, scale, betas, le
     (1, 3, 1280, F32, F32, "layer", 3, "none", False, True, None, 0),
     (1, 2, 4100, BF, BF, "rms", 1, "sigmoid", True, False, None, 0),
     (1, 3, 8192, BF, F32, "layer", 3, "tanh", True, True, None, 0),
+    (2, 300, 1000, BF, F32, "rms", 3, "silu", True, False, [300, 17], 0),
+    (1, 7, 1023, F32, F32, "layer", 1, "sigmoid", True, True, None, 0),
+    (2, 290, 2560, BF, BF, "layer", 2, "sigmoid", True, True, [0, 290], 8),
+    (1, 600, 4096, BF, F32, "rms", 1, "tanh", False, False, None, 0),
+    (1, 5, 4100, F32, F32, "layer", 3, "silu", True, True, None, 0),
+    (1, 520, 8192, BF, BF, "rms", 3, "sigmoid", True, False, None, 0),
     (1, 2, 5001, F32, F32, "layer", 0, "none", True, True, None, 0),
     (5, 400, 256, BF, BF, "rms", 2, "sigmoid", True, False, [400, 399, 0, 1, 17], 0),
 ]
