@@ -53,7 +53,7 @@ struct MfmaArgs {
     SsmArgs a;
     const float *init;    // [B,H,(nseg,)N,P]
     int64_t init_stride;  // as in WalkArgs
-    float *fin, *decay;
+    float *fin, *decay;   // decay: of each segment, from the shares forwards
     const float *prep;    // ssm_prep's chunks
 };
 
@@ -288,7 +288,9 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
                     if (FIT == FULL || (k < Nn && p < P)) f[k * P + p] = st[i][u][r];
                 }
     }
-    if (!OUT && threadIdx.x == 0) w.decay[static_cast<int64_t>(bh) * a.nseg + seg] = exp2f(total);
+    // by the walk forwards alone: the one from the end adds the chunks up in another
+    // order, which rounds differently, and runs at the same time
+    if (!OUT && !REV && threadIdx.x == 0) w.decay[static_cast<int64_t>(bh) * a.nseg + seg] = exp2f(total);
 }
 
 // PARTS 3: the state goes on to the caller. 1: it does not (its exact value
@@ -346,7 +348,7 @@ bool ssm_mfma_supported(const SsmArgs &a) {
 
 hipError_t launch_ssm_shares_mfma(const SsmArgs &a, const SsmOperand &dy, const float *prep, float *sf, float *sr,
                                   float *decay, hipStream_t stream) {
-    MfmaArgs f{a, nullptr, 0, sf, decay, prep}, r{a, nullptr, 0, sr, decay, prep};
+    MfmaArgs f{a, nullptr, 0, sf, decay, prep}, r{a, nullptr, 0, sr, nullptr, prep};
     r.a.x = dy;
     r.a.Bm = a.Cm;
     return run(ssm_fit(a, dy, dy), nullptr, &f, &r, stream);
