@@ -1,5 +1,5 @@
 """The state space scan where a workgroup walks several 64-token chunks, and
-where a lane of the vector walk holds two or four values.
+where a lane of the vector walk holds two or four values, against 64 bits.
 
 How a sequence is cut goes by the number of heads: with B H >= 192 the
 backward on the matrix cores takes segments of up to four chunks and the
@@ -7,10 +7,19 @@ forward of two or three, with B H >= 768 (512 for N > 64) the forward walks
 the whole sequence. The vector walk takes two values a lane for up to 32
 features and four for more where B H ceil(L / 64) >= 512.
 
+Bounds (block_ref.check). A term passes at most L decays, each a few half steps
+of fp32: 4 L + 128 of them at the sum of the terms' magnitudes. On the matrix
+cores a term of y takes at most two operands rounded to bf16 (the state's
+weighted rows and its copy, or the decayed products), one of dx one (the
+decayed products, or the state's gradient), dB and dC none that two parts do
+not hold: two half steps of bf16 at the same sum. The decay's gradient is a
+difference of sums that decay_sums gives, each term as above in fp32.
 """
 import pytest
 import torch
 
+from tests import block_ref as R
+from tests import scan_ref as S
 from test_sequence_layer_ttt_amd import ttt
 
 pytestmark = pytest.mark.gpu
@@ -36,6 +45,17 @@ def _inputs(case, seed, positive=False):
         dy, dso = dy.abs(), dso.abs()
     d = {k: t.cuda() for k, t in d.items()}
     return d, dy.cuda(), dso.cuda(), None if lens is None else torch.tensor(lens, dtype=torch.int32).cuda()
+
+
+def _poison(d, dy, n):
+    if n is not None:
+        for b, k in enumerate(n.tolist()):
+            for t in (d["x"], d["dt"], d["Bm"], d["Cm"], dy):
+                t[b, k:] = float("nan")
+
+
+def _check(got, ref, name, ops, mag, roundings=0.0):
+    R.check(got, ref.cpu(), name, ops, mag.cpu(), roundings)
 
 
 def _args(d):
@@ -64,6 +84,41 @@ LANES = [  # the vector walk
     (16, 70, 16, 100, 1, 20, BF, [70, 33] * 8, "reset"),
     (16, 130, 16, 64, 1, 64, F32, None, "grow"),
 ]
+
+
+@pytest.mark.parametrize("case", CHUNKS + WHOLE + LANES, ids=str)
+def test_forward(case):
+    d, dy, _, n = _inputs(case, 1)
+    ref = {k: S.t64(v) for k, v in d.items()}
+    want, mag = S.scan(ref, n), S.scan(S.absolute(ref), n)
+    _poison(d, dy, n)
+    y, so = ttt.ttt_ssm_forward(*_args(d), d["D"], d["dt_bias"], d["state"], n)
+    ops = 4 * case[1] + 128
+    _check(y, want["y"], "y", ops, mag["y"], 2.0 if case[6] is BF and case[3] <= 64 else 0.0)
+    _check(so, want["state_out"], "state_out", ops, mag["state_out"])
+
+
+@pytest.mark.parametrize("positive", [False, True], ids=["signed", "positive"])
+@pytest.mark.parametrize("case", CHUNKS + LANES, ids=str)
+def test_backward(case, positive):
+    """Positive operands: no sum cancels, so that the bounds of the decay's
+    gradient are close to it."""
+    d, dy, dso, n = _inputs(case, 2, positive)
+    ref, rdy, rso = {k: S.t64(v) for k, v in d.items()}, S.t64(dy), S.t64(dso)
+    want = S.scan(ref, n, rdy, rso)
+    mag = S.scan(S.absolute(ref), n, rdy.abs(), rso.abs())
+    _poison(d, dy, n)
+    got = ttt.ttt_ssm_backward(*_args(d), dy, d["D"], d["dt_bias"], d["state"], dso, n)
+    ops, rounded = 4 * case[1] + 128, 2.0 if case[6] is BF and case[3] <= 64 else 0.0
+    for k in ("dx", "dB", "dC"):
+        _check(got[k], want[k], k, ops, mag[k], rounded)
+    _check(got["dstate"], want["dstate"], "dstate", ops, mag["dstate"])
+    _check(got["dD"], want["dD"], "dD", ops, mag["dD"])
+    q = S.decay_sums(mag, ops)
+    mdt = (q * ref["A"].abs() + mag["xdu"]) * mag["sig"]
+    _check(got["ddt"], want["ddt"], "ddt", ops, mdt)
+    _check(got["dA"], want["dA"], "dA", ops, (q * mag["step"]).sum((0, 1)))
+    _check(got["ddt_bias"], want["ddt_bias"], "ddt_bias", ops, mdt.sum((0, 1)))
 
 
 @pytest.mark.parametrize("case", [CHUNKS[0], CHUNKS[1], CHUNKS[2], LANES[1]], ids=str)
