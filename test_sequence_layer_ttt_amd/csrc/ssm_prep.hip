@@ -53,7 +53,7 @@ __global__ __launch_bounds__(64 * HB) void decays(SsmArgs a, int nch, float *out
         double l = 0.0;
         if (t0 + lane < n) {
             step = softplus_f(dts[lane][i] + (a.dt_bias ? a.dt_bias[h] : 0.f));
-            l = fmax(static_cast<double>(step) * a.A[h] * 1.4426950408889634, -160.0);
+            l = at_least(static_cast<double>(step) * a.A[h] * 1.4426950408889634, -160.0);
         }
         const double s = wave_scan(l);
         const double all = __shfl(s, 63, 64);

@@ -124,7 +124,7 @@ __global__ __launch_bounds__(64) void walk(WalkArgs w) {
         if (lane < T) {
             const float d = lane < cn ? softplus_f(fd + bias) : 0.f;
             ds[lane] = d;
-            as[lane] = exp_f(fmaxf(d * A, -150.f));  // 0 below that
+            as[lane] = exp_f(at_least(d * A, -150.f));  // 0 below that
         }
         __syncthreads();
 #pragma unroll
@@ -245,7 +245,7 @@ __global__ __launch_bounds__(64) void walk(WalkArgs w) {
                 if (k < KD && v < VD) f[place(k, v)] = st[i][j];
             }
     }
-    if (!OUT && vb == 0 && lane == 0) w.decay[static_cast<int64_t>(bh) * a.nseg + seg] = exp_f(fmaxf(total, -150.f));
+    if (!OUT && vb == 0 && lane == 0) w.decay[static_cast<int64_t>(bh) * a.nseg + seg] = exp_f(at_least(total, -150.f));
 }
 
 template <int MODE, int KPL, int VPL> hipError_t run_walk_kv(const WalkArgs &w, hipStream_t s) {

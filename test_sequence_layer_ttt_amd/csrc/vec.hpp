@@ -100,6 +100,9 @@ __device__ __forceinline__ float exp_f(float x) {
     return __builtin_amdgcn_exp2f(t) * fmaf(r, 0.693147181f, 1.0f);
 }
 
+// x, or `low` where it is below that. A NaN stays one (fmax would return `low`).
+template <typename T> __device__ __forceinline__ T at_least(T x, T low) { return x < low ? low : x; }
+
 // log(1 + e^s) = max(s, 0) + log(1 + e), e = e^-|s| in (0, 1], which is
 // 2 atanh(q), q = e / (2 + e) <= 1/3, by its series to q^15 (the next term is
 // below 2^-26): small results keep their relative accuracy, about 2 steps.
