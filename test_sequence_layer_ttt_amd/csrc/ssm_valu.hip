@@ -141,7 +141,7 @@ __global__ __launch_bounds__(64) void walk(WalkArgs w) {
 #pragma unroll
         for (int i = 0; i < VN; ++i) {
             const int t = (64 * i + lane) / VP, v = (64 * i + lane) % VP;
-            vs[t][v] = v0 + v < VD ? fv[i] : 0.f;
+            vs[t][v] = v0 + v < VD && t < cn ? fv[i] : 0.f;  // an infinity behind the end would be 0 x inf
         }
         if (STRICT) {  // k . q of each token: four lanes a token
             __syncthreads();

@@ -86,3 +86,21 @@ def test_gradients_through_a_decay_that_is_not_a_number(shape):
     g = ttt.ttt_ssm_backward(**bad, dy=dy)
     assert _all_nan(g["dx"][0, :t, 1]) and _all_nan(g["ddt"][0, :, 1]) and _all_nan(g["dB"][0, :t])
     assert _all_nan(g["dstate"][0, 1]) and _all_nan(g["dA"][1]) and _all_nan(g["ddt_bias"][1])
+
+
+@pytest.mark.parametrize("L", [5, 16, 70])
+def test_an_infinite_last_token_of_the_walk(L):
+    """The rows staged behind a walk's last token add nothing to the state, also
+    where that token's values are infinite: the prompt's state is the one that
+    single tokens give."""
+    d = _inputs(2, L, 2, 20, 12, F32, 4)
+    d["x"][0, L - 1, 1, 3] = INF
+    st = d["state"].clone()
+    for t in range(L):
+        one = {k: d[k][:, t] for k in ("x", "dt", "B", "C")}
+        ttt.ttt_ssm_step(**one, A=d["A"], state=st, D=d["D"], dt_bias=d["dt_bias"])
+    _, so = _forward(d)
+    want = INF * d["B"][0, L - 1, 0].sign()
+    assert torch.equal(st[0, 1, :, 3], want) and torch.equal(so[0, 1, :, 3], want)
+    so[0, 1, :, 3] = 0
+    assert bool(torch.isfinite(so).all())
