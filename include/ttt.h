@@ -558,11 +558,13 @@ int ttt_conv_backward_workspace(int B, int L, int C, int K, size_t *bytes);
  * head, and the states at the borders of segments that run side by side);
  * calls that share one must not overlap.
  * Numerics: state and sums in fp32. bf16 inputs with P <= 64 take MFMA
- * products: the state's update is exact to about 24 bits (its one unrounded
- * operand is split into three bf16 parts); the outputs take the decayed
- * products C_t . B_s and the state as bf16 operands, and a value that is not
- * finite reaches every output of its 64-token chunk. Other inputs take fp32
- * vector arithmetic, token by token.
+ * products: the update of state_out and of the states at segments' borders is
+ * exact to about 24 bits (its one unrounded operand is split into three bf16
+ * parts); the outputs take the decayed products C_t . B_s and the state as
+ * bf16 operands, and within a segment a state whose update takes that operand
+ * in one part. Other inputs take fp32 vector arithmetic, token by token. A
+ * value that is not finite reaches the outputs from its token on that depend
+ * on it, and the state.
  */
 #define TTT_SSM_MAX_DIM 128
 #define TTT_SSM_MAX_HEADS ((1 << 22) - 1)

@@ -19,6 +19,11 @@
 //  * X and B of the next chunk are fetched to registers while this one is
 //    worked on, C straight to the fragment that needs it; X^T and B^T are read
 //    from the row-major tiles by transposing LDS reads.
+//  * A masked M_ij is a zero, and zero times an infinity is not. So infinities
+//    and NaN of x do not enter the tiles: the waves that stage x put zeros there
+//    and note each such feature's first token, from which on its outputs are
+//    NaN, and its state. (B's only meet their own token's column of M, which is
+//    selected.) Testing costs 1.5 us of the 8k prompt's 75.
 //  * Few heads: the sequence is cut into segments that run side by side. A
 //    first launch of the same walk without outputs gives each segment's share
 //    of the state, carried over the segments by ssm_carry.
@@ -47,6 +52,10 @@ template <int N, bool OUT> struct Smem {
     uint16_t s[OUT ? 64 * NS : 8];  // the state's bf16 copy, [feature][n]
     ChunkDecay d[2];
     alignas(16) float f[OUT ? 4 : 1][Q];  // each wave's decays to its tokens' tile
+    // features of x that are not finite, by the waves that found them: whether
+    // there are any, and the first token where one is
+    alignas(16) uint32_t found[OUT ? 2 : 1][4];
+    int first[OUT ? 2 : 1][4][64];
 };
 
 struct MfmaArgs {
@@ -117,9 +126,19 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
         if (FIT != SINGLE) fetch_own(t);
         sd.fetch(prep + static_cast<int64_t>(t / Q) * 4 * Q);
     };
+    uint32_t marked = 0;  // what `found` says of this wave's buffers
+    if constexpr (OUT) sm.found[0][wv] = sm.found[1][wv] = 0;
     auto put = [&](int t, int buf) {
         if (FIT == SINGLE) fetch_own(t);
-        sx.put(sm.x[buf], XS, P);
+        if constexpr (OUT) {
+            const bool found = sx.put_finite(sm.x[buf], XS, P, sm.first[buf][wv]);
+            if (found != (marked >> buf & 1)) {  // it holds what it held
+                sm.found[buf][wv] = found;
+                marked ^= 1u << buf;
+            }
+        } else {
+            sx.put(sm.x[buf], XS, P);
+        }
         sb.put(sm.b[buf], NS, Nn);
         sd.put(sm.d[buf]);
     };
@@ -149,6 +168,17 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
         if (more) fetch(chunk(ci + 1));
         const uint16_t *x = sm.x[buf], *bt = sm.b[buf];
         const ChunkDecay &d = sm.d[buf];
+        bool spoilt = false;
+        if constexpr (OUT) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(sm.found[buf]);
+            spoilt = __builtin_amdgcn_readfirstlane(q.x | q.y | q.z | q.w);
+        }
+        auto first = [&](int p) {  // the first token at which feature p is not finite
+            int f = Q;
+            for (int k = 0; k < 4; ++k)
+                if (sm.found[buf][k]) f = min(f, sm.first[buf][k][p]);
+            return f;
+        };
         bf16x8 xf[2][4];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
@@ -219,6 +249,11 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) o[u][r] = fmaf(Dh, xv[r], y[u][r]);
             }
+            if (__builtin_expect(spoilt, 0)) {
+                for (int u = 0; u < 4; ++u)
+                    for (int r = 0; r < 4; ++r)
+                        if (i >= first(16 * u + 4 * g + r)) o[u][r] = NAN;
+            }
             store_row<FIT>(yp + static_cast<int64_t>(t + i) * a.y.st, t + i < te, o, g, P);
         }
         const float whole = fast_exp2(d.total());
@@ -262,6 +297,12 @@ __device__ __forceinline__ void chunks(const MfmaArgs &w, Smem<N, OUT> &sm) {
                     for (int u = 0; u < UT; ++u)
                         st[i][u] = mfma32(bw[k], N >= 64 || wv < 2 ? xf[kb][u] : xf[kb][2 + u % 2], st[i][u]);
             }
+        }
+        if (OUT && __builtin_expect(spoilt, 0)) {
+            for (int u = 0; u < UT; ++u)
+                if (first(16 * (u0 + u) + c) < Q)
+                    for (int i = 0; i < NT; ++i)
+                        for (int r = 0; r < 4; ++r) st[i][u][r] = NAN;
         }
         if (more) put(chunk(ci + 1), buf ^ 1);
         if constexpr (OUT) {

@@ -82,6 +82,9 @@ __device__ __forceinline__ void weigh(bf16x8 f, f32x4 w0, f32x4 w1, bf16x8 (&out
         out[k] = __builtin_bit_cast(bf16x8, make_uint4(p[k][0], p[k][1], p[k][2], p[k][3]));
 }
 
+typedef __attribute__((ext_vector_type(2))) short s16x2;
+__device__ __forceinline__ s16x2 as_bf16x2(uint32_t v) { return __builtin_bit_cast(s16x2, v); }
+
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Feature f of a row of `cols`, 0 behind them (which are not read).
@@ -174,20 +177,49 @@ template <int F, Fit FIT> struct Stage {
             count = rows;
         }
     }
+    __device__ __forceinline__ uint4 values(int i, int cols) const {
+        if constexpr (FIT != SINGLE) return r[i];
+        const int t = threadIdx.x / PER + i * ROWS, f = threadIdx.x % PER * 8;
+        return t < count ? eight<SINGLE>(base + t * stride, f, cols) : make_uint4(0, 0, 0, 0);
+    }
     __device__ __forceinline__ void put(uint16_t *tile, int lds_stride, int cols) const {
         const int row = threadIdx.x / PER, f = threadIdx.x % PER * 8;
 #pragma unroll
+        for (int i = 0; i < NP; ++i) *reinterpret_cast<uint4 *>(tile + (row + i * ROWS) * lds_stride + f) = values(i, cols);
+    }
+    // The same, with zeros in the place of infinities and NaN. Returns whether
+    // the wave has any: then first[feature] is the first row where it found
+    // one, Q where it found none.
+    __device__ __forceinline__ bool put_finite(uint16_t *tile, int lds_stride, int cols, int *first) const {
+        static_assert(F == 64, "a lane for each feature");
+        const int row = threadIdx.x / PER, f = threadIdx.x % PER * 8;
+        uint4 v[NP];
+        float zero = 0.f;  // the sum of all values times 0
+#pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const int t = row + i * ROWS;
-            uint4 v;
-            if constexpr (FIT != SINGLE) {
-                v = r[i];
-            } else {
-                v = make_uint4(0, 0, 0, 0);
-                if (t < count) v = eight<SINGLE>(base + t * stride, f, cols);
-            }
-            *reinterpret_cast<uint4 *>(tile + t * lds_stride + f) = v;
+            v[i] = values(i, cols);
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) zero = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(w[k]), as_bf16x2(0), zero, false);
         }
+        const bool found = __any(zero != 0.f);
+        if (__builtin_expect(found, 0)) {
+            first[threadIdx.x % 64] = Q;
+            for (int i = 0; i < NP; ++i) {
+                uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t mask = 0x7f80u << 16 * (k % 2);
+                    if ((w[k / 2] & mask) == mask) {
+                        atomicMin(&first[f + k], row + i * ROWS);
+                        w[k / 2] &= k % 2 ? 0x0000ffffu : 0xffff0000u;
+                    }
+                }
+                v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) *reinterpret_cast<uint4 *>(tile + (row + i * ROWS) * lds_stride + f) = v[i];
+        return found;
     }
 };
 

@@ -104,3 +104,52 @@ def test_an_infinite_last_token_of_the_walk(L):
     assert torch.equal(st[0, 1, :, 3], want) and torch.equal(so[0, 1, :, 3], want)
     so[0, 1, :, 3] = 0
     assert bool(torch.isfinite(so).all())
+
+
+@pytest.mark.parametrize("value", [NAN, INF, -INF], ids=str)
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_a_row_that_is_not_finite(shape, value):
+    """A value of x, B or C that is not finite reaches what its token and those
+    behind it make of it: x its own feature, B the whole head, C its token. The
+    outputs before it, of a prompt as of single tokens, keep their bits."""
+    d = _inputs(*shape, 5)
+    B, L, H, P, N, _ = shape
+    y, so = _forward(d)
+    for t in (0, 13, 38, 64, L - 1):
+        if t >= L:
+            continue
+        for k in ("x", "B", "C"):
+            bad = dict(d, **{k: d[k].clone()})
+            i = (7 * t + 3) % (P if k == "x" else N)
+            bad[k][0, t, 0, i] = value
+            gy, gs = _forward(bad)
+            hit = torch.zeros_like(y, dtype=torch.bool)
+            if k == "x":
+                hit[0, t:, 0, i] = True
+            else:
+                hit[0, t:L if k == "B" else t + 1] = True
+            assert not bool(torch.isfinite(gy[hit]).any()), (k, t)
+            assert torch.equal(gy[~hit], y[~hit]), (k, t)
+            where = torch.zeros_like(so, dtype=torch.bool)
+            if k == "x":
+                where[0, 0, :, i] = True
+            elif k == "B":
+                where[0, :, i] = True
+            assert not bool(torch.isfinite(gs[where]).any()), (k, t)
+            assert torch.equal(gs[~where], so[~where]), (k, t)
+
+
+def test_rows_of_which_many_are_not_finite():
+    """Several features and tokens of one chunk, found by different waves, and a
+    chunk behind them that is finite again."""
+    B, L, H, P, N, dt = 1, 200, 768, 64, 16, BF
+    d = _inputs(B, L, H, P, N, dt, 6)
+    y, _ = _forward(d)
+    bad = dict(d, x=d["x"].clone())
+    at = [(70, 3, NAN), (70, 60, INF), (101, 3, INF), (66, 33, -INF), (127, 0, NAN), (64, 17, INF), (150, 5, NAN)]
+    hit = torch.zeros_like(y, dtype=torch.bool)
+    for t, p, v in at:
+        bad["x"][0, t, 5, p] = v
+        hit[0, t:, 5, p] = True
+    gy, _ = _forward(bad)
+    assert not bool(torch.isfinite(gy[hit]).any()) and torch.equal(gy[~hit], y[~hit])
