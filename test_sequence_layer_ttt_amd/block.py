@@ -8,7 +8,9 @@ layer's own entry points, these take strided views (innermost dimension
 contiguous) and run on the operands' device, whichever device is current, on
 its current stream. A `stream` that is given is made the current one for the
 call, so what the call allocates belongs to it. Autograd does not see these
-calls: gradients come from the _backward functions.
+calls, an output never requires a gradient: gradients come from the _backward
+functions. What a call writes into a tensor of the caller's changes the tensor's
+version, as torch's own operators do.
 """
 from __future__ import annotations
 

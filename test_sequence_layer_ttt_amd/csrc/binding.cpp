@@ -132,6 +132,16 @@ Tensor output(PyObject *o, const char *name, at::IntArrayRef shape, at::ScalarTy
     return o == Py_None ? make(shape, dt, k) : check(o, name, shape, dt, k, contiguous);
 }
 
+// What a call has written into a tensor of the caller's changes its version, so
+// that autograd does not go back through what it saved of it before (tensors of
+// inference mode have none).
+void written(const Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(PyObject *given, const Tensor &t) {  // an output that may be new
+    if (given != Py_None) written(t);
+}
+
 void done(int code) {
     if (code == TTT_OK) return;
     PyObject *e = PyObject_CallFunction(ttt_error, "is", code, ttt_last_error());
@@ -212,7 +222,11 @@ struct Grads {
     }
     PyObject *take() {
         PyObject *r = dict ? dict : given;
-        if (!dict) Py_INCREF(r);
+        if (!dict) {
+            PyObject *key, *value;
+            for (Py_ssize_t i = 0; PyDict_Next(given, &i, &key, &value);) written(THPVariable_Unpack(value));
+            Py_INCREF(r);
+        }
         dict = nullptr;
         return r;
     }
@@ -284,6 +298,8 @@ PyObject *conv_forward(PyObject *const *a) {
         return ttt_conv_forward(in.B, in.L, in.C, in.K, in.k.io, act, ox.p, ox.strides, in.w, in.bias, state, lens, oy.p,
                                 oy.strides, ptr(so), s);
     });
+    written(a[6], y);
+    written(a[7], so);
     return pair(y, so);
 }
 
@@ -297,6 +313,8 @@ PyObject *conv_step(PyObject *const *a) {
     call(in.k, [&](hipStream_t s) {
         return ttt_conv_step(in.B, in.C, in.K, in.k.io, act, ox.p, ox.strides, in.w, in.bias, ptr(state), ptr(y), s);
     });
+    written(state);
+    written(a[5], y);
     return THPVariable_Wrap(y);
 }
 
@@ -368,6 +386,8 @@ PyObject *ssm_forward(PyObject *const *a) {
                                in.A, in.ob.p, in.ob.strides, in.oc.p, in.oc.strides, in.D, in.dt_bias, state, lens, oy.p,
                                oy.strides, static_cast<float *>(ptr(so)), ws.p, ws.bytes, s);
     });
+    written(a[9], y);
+    written(a[10], so);
     return pair(y, so);
 }
 
@@ -381,6 +401,8 @@ PyObject *ssm_step(PyObject *const *a) {
                             in.ob.p, in.ob.strides, in.oc.p, in.oc.strides, in.D, in.dt_bias, static_cast<float *>(ptr(state)),
                             ptr(y), s);
     });
+    written(state);
+    written(a[8], y);
     return THPVariable_Wrap(y);
 }
 
@@ -462,6 +484,8 @@ PyObject *block_norm(PyObject *const *a) {
                               in.oy.p, in.oy.strides, in.gp(), in.gs(), in.pg, in.pb, in.qg, in.qb, in.sc, in.lens, ptr(ro),
                               ptr(x), s);
     });
+    written(a[12], ro);
+    written(a[13], x);
     return pair(ro, x);
 }
 
