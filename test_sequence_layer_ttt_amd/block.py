@@ -66,7 +66,10 @@ def _on(stream, operand, fn, *args):
         return fn(*args)
 
 
-def _need(name: str, *args) -> int:
+def _need(name: str, *args: int) -> int:
+    for v in args:
+        if not -2**31 <= v < 2**31:  # ctypes would cut it to 32 bits
+            raise ValueError(f"size {v} is too large")
     n = ctypes.c_size_t(0)
     _lib.check(getattr(_lib.load(), name)(*args, ctypes.byref(n)))
     return n.value
