@@ -56,6 +56,6 @@ def test_a_block_around_ttt_linear(B, L, H):
     for got, want, name in zip((r2, x2), ref_norm(r1, out, gate), ("resid", "x")):
         R.check(got, want, name, 96)
     # the convolution's next token goes on from its last rows
-    again = ttt.ttt_conv_step(x[:, 0], w, x[:, L - K + 1:].contiguous(), b)
+    again = ttt.ttt_conv_step(x[:, 0], w, x[:, L - K + 1:].clone(), b)
     longer, _ = ttt.ttt_conv_forward(torch.cat([x, x[:, :1]], 1), w, b)
     assert torch.equal(again, longer[:, -1])
