@@ -504,7 +504,9 @@ int ttt_ln_l2_bwd(int rows, int d, const float *Z, const float *target,
  * with the K - 1 tokens before the first taken from `state` (NULL: zeros).
  *   2 <= K <= 4; 0 <= C <= TTT_CONV_MAX_C; 0 <= B <= 65535; act TTT_ACT_NONE
  *   or TTT_ACT_SILU.
- *   x, y      : [B,L,C] io, strided.   weight : [C,K] fp32.
+ *   x, y      : [B,L,C] io, strided (batch, token: the C channels of a token
+ *               are contiguous, so [B,H,L,d] features are laid out anew first).
+ *   weight    : [C,K] fp32.
  *   bias      : [C] fp32 or NULL.      state  : [B,K-1,C] io, oldest first.
  *   state_out : [B,K-1,C] io or NULL, the last K - 1 tokens of (state, x);
  *               it may be exactly `state`.

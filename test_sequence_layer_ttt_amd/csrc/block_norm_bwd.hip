@@ -10,7 +10,8 @@
 // ([..]: with the mean's removal only).
 // B=4 L=2048 D=768 bf16: 101 MB in 30 us, 3.4 TB/s; bound by registers, which
 // the columns' sums and two rows take: two waves a SIMD hide less of the loads
-// and of four dependent row sums than the forward's do.
+// and of four dependent row sums than the forward's do. Vector units are busy
+// 61 % of the time (90 instructions a value), waves wait 46 % of theirs.
 #include "block_norm.hpp"
 
 namespace ttt {

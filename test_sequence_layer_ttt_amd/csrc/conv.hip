@@ -1,5 +1,5 @@
-// Short causal convolution of the projected features, one filter of K = 2..4
-// taps for each channel:
+// Short causal convolution of [B,L,C] features (a block's input, or columns of a
+// projection's output), one filter of K = 2..4 taps for each channel:
 //     z_t = bias + sum_k w_k x_{t-K+1+k},   y_t = z_t or z_t sigma(z_t),
 // where the K - 1 tokens before the first come from a state (or are zero) and
 // the last K - 1 tokens of each sequence are its state afterwards.
@@ -17,9 +17,11 @@
 //             The same walk with z_t formed again (x and dy read once, dx
 //             written once); dw and db are summed over a workgroup's tokens in
 //             registers and LDS and over the workgroups by column_sums, in a
-//             fixed order. B=4 L=2048 C=896 bf16: 19 us for 44 MB; vector
-//             bound, about 40 operations a value (two of them transcendental),
-//             1.75 workgroups a compute unit.
+//             fixed order. B=4 L=2048 C=896 bf16: 19.4 us for 44 MB. 52 vector
+//             instructions a value (2.4 of them transcendental) are 12.6 us on
+//             the compute units that hold two of the 448 workgroups; they hold
+//             the vector units 64 % of the time, waves wait 40 % of theirs: for
+//             their first rows, and for LDS in the K + 1 sums at the end.
 #include "block.hpp"
 #include "vec.hpp"
 

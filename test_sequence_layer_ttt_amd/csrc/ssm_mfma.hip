@@ -30,13 +30,13 @@
 // Floor: x, y once (2 * 128 bytes a token and head), B and C from the L2 that
 // the heads of a segment share; about 8 N * 64 + 4 * 64 * (N + 64) flops a
 // token and head.
-// Measured, bf16, P = 64: B=2 L=8192 H=32 N=64 outputs 41 us, shares 26 us (12
-// segments; x and y once would be 28 us); L=32768 H=32 N=128 outputs 130 us,
-// shares 93 us. Bound by latency and issue together: three workgroups (two at
-// N = 128) of four waves a compute unit, about 310 vector instructions for a
-// wave and chunk, which hold the vector unit 55 % of the time, waves waiting
-// 37 % of theirs; without its stores the first takes 35 us, without its loads
-// 39. Straight-line code for each wave's tiles, D x as a product of its own and
+// Measured, bf16, P = 64: B=2 L=8192 H=32 N=64 outputs 43 us, shares 27 us (12
+// segments; x and y once would be 28 us); L=32768 H=32 N=128 outputs 129 us,
+// shares 90 us. Bound by latency and issue together: three workgroups (two at
+// N = 128) of four waves a compute unit, 344 vector instructions for a wave and
+// chunk, which hold the vector unit 55 % of the time, waves waiting 39 % of
+// theirs. With 311 of them (no test of x) the first took 41 us; 35 without its
+// stores, 39 without its loads. Straight-line code for each wave's tiles, D x as a product of its own and
 // tiles without bank conflicts changed nothing (41 .. 42 us).
 #include "ssm_tile.hpp"
 
