@@ -224,7 +224,8 @@ struct Grads {
         PyObject *r = dict ? dict : given;
         if (!dict) {
             PyObject *key, *value;
-            for (Py_ssize_t i = 0; PyDict_Next(given, &i, &key, &value);) written(THPVariable_Unpack(value));
+            for (Py_ssize_t i = 0; PyDict_Next(given, &i, &key, &value);)
+                if (THPVariable_Check(value)) written(THPVariable_Unpack(value));  // others ran since it was checked
             Py_INCREF(r);
         }
         dict = nullptr;
