@@ -659,6 +659,117 @@ int ttt_block_norm_backward(int B, int L, int D, int io, int resid_io, int layer
                             size_t workspace_bytes, hipStream_t stream);
 int ttt_block_norm_backward_workspace(int B, int L, int D, int gate_shape, size_t *bytes);
 
+/*
+ * Gated linear recurrence: a state for each channel that decays by a gate of
+ * its own with every token and gains the token's gated feature,
+ *     h_t = a_t h_{t-1} + s_t sigma(i_t) x_t,   y_t = h_t
+ *     log a_t = -rate sigma(r_t),  s_t = sqrt(1 - a_t^2)   with a rate
+ *     a_t = sigma(r_t),            s_t = 1 - a_t           where rate is NULL
+ * (sigma(i_t) = 1 where i is NULL).
+ *   1 <= D <= TTT_LRU_MAX_D; 0 <= B <= 65535; B*ceil(L/64) at most
+ *   TTT_LRU_MAX_TILES.
+ *   x, r, i, y : [B,L,D] io, strided (batch, token).
+ *   rate       : [D] fp32, >= 0, or NULL. Below 0 the state would grow: s is NaN.
+ *   state      : [B,D] fp32 or NULL (zeros); state_out : the same or NULL; it
+ *                may be exactly `state`.
+ * The workspace holds ttt_lru_forward_workspace's bytes (decays and states at
+ * the borders of the tiles that run side by side; none for a prompt of one
+ * tile); calls that share one must not overlap.
+ * Numerics: gates, decays and the state in fp32; 1 - a keeps its relative
+ * accuracy where a is near 1. A value that is not finite reaches the outputs of
+ * its channel from its token on, as itself or as NaN, and the state.
+ */
+#define TTT_LRU_MAX_D (1 << 20)
+#define TTT_LRU_MAX_TILES ((1 << 22) - 1)
+int ttt_lru_forward(int B, int L, int D, int io, const void *x, const int64_t *x_strides,
+                    const void *r, const int64_t *r_strides, const void *i,
+                    const int64_t *i_strides, const float *rate, const float *state,
+                    const int *lens, void *y, const int64_t *y_strides, float *state_out,
+                    void *workspace, size_t workspace_bytes, hipStream_t stream);
+int ttt_lru_forward_workspace(int B, int L, int D, size_t *bytes);
+
+/*
+ * One token of ttt_lru_forward for each sequence: x, r, i [B,D] io (strides:
+ * the batch stride alone), y [B,D] io contiguous, state [B,D] fp32 updated in
+ * place. B*D < 2^31.
+ */
+int ttt_lru_step(int B, int D, int io, const void *x, const int64_t *x_strides, const void *r,
+                 const int64_t *r_strides, const void *i, const int64_t *i_strides,
+                 const float *rate, float *state, void *y, hipStream_t stream);
+
+/*
+ * Gradients of <dy, y> + <dstate_out, state_out> through ttt_lru_forward from
+ * its inputs (the forward saves nothing; dstate_out NULL: zero): dx, dr, di
+ * [B,L,D] io, strided; drate [D] and dstate [B,D] fp32; di, drate and dstate
+ * NULL exactly when i, rate and state are. Where a gate is so far closed that
+ * s_t = 0, the derivative of s_t (infinite there) counts as 0. The workspace
+ * holds ttt_lru_backward_workspace's bytes; calls that share one must not
+ * overlap.
+ */
+int ttt_lru_backward(int B, int L, int D, int io, const void *x, const int64_t *x_strides,
+                     const void *r, const int64_t *r_strides, const void *i,
+                     const int64_t *i_strides, const float *rate, const float *state,
+                     const int *lens, const void *dy, const int64_t *dy_strides,
+                     const float *dstate_out, void *dx, const int64_t *dx_strides, void *dr,
+                     const int64_t *dr_strides, void *di, const int64_t *di_strides,
+                     float *drate, float *dstate, void *workspace, size_t workspace_bytes,
+                     hipStream_t stream);
+int ttt_lru_backward_workspace(int B, int L, int D, size_t *bytes);
+
+/*
+ * Products in 8-bit integers, for projections whose weights and inputs are
+ * held in 8 bits with a scale for each output feature and each token.
+ *   1 <= K <= TTT_I8_MAX_K; 0 <= M, N <= TTT_I8_MAX_ROWS (N: features);
+ *   ceil(M/64)*ceil(N/64) at most TTT_I8_MAX_TILES.
+ * Rows of 8-bit values may have a stride (x_strides and the like: one number,
+ * the row stride) and any address; rows of K a multiple of 16 on 16-byte
+ * boundaries go the fastest way.
+ *
+ * ttt_i8_quantize: rows of x [M,K] io as q [M,K] and scale [M] fp32,
+ *     scale = max |x| / 127,   q = x / scale to the nearest whole number (ties
+ * to even; of the exact quotient by the fp32 scale), -127 <= q <= 127. A row of
+ * zeros has scale 0. A row that holds an infinity or a NaN has a NaN for its
+ * scale (so its products are NaN) and zeros for q.
+ */
+#define TTT_I8_MAX_K 65536
+#define TTT_I8_MAX_ROWS (1 << 24)
+#define TTT_I8_MAX_TILES ((1 << 22) - 1)
+int ttt_i8_quantize(int M, int K, int io, const void *x, const int64_t *x_strides, int8_t *q,
+                    const int64_t *q_strides, float *scale, hipStream_t stream);
+
+/*
+ *     y[m][n] = x_scale[m] w_scale[n] sum_k x[m][k] w[n][k]  (+ bias[n])
+ * x [M,K], w [N,K] (output-major, as ttt_qkv_project's theta), any 8-bit
+ * values; x_scale [M], w_scale [N], bias [N] fp32 (bias may be NULL); y [M,N]
+ * out_io, row-strided. The sum is exact; scales, bias and the sum's conversion
+ * are fp32, y is rounded once.
+ */
+int ttt_i8_project(int M, int K, int N, int out_io, const int8_t *x, const int64_t *x_strides,
+                   const float *x_scale, const int8_t *w, const int64_t *w_strides,
+                   const float *w_scale, const float *bias, void *y, const int64_t *y_strides,
+                   hipStream_t stream);
+
+/*
+ * ttt_i8_project of x's quantised rows (ttt_i8_quantize's values), x and y in
+ * io. The workspace holds ttt_i8_linear_workspace's bytes, 16-byte aligned (the
+ * quantised rows and their scales); calls that share one must not overlap.
+ */
+int ttt_i8_linear(int M, int K, int N, int io, const void *x, const int64_t *x_strides,
+                  const int8_t *w, const int64_t *w_strides, const float *w_scale,
+                  const float *bias, void *y, const int64_t *y_strides, void *workspace,
+                  size_t workspace_bytes, hipStream_t stream);
+int ttt_i8_linear_workspace(int M, int K, size_t *bytes);
+
+/*
+ * ttt_qkv_project with theta [3,H*d,d_model] in 8 bits, theta_scale [3,H*d]
+ * fp32, X [B,L,d_model] bf16 quantised token by token: XQ, XK, XV [B,H,L,d]
+ * bf16, 16-byte aligned; d = 64. Workspace: ttt_i8_linear_workspace(B*L,
+ * d_model).
+ */
+int ttt_qkv_project_i8(int B, int L, int d_model, int H, int d, const void *X,
+                       const int8_t *theta, const float *theta_scale, void *XQ, void *XK,
+                       void *XV, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Message for the last non-zero return on this thread ("" if none). */
 const char *ttt_last_error(void);
 

@@ -88,6 +88,20 @@ def load():
     lib.ttt_ssm_step.argtypes = [_i] * 6 + [_P] * 13 + [_P]
     lib.ttt_ssm_backward.argtypes = [_i] * 7 + [_P] * 29 + [size, _P]
     lib.ttt_ssm_backward_workspace.argtypes = [_i] * 6 + [ctypes.POINTER(size)]
+    lib.ttt_lru_forward.argtypes = [_i] * 4 + [_P] * 13 + [size, _P]
+    lib.ttt_lru_forward_workspace.argtypes = [_i] * 3 + [ctypes.POINTER(size)]
+    lib.ttt_lru_step.argtypes = [_i] * 3 + [_P] * 9 + [_P]
+    lib.ttt_lru_backward.argtypes = [_i] * 4 + [_P] * 21 + [size, _P]
+    lib.ttt_lru_backward_workspace.argtypes = [_i] * 3 + [ctypes.POINTER(size)]
+    lib.ttt_i8_quantize.argtypes = [_i] * 3 + [_P] * 5 + [_P]
+    lib.ttt_i8_project.argtypes = [_i] * 4 + [_P] * 9 + [_P]
+    lib.ttt_i8_linear.argtypes = [_i] * 4 + [_P] * 9 + [size, _P]
+    lib.ttt_i8_linear_workspace.argtypes = [_i] * 2 + [ctypes.POINTER(size)]
+    lib.ttt_qkv_project_i8.argtypes = [_i] * 5 + [_P] * 7 + [size, _P]
+    for name in ("ttt_lru_forward", "ttt_lru_forward_workspace", "ttt_lru_step", "ttt_lru_backward",
+                 "ttt_lru_backward_workspace", "ttt_i8_quantize", "ttt_i8_project", "ttt_i8_linear",
+                 "ttt_i8_linear_workspace", "ttt_qkv_project_i8"):
+        getattr(lib, name).restype = _i
     for name in ("ttt_ssm_forward", "ttt_ssm_forward_workspace", "ttt_ssm_step", "ttt_ssm_backward",
                  "ttt_ssm_backward_workspace", "ttt_conv_forward", "ttt_conv_step", "ttt_conv_backward", "ttt_conv_backward_workspace",
                  "ttt_block_norm", "ttt_block_norm_backward", "ttt_block_norm_backward_workspace"):

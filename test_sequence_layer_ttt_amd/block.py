@@ -1,6 +1,7 @@
 """Python binding of the operators around the layer: the short causal
-convolution, the selective state space scan and the block norm, under the C
-ABI's names (ttt.py offers them too).
+convolution, the selective state space scan, the gated linear recurrence, the
+block norm and the 8-bit integer products, under the C ABI's names (ttt.py
+offers them too).
 
 The marshalling is native (csrc/binding.cpp): it checks the tensors, makes the
 outputs and workspaces that are not given and calls libttt.so. Unlike the
@@ -169,6 +170,108 @@ def ttt_ssm_backward(x, dt, A, B, C, dy, D=None, dt_bias=None, state=None, dstat
     if stream is not None:
         return _on(stream, x, _native.ssm_backward, *args)
     return _native.ssm_backward(*args)
+
+
+# --- gated linear recurrence -----------------------------------------------------
+
+
+def ttt_lru_forward_workspace(B: int, L: int, D: int) -> int:
+    """Bytes of device workspace ttt_lru_forward needs."""
+    return _need("ttt_lru_forward_workspace", B, L, D)
+
+
+def ttt_lru_forward(x, r, rate=None, i=None, state=None, lens=None, y=None, state_out=None, workspace=None,
+                    stream=None):
+    """Gated linear recurrence, a state for each channel: h_t = a_t h_{t-1} +
+    s_t sigma(i_t) x_t and y_t = h_t, with log a_t = -rate sigma(r_t), s_t =
+    sqrt(1 - a_t^2) or, without a rate, a_t = sigma(r_t), s_t = 1 - a_t (sigma(i)
+    is 1 without i). x, r, i, y [B,L,D] in fp32 or bf16 (views with a contiguous
+    last dimension allowed, as slices of one projection's output); rate [D] fp32
+    >= 0; state, state_out [B,D] fp32; lens [B] int32 optional lengths. Returns
+    (y, state_out); state_out may be `state` itself."""
+    args = (x, r, rate, i, state, lens, y, state_out, workspace)
+    if stream is not None:
+        return _on(stream, x, _native.lru_forward, *args)
+    return _native.lru_forward(*args)
+
+
+def ttt_lru_step(x, r, state, rate=None, i=None, y=None, stream=None):
+    """One token of ttt_lru_forward for each sequence: x, r, i [B,D] (views with
+    a contiguous last dimension allowed), state [B,D] fp32 updated in place.
+    Returns y [B,D]."""
+    args = (x, r, state, rate, i, y)
+    if stream is not None:
+        return _on(stream, x, _native.lru_step, *args)
+    return _native.lru_step(*args)
+
+
+def ttt_lru_backward_workspace(B: int, L: int, D: int) -> int:
+    """Bytes of device workspace ttt_lru_backward needs."""
+    return _need("ttt_lru_backward_workspace", B, L, D)
+
+
+def ttt_lru_backward(x, r, dy, rate=None, i=None, state=None, dstate_out=None, lens=None, workspace=None, grads=None,
+                     stream=None) -> dict:
+    """Gradients of <dy, y> + <dstate_out, state_out> through ttt_lru_forward:
+    dx, dr and, for those of i, rate and state that are given, di [B,L,D] in x's
+    type, drate [D] and dstate [B,D] fp32. `grads` may hold the outputs (a dict
+    like the one returned; dx, dr, di may be strided, slices of one buffer too)."""
+    args = (x, r, dy, rate, i, state, dstate_out, lens, workspace, grads)
+    if stream is not None:
+        return _on(stream, x, _native.lru_backward, *args)
+    return _native.lru_backward(*args)
+
+
+# --- products in 8-bit integers ----------------------------------------------------
+
+
+def ttt_i8_quantize(x, q=None, scale=None, stream=None):
+    """Rows of x [...,K] (fp32 or bf16) in 8 bits: scale [...] = max |x| / 127 in
+    fp32 and q [...,K] int8, x / scale to the nearest whole number (ties to even).
+    A row that holds an infinity or a NaN has a NaN for its scale. For tokens, and
+    once for a weight [N,K]. Returns (q, scale)."""
+    args = (x, q, scale)
+    if stream is not None:
+        return _on(stream, x, _native.i8_quantize, *args)
+    return _native.i8_quantize(*args)
+
+
+def ttt_i8_project(x, x_scale, w, w_scale, bias=None, dtype=torch.bfloat16, y=None, stream=None):
+    """y[...,n] = x_scale[...] w_scale[n] sum_k x[...,k] w[n,k] (+ bias[n]): x
+    [...,K] int8 with x_scale [...] fp32 for each row, w [N,K] int8 with w_scale
+    [N] and bias [N] fp32; the sum is exact. y [...,N] in `dtype`, bf16 or fp32.
+    Rows may be strided (one stride apart)."""
+    io = {torch.bfloat16: _lib.TTT_BF16, torch.float32: _lib.TTT_F32}.get(dtype)
+    if io is None:
+        raise TypeError(f"dtype {dtype} not supported")
+    args = (x, x_scale, w, w_scale, bias, io, y)
+    if stream is not None:
+        return _on(stream, x, _native.i8_project, *args)
+    return _native.i8_project(*args)
+
+
+def ttt_i8_linear_workspace(M: int, K: int) -> int:
+    """Bytes of device workspace ttt_i8_linear needs for M rows of K."""
+    return _need("ttt_i8_linear_workspace", M, K)
+
+
+def ttt_i8_linear(x, w, w_scale, bias=None, y=None, workspace=None, stream=None):
+    """ttt_i8_project of x's rows quantised as ttt_i8_quantize does: x [...,K] and
+    y [...,N] in fp32 or bf16, w [N,K] int8 with w_scale [N] fp32."""
+    args = (x, w, w_scale, bias, y, workspace)
+    if stream is not None:
+        return _on(stream, x, _native.i8_linear, *args)
+    return _native.i8_linear(*args)
+
+
+def ttt_qkv_project_i8(X, theta, theta_scale, H: int, out=None, workspace=None, stream=None):
+    """ttt_qkv_project in 8 bits: X [B,L,d_model] bf16 quantised token by token,
+    theta [3,H*64,d_model] int8 with theta_scale [3,H*64] fp32. Returns XQ, XK, XV
+    [B,H,L,64] bf16."""
+    args = (X, theta, theta_scale, H, None if out is None else tuple(out), workspace)
+    if stream is not None:
+        return _on(stream, X, _native.qkv_project_i8, *args)
+    return _native.qkv_project_i8(*args)
 
 
 # --- norms, gate and residual between two blocks -------------------------------

@@ -44,6 +44,7 @@ std::string text(at::ScalarType t) {
         case at::kHalf: return "torch.float16";
         case at::kDouble: return "torch.float64";
         case at::kLong: return "torch.int64";
+        case at::kChar: return "torch.int8";
         default: return std::string("torch.") + c10::toString(t);
     }
 }
@@ -519,6 +520,236 @@ PyObject *block_norm_backward(PyObject *const *a) {
     return g.take();
 }
 
+// --- gated linear recurrence -----------------------------------------------------
+
+// x, r, rate, i
+struct LruIn {
+    const Tensor &x;
+    Kind k;
+    int B, L, D;
+    const Tensor &r;
+    const Tensor *i;
+    const float *rate;
+    Operand ox, orr;
+    std::optional<Operand> oi;
+    LruIn(PyObject *px, PyObject *pr, PyObject *prate, PyObject *pi, bool one)
+        : x(ranked(px, "x", {one ? 2 : 3})), k(kind_of(x, "x")), B(size(x.size(0), "B")), L(one ? 1 : size(x.size(1), "L")),
+          D(size(x.size(-1), "D")), r(check(pr, "r", x.sizes(), k.dt, k, false)), i(nullptr),
+          rate(opt<const float>(prate, "rate", {D}, at::kFloat, k)), ox(x, "x"), orr(r, "r") {
+        if (pi == Py_None) return;
+        i = &check(pi, "i", x.sizes(), k.dt, k, false);
+        oi.emplace(*i, "i");
+    }
+    const void *ip() const { return oi ? oi->p : nullptr; }
+    const int64_t *is() const { return oi ? oi->strides : nullptr; }
+    Shape state() const { return {B, D}; }
+};
+
+// x, r, rate, i, state, lens, y, state_out, workspace
+PyObject *lru_forward(PyObject *const *a) {
+    const LruIn in(a[0], a[1], a[2], a[3], false);
+    const float *state = opt<const float>(a[4], "state", in.state(), at::kFloat, in.k);
+    const int *lens = opt<const int>(a[5], "lens", {in.B}, at::kInt, in.k);
+    const Tensor y = output(a[6], "y", in.x.sizes(), in.k.dt, in.k, false);
+    const Tensor so = output(a[7], "state_out", in.state(), at::kFloat, in.k);
+    size_t need = 0;
+    done(ttt_lru_forward_workspace(in.B, in.L, in.D, &need));
+    const Workspace ws(a[8], need, in.k);
+    const Operand oy(y, "y");
+    call(in.k, [&](hipStream_t s) {
+        return ttt_lru_forward(in.B, in.L, in.D, in.k.io, in.ox.p, in.ox.strides, in.orr.p, in.orr.strides, in.ip(), in.is(),
+                               in.rate, state, lens, oy.p, oy.strides, static_cast<float *>(ptr(so)), ws.p, ws.bytes, s);
+    });
+    written(a[6], y);
+    written(a[7], so);
+    return pair(y, so);
+}
+
+// x, r, state, rate, i, y
+PyObject *lru_step(PyObject *const *a) {
+    const LruIn in(a[0], a[1], a[3], a[4], true);
+    const Tensor &state = check(a[2], "state", in.state(), at::kFloat, in.k);
+    const Tensor y = output(a[5], "y", in.x.sizes(), in.k.dt, in.k);
+    call(in.k, [&](hipStream_t s) {
+        return ttt_lru_step(in.B, in.D, in.k.io, in.ox.p, in.ox.strides, in.orr.p, in.orr.strides, in.ip(), in.is(), in.rate,
+                            static_cast<float *>(ptr(state)), ptr(y), s);
+    });
+    written(state);
+    written(a[5], y);
+    return THPVariable_Wrap(y);
+}
+
+// x, r, dy, rate, i, state, dstate_out, lens, workspace, grads
+PyObject *lru_backward(PyObject *const *a) {
+    const LruIn in(a[0], a[1], a[3], a[4], false);
+    const Tensor &dy = check(a[2], "dy", in.x.sizes(), in.k.dt, in.k, false);
+    const float *state = opt<const float>(a[5], "state", in.state(), at::kFloat, in.k);
+    const float *dso = opt<const float>(a[6], "dstate_out", in.state(), at::kFloat, in.k);
+    const int *lens = opt<const int>(a[7], "lens", {in.B}, at::kInt, in.k);
+    Grads g(a[9], in.k);
+    const Tensor dx = g.get("dx", in.x.sizes(), in.k.dt, false), dr = g.get("dr", in.x.sizes(), in.k.dt, false);
+    Tensor di, dq, ds;
+    if (in.i) di = g.get("di", in.x.sizes(), in.k.dt, false);
+    if (a[3] != Py_None) dq = g.get("drate", {in.D}, at::kFloat);
+    if (a[5] != Py_None) ds = g.get("dstate", in.state(), at::kFloat);
+    g.whole();
+    auto f = [](const Tensor &t) { return t.defined() ? static_cast<float *>(ptr(t)) : nullptr; };
+    size_t need = 0;
+    done(ttt_lru_backward_workspace(in.B, in.L, in.D, &need));
+    const Workspace ws(a[8], need, in.k);
+    const Operand oy(dy, "dy"), odx(dx, "dx"), odr(dr, "dr");
+    std::optional<Operand> odi;
+    if (in.i) odi.emplace(di, "di");
+    call(in.k, [&](hipStream_t s) {
+        return ttt_lru_backward(in.B, in.L, in.D, in.k.io, in.ox.p, in.ox.strides, in.orr.p, in.orr.strides, in.ip(), in.is(),
+                                in.rate, state, lens, oy.p, oy.strides, dso, odx.p, odx.strides, odr.p, odr.strides,
+                                odi ? odi->p : nullptr, odi ? odi->strides : nullptr, f(dq), f(ds), ws.p, ws.bytes, s);
+    });
+    return g.take();
+}
+
+// --- products in 8-bit integers ----------------------------------------------------
+
+// rows of the innermost dimension: all others as one, by one stride
+struct RowsOf {
+    const Tensor &t;
+    int M, K;
+    int64_t stride;
+    Shape lead;
+    RowsOf(const Tensor &x, const char *name) : t(x), M(0), K(0), stride(0) {
+        if (t.dim() < 1) raise(PyExc_ValueError, std::string(name) + " has no dimension");
+        lead.assign(t.sizes().begin(), t.sizes().end() - 1);
+        K = size(t.size(-1), "K");
+        if (K > 1 && t.stride(-1) != 1)
+            raise(PyExc_ValueError, std::string("the innermost dimension of ") + name + " must be contiguous");
+        int64_t n = 1;
+        stride = K;
+        for (int64_t i = t.dim() - 2; i >= 0; --i) {
+            if (t.size(i) == 1) continue;
+            if (n == 1)
+                stride = t.stride(i);
+            else if (n && t.stride(i) != n * stride)
+                raise(PyExc_ValueError, "the rows of " + std::string(name) + " are not one stride apart");
+            n *= t.size(i);
+        }
+        M = size(n, "M");
+    }
+    RowsOf(const RowsOf &) = delete;
+    Shape with(int64_t inner) const {
+        Shape s = lead;
+        s.push_back(inner);
+        return s;
+    }
+};
+
+Kind on_device(const Tensor &t, const char *name, at::ScalarType dt) {
+    if (t.scalar_type() != dt)
+        raise(PyExc_TypeError, std::string(name) + " has dtype " + text(t.scalar_type()) + ", expected " + text(dt));
+    if (!t.is_cuda()) raise(PyExc_ValueError, std::string(name) + " must be a device tensor (got " + t.device().str() + ")");
+    return {static_cast<int>(t.get_device()), dt, 0};
+}
+
+// x, q, scale
+PyObject *i8_quantize(PyObject *const *a) {
+    const Tensor &x = tensor(a[0], "x");
+    const Kind k = kind_of(x, "x");
+    const RowsOf r(x, "x");
+    const Tensor q = output(a[1], "q", x.sizes(), at::kChar, k, false), scale = output(a[2], "scale", r.lead, at::kFloat, k);
+    const RowsOf rq(q, "q");
+    call(k, [&](hipStream_t s) {
+        return ttt_i8_quantize(r.M, r.K, k.io, ptr(x), &r.stride, static_cast<int8_t *>(ptr(q)), &rq.stride,
+                               static_cast<float *>(ptr(scale)), s);
+    });
+    written(a[1], q);
+    written(a[2], scale);
+    return pair(q, scale);
+}
+
+// w, w_scale, bias
+struct I8Weight {
+    const RowsOf w;
+    const float *scale, *bias;
+    I8Weight(PyObject *pw, PyObject *ps, PyObject *pb, int64_t K, const Kind &k)
+        : w(check(pw, "w", {ranked(pw, "w", {2}).size(0), K}, at::kChar, k, false), "w"),
+          scale(static_cast<const float *>(ptr(check(ps, "w_scale", {w.M}, at::kFloat, k)))),
+          bias(opt<const float>(pb, "bias", {w.M}, at::kFloat, k)) {}
+};
+
+// x, x_scale, w, w_scale, bias, bf16, y
+PyObject *i8_project(PyObject *const *a) {
+    const Tensor &x = tensor(a[0], "x");
+    const Kind k = on_device(x, "x", at::kChar);
+    const RowsOf r(x, "x");
+    const float *xs = static_cast<const float *>(ptr(check(a[1], "x_scale", r.lead, at::kFloat, k)));
+    const I8Weight w(a[2], a[3], a[4], r.K, k);
+    const int io = number(a[5]);
+    const Tensor y = output(a[6], "y", r.with(w.w.M), io == TTT_BF16 ? at::kBFloat16 : at::kFloat, k, false);
+    const RowsOf ry(y, "y");
+    call(k, [&](hipStream_t s) {
+        return ttt_i8_project(r.M, r.K, w.w.M, io, static_cast<const int8_t *>(ptr(x)), &r.stride, xs,
+                              static_cast<const int8_t *>(ptr(w.w.t)), &w.w.stride, w.scale, w.bias, ptr(y), &ry.stride, s);
+    });
+    written(a[6], y);
+    return THPVariable_Wrap(y);
+}
+
+// x, w, w_scale, bias, y, workspace
+PyObject *i8_linear(PyObject *const *a) {
+    const Tensor &x = tensor(a[0], "x");
+    const Kind k = kind_of(x, "x");
+    const RowsOf r(x, "x");
+    const I8Weight w(a[1], a[2], a[3], r.K, k);
+    const Tensor y = output(a[4], "y", r.with(w.w.M), k.dt, k, false);
+    const RowsOf ry(y, "y");
+    size_t need = 0;
+    done(ttt_i8_linear_workspace(r.M, r.K, &need));
+    const Workspace ws(a[5], need, k);
+    call(k, [&](hipStream_t s) {
+        return ttt_i8_linear(r.M, r.K, w.w.M, k.io, ptr(x), &r.stride, static_cast<const int8_t *>(ptr(w.w.t)), &w.w.stride,
+                             w.scale, w.bias, ptr(y), &ry.stride, ws.p, ws.bytes, s);
+    });
+    written(a[4], y);
+    return THPVariable_Wrap(y);
+}
+
+// X, theta, theta_scale, H, out (None or a tuple of three), workspace
+PyObject *qkv_project_i8(PyObject *const *a) {
+    const Tensor &x = ranked(a[0], "X", {3});
+    const Kind k = on_device(x, "X", at::kBFloat16);
+    const int B = size(x.size(0), "B"), L = size(x.size(1), "L"), dm = size(x.size(2), "d_model");
+    const long heads = PyLong_AsLong(a[3]);
+    if (heads == -1 && PyErr_Occurred()) throw PyError{};
+    if (heads < 0) raise(PyExc_ValueError, "H = " + std::to_string(heads) + " is negative");
+    const int H = size(heads, "H");
+    const int64_t hd = static_cast<int64_t>(H) * 64;
+    check(a[0], "X", x.sizes(), at::kBFloat16, k);
+    const Tensor &th = check(a[1], "theta", {3, hd, dm}, at::kChar, k), &ts = check(a[2], "theta_scale", {3, hd}, at::kFloat, k);
+    if (a[4] != Py_None && (!PyTuple_Check(a[4]) || PyTuple_GET_SIZE(a[4]) != 3))
+        raise(PyExc_ValueError, "out must be a tuple of three tensors");
+    const char *names[3] = {"XQ", "XK", "XV"};
+    Tensor out[3];
+    for (int i = 0; i < 3; ++i)
+        out[i] = output(a[4] == Py_None ? Py_None : PyTuple_GET_ITEM(a[4], i), names[i], {B, H, L, 64}, at::kBFloat16, k);
+    size_t need = 0;
+    done(ttt_i8_linear_workspace(size(static_cast<int64_t>(B) * L, "B*L"), dm, &need));
+    const Workspace ws(a[5], need, k);
+    call(k, [&](hipStream_t s) {
+        return ttt_qkv_project_i8(B, L, dm, H, 64, ptr(x), static_cast<const int8_t *>(ptr(th)),
+                                  static_cast<const float *>(ptr(ts)), ptr(out[0]), ptr(out[1]), ptr(out[2]), ws.p, ws.bytes, s);
+    });
+    PyObject *r = PyTuple_New(3);
+    for (int i = 0; r && i < 3; ++i) {
+        if (a[4] != Py_None) written(out[i]);
+        PyObject *o = THPVariable_Wrap(out[i]);
+        if (!o) {
+            Py_DECREF(r);
+            return nullptr;
+        }
+        PyTuple_SET_ITEM(r, i, o);
+    }
+    return r;
+}
+
 // the class that errors of the C ABI are raised as
 PyObject *init(PyObject *const *a) {
     Py_XDECREF(ttt_error);
@@ -531,7 +762,9 @@ PyObject *init(PyObject *const *a) {
     { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&method<name, n>)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {METHOD(init, 1), METHOD(conv_forward, 8), METHOD(conv_step, 6), METHOD(conv_backward, 10),
                          METHOD(ssm_forward, 12), METHOD(ssm_step, 9), METHOD(ssm_backward, 13), METHOD(block_norm, 14),
-                         METHOD(block_norm_backward, 16), {nullptr, nullptr, 0, nullptr}};
+                         METHOD(block_norm_backward, 16), METHOD(lru_forward, 9), METHOD(lru_step, 6),
+                         METHOD(lru_backward, 10), METHOD(i8_quantize, 3), METHOD(i8_project, 7), METHOD(i8_linear, 6),
+                         METHOD(qkv_project_i8, 6), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,38 @@
+// Arguments of the 8-bit integer product and the quantiser of its rows
+// (i8_quantize.hip, i8_gemm.hip). All strides are in elements, the innermost
+// dimension contiguous.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ttt {
+
+struct I8QuantArgs {
+    int M, K, io;
+    const void *x;  // [M,K]
+    int64_t xr;
+    int8_t *q;  // [M,K], rows of qr
+    int64_t qr;
+    float *scale;  // [M]
+};
+
+struct I8Args {
+    int M, K, N, out_io;  // tokens, contraction, features
+    const int8_t *x;      // [M,K]
+    int64_t xr;
+    const float *xs;  // [M]
+    const int8_t *w;  // [N,K]
+    int64_t wr;
+    const float *ws, *bias;  // [N]; bias may be null
+    void *y;                 // [M,N]
+    int64_t yr;
+    // as the layer's views: three of [B,H,L,64] instead of y, N = 192 H, M = B L
+    int L = 0, H = 0;
+    void *v[3] = {};
+};
+
+hipError_t launch_i8_quantize(const I8QuantArgs &a, hipStream_t stream);
+hipError_t launch_i8_project(const I8Args &a, hipStream_t stream);
+
+}  // namespace ttt
