@@ -30,6 +30,7 @@ struct I8Args {
     // as the layer's views: three of [B,H,L,64] instead of y, N = 192 H, M = B L
     int L = 0, H = 0;
     void *v[3] = {};
+    bool vec = false;  // y in 16-byte accesses (set by the launch)
 };
 
 hipError_t launch_i8_quantize(const I8QuantArgs &a, hipStream_t stream);

@@ -112,9 +112,273 @@ __global__ __launch_bounds__(256) void i8_any(I8Args a) {
         for (int j = 0; j < 2; ++j) store4(a, m0 + wt + 16 * j + c, n0 + wf + 16 * i + 4 * g, acc[i][j]);
 }
 
+// Where logical chunk j of row r of a half lies among its eight: j ^ key(r).
+__device__ __forceinline__ int keyA(int r) { return (r & 3) | ((r >> 2) & 4); }
+
+// Workgroup id -> tile. Workgroups go to the 8 XCDs round robin; each XCD takes
+// a run of tiles, by fours of feature blocks over all token blocks, so that the
+// 32 tiles it works on at a time share 4 blocks of w and 8 of x in its L2.
+__device__ __forceinline__ void tile_of(int id, int nfb, int ntb, int *fb, int *tb) {
+    const int T = nfb * ntb, q = T / 8, r = T % 8, x = id % 8;
+    const int i = x * q + min(x, r) + id / 8;
+    const int f0 = i / (4 * ntb) * 4, k = i - f0 * ntb, n = min(4, nfb - f0);
+    *fb = f0 + k % n;
+    *tb = k / n;
+}
+
+// A lane's 16 consecutive features from n on, of the tokens that `each` puts.
+template <typename F> __device__ __forceinline__ void store_rows(const I8Args &a, int n, F each) {
+    if (n >= a.N) return;
+    float ws[16], bias[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const int f = min(n + e, a.N - 1);
+        ws[e] = a.ws[f];
+        bias[e] = a.bias ? a.bias[f] : 0.f;
+    }
+    const bool vec = a.vec && n + 16 <= a.N;
+    each([&](int m, auto acc) {
+        if (m >= a.M) return;
+        const float sx = a.xs[m];
+        float o[16];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const i32x4 v = acc(t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[4 * t + e] = fmaf(static_cast<float>(v[e]) * sx, ws[4 * t + e], bias[4 * t + e]);
+        }
+        uint16_t *y16;
+        if (a.H) {  // 16 features of one head
+            const int HD = a.H * 64, v = n / HD, hj = n - v * HD, b = m / a.L, t = m - b * a.L;
+            y16 = static_cast<uint16_t *>(v == 0 ? a.v[0] : v == 1 ? a.v[1] : a.v[2]);
+            y16 += ((static_cast<int64_t>(b) * a.H + hj / 64) * a.L + t) * 64 + hj % 64;
+        } else {
+            y16 = static_cast<uint16_t *>(a.y) + (m * a.yr + n);
+        }
+        if (a.out_io) {
+            if (vec) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    reinterpret_cast<uint4 *>(y16)[h] =
+                        make_uint4(tile::pack2(o[8 * h], o[8 * h + 1]), tile::pack2(o[8 * h + 2], o[8 * h + 3]),
+                                   tile::pack2(o[8 * h + 4], o[8 * h + 5]), tile::pack2(o[8 * h + 6], o[8 * h + 7]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (n + e < a.N) y16[e] = f32_to_bf16(o[e]);
+            }
+        } else {
+            float *y = static_cast<float *>(a.y) + (m * a.yr + n);
+            if (vec) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    reinterpret_cast<float4 *>(y)[t] = make_float4(o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (n + e < a.N) y[e] = o[e];
+            }
+        }
+    });
+}
+
+// Large products: a workgroup of 8 waves takes 256 features x 256 tokens.
+// Contraction steps of 128 bytes; both operands lie in LDS in halves of 128
+// rows, two stages of 64 KB, filled by direct global-to-LDS loads.
+//  * a wave (wr, wc) takes 64 x 32 of each of the four quadrants (a half of the
+//    features by a half of the tokens): 4 x 2 MFMA tiles, and walks them as
+//    (0,0), (1,0), (1,1), (0,1), so that a step reads every fragment once;
+//  * a quadrant is two sections: M reads the fragments that it or the next
+//    quadrant lacks (8 or 4 of 1 KB) and asks for the half of two steps ahead
+//    whose place was read last, C is its 16 products. A barrier ends each
+//    section, and the waves 4 .. 7 run one section behind the waves 0 .. 3: on
+//    each SIMD one wave multiplies while the other one reads;
+//  * a half is asked for 7 M sections before it is read: s_waitcnt vmcnt(12) at
+//    the end of M leaves the 12 younger loads in flight. That wait and the one
+//    for the section's own LDS reads stand before the section's barrier, so
+//    behind it every wave's loads have landed, and the place of what was read
+//    may be filled again;
+//  * rows of 128 bytes, 16-byte chunk j of row r at j ^ key(r): 8 distinct
+//    places for the 8 rows that a fragment read touches at once. A's MFMA row
+//    4 g + e of tile t is feature 16 g + 4 t + e, so that a lane ends up with 16
+//    consecutive features of a token (32 bytes of bf16) and four lanes with 64;
+//  * past K the chunks are read again from the last one and A's are taken as
+//    zeros; rows past the end are read from the last one and not stored.
+constexpr int BT = 256, BK = 128;
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// Rows from p on, for loads by a 32-bit offset; the offsets stay within the rows.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const int8_t *p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(p), 0, 0xffffffff, 0x00027000);
+}
+__device__ __forceinline__ void fence() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void section_end() {  // barrier alone: no wait
+    fence();
+    __builtin_amdgcn_s_barrier();
+    fence();
+}
+
+template <bool TAIL> __global__ __launch_bounds__(512, 2) void i8_big(I8Args a, int nfb, int ntb) {
+    // halves of A, then of B, each for both stages: 64 KB that one address reaches
+    __shared__ __attribute__((aligned(16))) int8_t sm[2][2][2][128 * BK];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, c = lane & 15;
+    const int wr = w >> 2, wc = w & 3;
+    int fb, tb;
+    tile_of(blockIdx.x, nfb, ntb, &fb, &tb);
+    const int n0 = fb * BT, m0 = tb * BT;
+    const int nk = (a.K + BK - 1) / BK, tail = TAIL ? a.K % BK : 0;  // a multiple of 16
+
+    // loads: a wave's instruction q fills rows 16 w + 8 q .. + 7 of a half
+    const auto baseA = buffer(a.w + static_cast<int64_t>(n0) * a.wr), baseB = buffer(a.x + static_cast<int64_t>(m0) * a.xr);
+    uint32_t off[4][2];  // of A0, A1, B0, B1 from their base
+    const int rl = lane >> 3, pc = lane & 7;
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int r = 16 * w + 8 * q + rl;
+            const int ch = pc ^ (h < 2 ? keyA(r) : r & 7);
+            const int row = min((h & 1) * 128 + r, (h < 2 ? a.N - n0 : a.M - m0) - 1);
+            off[h][q] = static_cast<uint32_t>(row) * static_cast<uint32_t>(h < 2 ? a.wr : a.xr) + 16 * ch;
+        }
+    auto ask = [&](int k, int stage, int h) {
+        const int kk = k < nk ? k : 0;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t o = off[h][q];
+            if (TAIL && kk == nk - 1) {
+                const int r = 16 * w + 8 * q + rl, ch = pc ^ (h < 2 ? keyA(r) : r & 7);
+                o -= 16 * max(ch - (tail / 16 - 1), 0);
+            }
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(h < 2 ? baseA : baseB,
+                                                     (lds_void *)&sm[h >> 1][stage][h & 1][(16 * w + 8 * q) * BK], 16, o,
+                                                     kk * BK, 0, 0);
+        }
+    };
+    const int ra = 64 * wr + 16 * (c >> 2) + (c & 3);  // A's row of tile 0 (tile t: + 4 t)
+    const int rb = 32 * wc + c;                         // B's row of tile 0 (tile s: + 16 s)
+    const int8_t *pa[2], *pb[2];
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+        pa[kk] = &sm[0][0][0][ra * BK + 16 * ((4 * kk + g) ^ (c & 7))];  // keyA(ra + 4 t) = c & 7
+        pb[kk] = &sm[1][0][0][rb * BK + 16 * ((4 * kk + g) ^ (c & 7))];
+    }
+    auto read_a = [&](int stage, int h, i32x4 (&f)[2][4]) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                f[kk][t] = *reinterpret_cast<const i32x4 *>(pa[kk] + (2 * stage + h) * 128 * BK + 4 * t * BK);
+    };
+    auto read_b = [&](int stage, int h, i32x4 (&f)[2][2]) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                f[kk][s] = *reinterpret_cast<const i32x4 *>(pb[kk] + (2 * stage + h) * 128 * BK + 16 * s * BK);
+    };
+    auto cut = [&](int k, i32x4 (&f)[2][4]) {  // past K
+        if (TAIL && k == nk - 1) {
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    if (16 * (4 * kk + g) >= tail) f[kk][t] = i32x4{0, 0, 0, 0};
+        }
+    };
+    i32x4 acc[2][2][4][2] = {};  // quadrant (A half, B half), tiles
+    auto multiply = [&](i32x4 (&q)[4][2], const i32x4 (&fa)[2][4], const i32x4 (&fb_)[2][2]) {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) q[t][s] = mfma_i8(fa[kk][t], fb_[kk][s], q[t][s]);
+        __builtin_amdgcn_s_setprio(0);
+        section_end();
+    };
+    auto m_end = [&] {
+        fence();
+        __builtin_amdgcn_s_waitcnt(0x0F70 | 12);  // vmcnt(12)
+        __builtin_amdgcn_s_waitcnt(0xC07F);       // lgkmcnt(0)
+        section_end();
+    };
+    i32x4 a0[2][4], a1[2][4], b0[2][2], b1[2][2];
+    // A0 A1 B0 B1 are halves 0 1 2 3, asked for in the order 2 0 1 3
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        ask(k, k, 2);
+        ask(k, k, 0);
+        ask(k, k, 1);
+        ask(k, k, 3);
+    }
+    m_end();  // the first halves 2 and 0
+    read_b(0, 0, b0);
+    m_end();
+    if (wr) section_end();
+    auto step = [&](int k, int stage) {
+        read_a(stage, 0, a0);
+        ask(k + 2, stage, 2);
+        cut(k, a0);
+        m_end();
+        multiply(acc[0][0], a0, b0);
+        read_a(stage, 1, a1);
+        ask(k + 2, stage, 0);
+        cut(k, a1);
+        m_end();
+        multiply(acc[1][0], a1, b0);
+        read_b(stage, 1, b1);
+        ask(k + 2, stage, 1);
+        m_end();
+        multiply(acc[1][1], a1, b1);
+        read_b(stage ^ 1, 0, b0);
+        ask(k + 2, stage, 3);
+        m_end();
+        multiply(acc[0][1], a0, b1);
+    };
+    for (int k = 0; k < nk; k += 2) {
+        step(k, 0);
+        if (k + 1 < nk) step(k + 1, 1);
+    }
+    if (!wr) section_end();
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // the loads behind the last step
+
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int n = n0 + 128 * i + 64 * wr + 16 * g;  // the lane's 16 features
+        store_rows(a, n, [&](auto put) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) put(m0 + 128 * j + 32 * wc + 16 * s + c, [&](int t) { return acc[i][j][t][s]; });
+        });
+    }
+}
+
+bool aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
 }  // namespace
 
-hipError_t launch_i8_project(const I8Args &a, hipStream_t s) {
+hipError_t launch_i8_project(const I8Args &in, hipStream_t s) {
+    I8Args a = in;
+    a.vec = a.H || (aligned(a.y) && a.yr * (a.out_io ? 2 : 4) % 16 == 0);
+    // whole 16-byte chunks, and a tile's offsets in 32 bits
+    const bool chunks = a.K % 16 == 0 && a.xr % 16 == 0 && a.wr % 16 == 0 && aligned(a.x) && aligned(a.w) &&
+                        a.xr < (1 << 23) && a.wr < (1 << 23);
+    const int nfb = (a.N + BT - 1) / BT, ntb = (a.M + BT - 1) / BT;
+    if (chunks && static_cast<int64_t>(nfb) * ntb >= 4) {
+        const dim3 grid(static_cast<unsigned>(nfb * ntb));
+        if (a.K % BK)
+            hipLaunchKernelGGL(i8_big<true>, grid, dim3(512), 0, s, a, nfb, ntb);
+        else
+            hipLaunchKernelGGL(i8_big<false>, grid, dim3(512), 0, s, a, nfb, ntb);
+        return hipGetLastError();
+    }
     const int64_t tiles = (static_cast<int64_t>(a.N) + GT - 1) / GT * ((static_cast<int64_t>(a.M) + GT - 1) / GT);
     hipLaunchKernelGGL(i8_any, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, s, a);
     return hipGetLastError();
