@@ -24,6 +24,13 @@ View optional(const void *p, const char *name, int B, int L, int D, const int64_
     return p ? view(p, name, B, L, 1, D, strides, 2, es) : flat(nullptr, name, 0, es);
 }
 
+int scratch(const void *workspace, size_t bytes, size_t need) {
+    if (bytes < need) return fail(TTT_E_SHAPE, "workspace of %zu bytes, %zu needed", bytes, need);
+    if (need && (reinterpret_cast<uintptr_t>(workspace) & 15))
+        return fail(TTT_E_ALIGN, "workspace (%p) is not 16-byte aligned", workspace);
+    return TTT_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -53,8 +60,8 @@ int ttt_lru_forward(int B, int L, int D, int io, const void *x, const int64_t *x
         (st = v.add_in(flat(lens, "lens", lens ? B : 0, 4))) || (st = v.add_out(vy)) ||
         (st = v.add_out(flat(state_out, "state_out", state_out ? sn : 0, 4))))
         return st;
-    if (workspace_bytes < need) return fail(TTT_E_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
-    if ((st = v.add_out(flat(workspace, "workspace", static_cast<int64_t>(need / 4), 4))) ||
+    if ((st = scratch(workspace, workspace_bytes, need)) ||
+        (st = v.add_out(flat(workspace, "workspace", static_cast<int64_t>(need / 4), 4))) ||
         (st = v.alias(state_out, state)))
         return st;
     if (!B || (!L && !state_out)) return ok();
@@ -119,8 +126,8 @@ int ttt_lru_backward(int B, int L, int D, int io, const void *x, const int64_t *
         (st = v.add_out(vdr)) || (st = v.add_out(vdi)) || (st = v.add_out(flat(drate, "drate", drate ? D : 0, 4))) ||
         (st = v.add_out(flat(dstate, "dstate", dstate ? sn : 0, 4))))
         return st;
-    if (workspace_bytes < need) return fail(TTT_E_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
-    if ((st = v.add_out(flat(workspace, "workspace", static_cast<int64_t>(need / 4), 4))) || (st = v.alias())) return st;
+    if ((st = scratch(workspace, workspace_bytes, need)) ||
+        (st = v.add_out(flat(workspace, "workspace", static_cast<int64_t>(need / 4), 4))) || (st = v.alias())) return st;
     ttt::LruBwdArgs g{{B, L, D, io, x, r, i, vx.sb, vx.st, vr.sb, vr.st, vi.sb, vi.st, rate, state, lens, nullptr, 0, 0,
                        nullptr, static_cast<float *>(workspace)},
                       dy, vd.sb, vd.st, dstate_out, dx, dr, di, vdx.sb, vdx.st, vdr.sb, vdr.st, vdi.sb, vdi.st, drate, dstate};
@@ -216,10 +223,8 @@ int ttt_i8_linear(int M, int K, int N, int io, const void *x, const int64_t *x_s
     if ((st = v.add_in(vx)) || (st = v.add_in(vw)) || (st = v.add_in(flat(w_scale, "w_scale", N, 4))) ||
         (st = v.add_in(flat(bias, "bias", bias ? N : 0, 4))) || (st = v.add_out(vy)))
         return st;
-    if (workspace_bytes < need) return fail(TTT_E_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
-    if (need && (reinterpret_cast<uintptr_t>(workspace) & 15))
-        return fail(TTT_E_ALIGN, "workspace (%p) is not 16-byte aligned", workspace);
-    if ((st = v.add_out(flat(workspace, "workspace", static_cast<int64_t>(need / 4), 4))) || (st = v.alias())) return st;
+    if ((st = scratch(workspace, workspace_bytes, need)) ||
+        (st = v.add_out(flat(workspace, "workspace", static_cast<int64_t>(need / 4), 4))) || (st = v.alias())) return st;
     if (!M || !N) return ok();
     ttt::I8Args a{M, K, N, io, nullptr, 0, nullptr, w, vw.sb, w_scale, bias, y, vy.sb};
     return quantised(M, K, io, x, vx.sb, workspace, &a, stream);
@@ -248,10 +253,8 @@ int ttt_qkv_project_i8(int B, int L, int d_model, int H, int d, const void *X, c
         if (M * H && (reinterpret_cast<uintptr_t>(out[k]) & 15))
             return fail(TTT_E_ALIGN, "%s (%p) is not 16-byte aligned", names[k], out[k]);
     }
-    if (workspace_bytes < need) return fail(TTT_E_SHAPE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
-    if (need && (reinterpret_cast<uintptr_t>(workspace) & 15))
-        return fail(TTT_E_ALIGN, "workspace (%p) is not 16-byte aligned", workspace);
-    if ((st = v.add_out(flat(workspace, "workspace", static_cast<int64_t>(need / 4), 4))) || (st = v.alias())) return st;
+    if ((st = scratch(workspace, workspace_bytes, need)) ||
+        (st = v.add_out(flat(workspace, "workspace", static_cast<int64_t>(need / 4), 4))) || (st = v.alias())) return st;
     if (!M || !N) return ok();
     ttt::I8Args a{static_cast<int>(M), d_model, static_cast<int>(N), TTT_BF16, nullptr, 0, nullptr, theta, d_model,
                   theta_scale, nullptr, nullptr, 0, L, H, {XQ, XK, XV}};

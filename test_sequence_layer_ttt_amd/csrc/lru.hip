@@ -6,13 +6,6 @@ namespace {
 
 using namespace lru;
 
-// A thread's share of a tile: V channels of U consecutive tokens.
-template <int V> struct Tile {
-    static constexpr int CL = CH / V;       // lanes along the channels
-    static constexpr int TG = NT / CL;      // runs of tokens
-    static constexpr int U = TOKENS / TG;   // tokens of a run
-};
-
 __device__ __forceinline__ int live_tokens(const int *lens, int b, int L) {
     return lens ? max(0, min(lens[b], L)) : L;
 }
@@ -30,98 +23,90 @@ __device__ __forceinline__ void token(const float (&x)[V], const float (&r)[V], 
     }
 }
 
-// Scan over the runs of a tile: on entry a thread's (A, H) of its run, on exit
-// those of all runs before it; the tile's own are returned for channel
-// threadIdx.x (threads below CH).
-template <int V>
-__device__ __forceinline__ float2 tile_scan(float (&A)[V], float (&H)[V], float2 (*sm)[CH]) {
-    constexpr int TG = Tile<V>::TG, CL = Tile<V>::CL;
-    const int lane = threadIdx.x % CL, run = threadIdx.x / CL;
-#pragma unroll
-    for (int v = 0; v < V; ++v) sm[run][lane * V + v] = make_float2(A[v], H[v]);
-    __syncthreads();
-    float2 all = make_float2(1.f, 0.f);
-    if (threadIdx.x < CH) {
-#pragma unroll
-        for (int g = 0; g < TG; ++g) {
-            const float2 q = sm[g][threadIdx.x];
-            sm[g][threadIdx.x] = all;
-            all = make_float2(all.x * q.x, fmaf(q.x, all.y, q.y));
-        }
+// One pass over the prompt. A workgroup takes a tile of T tokens x 128 channels:
+// a thread scans V channels of U consecutive tokens from a zero state, with the
+// running state and decay of each in registers; LDS joins the tile's runs, and
+// what the tile does to a state, (A, H): h -> A h + H, is published for the
+// tiles behind it. With the state before the tile known, a token's output is
+// A_t first + H_t.
+//
+// The state before a tile: tiles are joined in groups of GROUP; a tile takes the
+// state behind the group before its own and applies, in their order, the (A, H)
+// of the tiles before it in its group; the last tile of a group publishes the
+// state behind it. So the order of the sums is fixed, and a prompt of n tiles is a
+// chain of n / GROUP links.
+//
+// Tiles wait for tiles: each takes its place in line by a counter as it starts,
+// all channels of a tile's tokens before the next tile's, so that whatever a
+// tile waits for has started before it and waits for earlier ones alone. A
+// published value carries its own flag: a word is ready where it is not all
+// ones (cleared to that before; a NaN of this very pattern is published as
+// another NaN). Words are written and read as single atomics at the scope of
+// the device, past the XCDs' L2 caches.
+constexpr int GROUP = 8;
+constexpr uint32_t WAIT32 = 0xffffffffu;
+constexpr uint64_t WAIT64 = 0xffffffffffffffffull;
+constexpr int POLLS = 1 << 22;  // seconds: a word that never comes is a NaN then
+
+struct Plan {
+    int tokens;  // of a tile
+    int64_t tiles, groups;
+};
+Plan plan(int B, int L, int D);
+
+// workspace: the counter, then the tiles' (A, H) [B][tiles][D], then the states behind groups [B][groups][D]
+struct Words {
+    uint32_t *ticket;
+    uint64_t *share;
+    uint32_t *state;
+    __device__ __forceinline__ Words(float *ws, int64_t shares)
+        : ticket(reinterpret_cast<uint32_t *>(ws)), share(reinterpret_cast<uint64_t *>(ws + 4)),
+          state(reinterpret_cast<uint32_t *>(ws + 4 + 2 * shares)) {}
+};
+template <typename W> __device__ __forceinline__ W peek(const W *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename W> __device__ __forceinline__ void publish(W *p, W v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename W> __device__ __forceinline__ W await(const W *p, W v, W wait) {
+    for (int n = 0; v == wait && n < POLLS; ++n) {
+        __builtin_amdgcn_s_sleep(2);
+        v = peek(p);
     }
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const float2 q = sm[run][lane * V + v];
-        A[v] = q.x;
-        H[v] = q.y;
-    }
-    return all;
+    return v;
 }
 
-// Each tile's decay and own share of the state behind it: ws[b][chunk][2][D].
-template <typename T, int V, bool RATE>
-__global__ __launch_bounds__(NT) void lru_shares(LruArgs a) {
-    constexpr int TG = Tile<V>::TG, CL = Tile<V>::CL, U = Tile<V>::U;
-    __shared__ float2 sm[TG][CH];
-    const int lane = threadIdx.x % CL, run = threadIdx.x / CL;
-    const int b = blockIdx.z, chunk = blockIdx.x, c0 = blockIdx.y * CH, c = c0 + lane * V;
-    const int n = live_tokens(a.lens, b, a.L);
-    const int t0 = chunk * TOKENS + run * U, t1 = min(t0 + U, n);
-    float A[V], H[V], rate[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f, rate[v] = RATE && c < a.D ? a.rate[c + v] : 0.f;
-    if (c < a.D && t0 < t1) {
-        const T *x = static_cast<const T *>(a.x) + b * a.xb + c, *r = static_cast<const T *>(a.r) + b * a.rb + c;
-        const T *ig = a.i ? static_cast<const T *>(a.i) + b * a.ib + c : nullptr;
-        for (int t = t0; t < t1; ++t) {
-            float xv[V], rv[V], iv[V] = {}, d[V], u[V];
-            vec_load<T, V>(x + t * a.xt, xv);
-            vec_load<T, V>(r + t * a.rt, rv);
-            if (ig) vec_load<T, V>(ig + t * a.it, iv);
-            token<V, RATE>(xv, rv, iv, ig != nullptr, rate, d, u);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                H[v] = fmaf(d[v], H[v], u[v]);
-                A[v] *= d[v];
-            }
-        }
-    }
-    const float2 all = tile_scan<V>(A, H, sm);
-    const int cc = c0 + threadIdx.x;
-    if (threadIdx.x < CH && cc < a.D) {
-        float *w = a.ws + (static_cast<int64_t>(b) * chunks(a.L) + chunk) * 2 * a.D;
-        w[cc] = all.x;
-        w[a.D + cc] = all.y;
-    }
+__global__ __launch_bounds__(NT) void lru_clear(uint4 *p, int64_t n) {
+    const int64_t k = static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x;
+    if (k < n) p[k] = make_uint4(WAIT32, WAIT32, WAIT32, WAIT32);
 }
 
-// The state before each tile, over its share in ws.
-__global__ __launch_bounds__(NT) void lru_carry(LruArgs a) {
-    const int c = blockIdx.x * NT + threadIdx.x, b = blockIdx.y, n = chunks(a.L);
-    if (c >= a.D) return;
-    float *w = a.ws + static_cast<int64_t>(b) * n * 2 * a.D + c;
-    float h = a.state ? a.state[static_cast<int64_t>(b) * a.D + c] : 0.f;
-    for (int k = 0; k < n; ++k, w += 2 * static_cast<int64_t>(a.D)) {
-        const float A = w[0], H = w[a.D];
-        w[0] = h;
-        h = fmaf(A, h, H);
-    }
-}
-
-template <typename T, int V, bool RATE>
-__global__ __launch_bounds__(NT) void lru_outputs(LruArgs a) {
+template <typename T, int V, int U, bool RATE, bool MANY>
+__global__ __launch_bounds__(NT) void lru_scan(LruArgs a, int nch, int ngr) {
     typedef VecIO<T, V> IO;
-    constexpr int TG = Tile<V>::TG, CL = Tile<V>::CL, U = Tile<V>::U;
+    constexpr int CL = CH / V, TG = NT / CL;  // lanes along the channels, runs of tokens
     __shared__ float2 sm[TG][CH];
+    __shared__ float sfirst[CH];
+    __shared__ uint32_t place;
     const int lane = threadIdx.x % CL, run = threadIdx.x / CL;
-    const int b = blockIdx.z, chunk = blockIdx.x, c0 = blockIdx.y * CH, c = c0 + lane * V;
-    const int n = live_tokens(a.lens, b, a.L), nch = chunks(a.L);
-    const int t0 = chunk * TOKENS + run * U;
+    int b = blockIdx.z, k = blockIdx.x, cb = blockIdx.y;
+    const Words words(a.ws, static_cast<int64_t>(a.B) * nch * a.D);
+    if constexpr (MANY) {
+        if (threadIdx.x == 0) place = atomicAdd(words.ticket, 1u) + 1;  // from all ones on
+        __syncthreads();
+        const uint32_t ncb = gridDim.y, t = place;
+        cb = static_cast<int>(t % ncb);
+        b = static_cast<int>(t / ncb % a.B);
+        k = static_cast<int>(t / ncb / a.B);
+    }
+    const int c0 = cb * CH, c = c0 + lane * V;
+    const int n = live_tokens(a.lens, b, a.L);
+    const int t0 = (k * TG + run) * U;
     float A[V], H[V], At[U][V], Ht[U][V], rate[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f, rate[v] = RATE && c < a.D ? a.rate[c + v] : 0.f;
     const bool in = c < a.D;
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f, rate[v] = RATE && in ? a.rate[c + v] : 0.f;
     const T *x = static_cast<const T *>(a.x) + b * a.xb + c, *r = static_cast<const T *>(a.r) + b * a.rb + c;
     const T *ig = a.i ? static_cast<const T *>(a.i) + b * a.ib + c : nullptr;
 #pragma unroll
@@ -142,15 +127,61 @@ __global__ __launch_bounds__(NT) void lru_outputs(LruArgs a) {
 #pragma unroll
         for (int v = 0; v < V; ++v) At[u][v] = A[v], Ht[u][v] = H[v];
     }
+    // the runs before each run, and the tile's own (A, H)
+#pragma unroll
+    for (int v = 0; v < V; ++v) sm[run][lane * V + v] = make_float2(A[v], H[v]);
+    __syncthreads();
     const int64_t row = static_cast<int64_t>(b) * a.D;
-    float first[V];
-    const float *from = nch > 1 ? a.ws + (static_cast<int64_t>(b) * nch + chunk) * 2 * a.D : a.state ? a.state + row : nullptr;
+    const int cc = c0 + threadIdx.x;
+    if (threadIdx.x < CH) {
+        float2 all = make_float2(1.f, 0.f);
 #pragma unroll
-    for (int v = 0; v < V; ++v) first[v] = in && from ? from[c + v] : 0.f;
-    tile_scan<V>(A, H, sm);
+        for (int q = 0; q < TG; ++q) {
+            const float2 s = sm[q][threadIdx.x];
+            sm[q][threadIdx.x] = all;
+            all = make_float2(all.x * s.x, fmaf(s.x, all.y, s.y));
+        }
+        float h = 0.f;
+        if (cc < a.D) {
+            // the first tile's share holds the state before it, which no other tile reads
+            if (k == 0 && a.state) h = a.state[row + cc];
+            if constexpr (MANY) {
+                const int j = k / GROUP, before = k % GROUP;  // the group, tiles before this one in it
+                const bool ends = before == GROUP - 1;
+                uint64_t *share = words.share + (static_cast<int64_t>(b) * nch + k) * a.D + cc;
+                uint32_t *state = words.state + (static_cast<int64_t>(b) * ngr + j) * a.D + cc;
+                if (!ends && k + 1 < nch) {
+                    const float own = k == 0 ? fmaf(all.x, h, all.y) : all.y;
+                    uint64_t w = static_cast<uint64_t>(__float_as_uint(own)) << 32 | __float_as_uint(all.x);
+                    publish(share, w == WAIT64 ? w << 1 >> 1 : w);
+                }
+                uint64_t w[GROUP - 1];
+#pragma unroll
+                for (int q = 0; q < GROUP - 1; ++q)
+                    w[q] = q < before ? peek(share - static_cast<int64_t>(before - q) * a.D) : 0;
+                if (j > 0) h = __uint_as_float(await(state - a.D, peek(state - a.D), WAIT32));
+#pragma unroll
+                for (int q = 0; q < GROUP - 1; ++q)
+                    if (q < before) {
+                        const uint64_t p = await(share - static_cast<int64_t>(before - q) * a.D, w[q], WAIT64);
+                        h = fmaf(__uint_as_float(static_cast<uint32_t>(p)), h, __uint_as_float(static_cast<uint32_t>(p >> 32)));
+                    }
+                if (ends && k + 1 < nch) {
+                    const uint32_t s = __float_as_uint(fmaf(all.x, h, all.y));
+                    publish(state, s == WAIT32 ? s >> 1 : s);
+                }
+            }
+        }
+        sfirst[threadIdx.x] = h;
+    }
+    __syncthreads();
     if (!in) return;
+    float first[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) first[v] = fmaf(A[v], first[v], H[v]);
+    for (int v = 0; v < V; ++v) {
+        const float2 q = sm[run][lane * V + v];
+        first[v] = fmaf(q.x, sfirst[lane * V + v], q.y);
+    }
     T *y = static_cast<T *>(a.y) + b * a.yb + c;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -160,7 +191,7 @@ __global__ __launch_bounds__(NT) void lru_outputs(LruArgs a) {
         for (int v = 0; v < V; ++v) o[v] = t < n ? fmaf(At[u][v], first[v], Ht[u][v]) : 0.f;
         if (t < a.L) IO::store(y + t * a.yt, o);
     }
-    if (a.state_out && chunk == nch - 1 && run == TG - 1) {
+    if (a.state_out && k == nch - 1 && run == TG - 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v) a.state_out[row + c + v] = fmaf(At[U - 1][v], first[v], Ht[U - 1][v]);
     }
@@ -201,20 +232,41 @@ template <typename T> bool vectors(const LruArgs &a) {
            aligned(a.x, 16) && aligned(a.r, 16) && aligned(a.i, 16) && aligned(a.y, 16);
 }
 
+// Tiles of 128 tokens where that leaves four for each compute unit, else of 64, of 32.
+Plan plan(int B, int L, int D) {
+    const int64_t wide = (static_cast<int64_t>(D) + CH - 1) / CH * B;
+    int tokens = 128;
+    while (tokens > 32 && wide * ((L + tokens - 1) / tokens) < 1024) tokens /= 2;
+    Plan p{tokens, (static_cast<int64_t>(L) + tokens - 1) / tokens, 0};
+    p.groups = p.tiles / GROUP;
+    return p;
+}
+
+template <typename T, int V, int U, bool RATE> hipError_t scan(const LruArgs &a, const Plan &p, hipStream_t s) {
+    const int nch = static_cast<int>(p.tiles), ngr = static_cast<int>(p.groups);
+    const dim3 grid(nch, (a.D + CH - 1) / CH, a.B);
+    if (nch > 1) {
+        const int64_t words = lru_forward_floats(a.B, a.L, a.D) / 4;
+        hipLaunchKernelGGL(lru_clear, dim3(static_cast<unsigned>((words + NT - 1) / NT)), dim3(NT), 0, s,
+                           reinterpret_cast<uint4 *>(a.ws), words);
+        hipLaunchKernelGGL((lru_scan<T, V, U, RATE, true>), grid, dim3(NT), 0, s, a, nch, ngr);
+    } else {
+        hipLaunchKernelGGL((lru_scan<T, V, U, RATE, false>), grid, dim3(NT), 0, s, a, nch, ngr);
+    }
+    return hipGetLastError();
+}
+
 template <typename T, int V, bool RATE> hipError_t forward(const LruArgs &a, hipStream_t s) {
-    const int nch = chunks(a.L);
-    if (!nch) {  // the caller has asked for the state alone
+    const Plan p = plan(a.B, a.L, a.D);
+    if (!p.tiles) {  // the caller has asked for the state alone
         const int64_t n = static_cast<int64_t>(a.B) * a.D;
         hipLaunchKernelGGL(lru_pass, dim3(static_cast<unsigned>((n + NT - 1) / NT)), dim3(NT), 0, s, a);
         return hipGetLastError();
     }
-    const dim3 grid(nch, (a.D + CH - 1) / CH, a.B);
-    if (nch > 1) {
-        hipLaunchKernelGGL((lru_shares<T, V, RATE>), grid, dim3(NT), 0, s, a);
-        hipLaunchKernelGGL(lru_carry, dim3((a.D + NT - 1) / NT, a.B), dim3(NT), 0, s, a);
-    }
-    hipLaunchKernelGGL((lru_outputs<T, V, RATE>), grid, dim3(NT), 0, s, a);
-    return hipGetLastError();
+    constexpr int TG = NT / (CH / V);
+    return p.tokens == 128 ? scan<T, V, 128 / TG, RATE>(a, p, s)
+           : p.tokens == 64 ? scan<T, V, 64 / TG, RATE>(a, p, s)
+                            : scan<T, V, 32 / TG, RATE>(a, p, s);
 }
 
 template <typename T, int V, bool RATE> hipError_t step(const LruArgs &a, hipStream_t s) {
@@ -238,8 +290,9 @@ template <typename T> hipError_t step_t(const LruArgs &a, hipStream_t s) {
 }  // namespace
 
 int64_t lru_forward_floats(int B, int L, int D) {
-    const int64_t n = lru::chunks(L);
-    return n > 1 ? 2 * n * B * D : 0;
+    const Plan p = plan(B, L, D);
+    // in whole 16 bytes
+    return p.tiles > 1 ? (4 + (2 * p.tiles + p.groups) * B * D + 3) / 4 * 4 : 0;
 }
 hipError_t launch_lru_forward(const LruArgs &a, hipStream_t s) {
     return a.io ? forward_t<bf16_t>(a, s) : forward_t<float>(a, s);

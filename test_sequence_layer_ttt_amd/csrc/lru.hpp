@@ -46,10 +46,7 @@ int64_t lru_backward_floats(int B, int L, int D);
 namespace lru {
 
 constexpr int NT = 256;     // threads of a workgroup
-constexpr int TOKENS = 128;  // its tile: tokens,
-constexpr int CH = 128;      // channels
-
-inline __host__ __device__ int chunks(int L) { return (L + TOKENS - 1) / TOKENS; }
+constexpr int CH = 128;     // channels of its tile
 
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
