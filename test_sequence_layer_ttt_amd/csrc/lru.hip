@@ -106,17 +106,28 @@ __global__ __launch_bounds__(NT) void lru_scan(LruArgs a, int nch, int ngr) {
     float A[V], H[V], At[U][V], Ht[U][V], rate[V];
     const bool in = c < a.D;
 #pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f, rate[v] = RATE && in ? a.rate[c + v] : 0.f;
+    for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f, rate[v] = 0.f;
+    if (RATE && in) load_rate<V>(a.rate + c, rate);
     const T *x = static_cast<const T *>(a.x) + b * a.xb + c, *r = static_cast<const T *>(a.r) + b * a.rb + c;
     const T *ig = a.i ? static_cast<const T *>(a.i) + b * a.ib + c : nullptr;
+    const bool some = in && t0 < n;
+    typename IO::Raw rx[U], rr[U], ri[U];
+    if (some) {  // all at once; rows past the sequence's end are read from its last
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t t = min(t0 + u, n - 1);
+            rx[u] = IO::raw(x + t * a.xt);
+            rr[u] = IO::raw(r + t * a.rt);
+            if (ig) ri[u] = IO::raw(ig + t * a.it);
+        }
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int t = t0 + u;
-        if (in && t < n) {
+        if (some && t0 + u < n) {
             float xv[V], rv[V], iv[V] = {}, d[V], w[V];
-            vec_load<T, V>(x + t * a.xt, xv);
-            vec_load<T, V>(r + t * a.rt, rv);
-            if (ig) vec_load<T, V>(ig + t * a.it, iv);
+            IO::unpack(rx[u], xv);
+            IO::unpack(rr[u], rv);
+            if (ig) IO::unpack(ri[u], iv);
             token<V, RATE>(xv, rv, iv, ig != nullptr, rate, d, w);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -186,10 +197,14 @@ __global__ __launch_bounds__(NT) void lru_scan(LruArgs a, int nch, int ngr) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int t = t0 + u;
-        float o[V];
+        float o[V] = {};
+        if (t < n) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = t < n ? fmaf(At[u][v], first[v], Ht[u][v]) : 0.f;
-        if (t < a.L) IO::store(y + t * a.yt, o);
+            for (int v = 0; v < V; ++v) o[v] = fmaf(At[u][v], first[v], Ht[u][v]);
+            IO::store(y + t * a.yt, o);
+        } else if (t < a.L) {
+            IO::store(y + t * a.yt, o);
+        }
     }
     if (a.state_out && k == nch - 1 && run == TG - 1) {
 #pragma unroll
@@ -216,7 +231,7 @@ __global__ __launch_bounds__(NT) void lru_step(LruArgs a) {
     vec_load<T, V>(static_cast<const T *>(a.r) + b * a.rb + c, rv);
     if (a.i) vec_load<T, V>(static_cast<const T *>(a.i) + b * a.ib + c, iv);
     vec_load<float, V>(a.state_out + b * a.D + c, h);
-    if constexpr (RATE) vec_load<float, V>(a.rate + c, rate);
+    if constexpr (RATE) load_rate<V>(a.rate + c, rate);
     token<V, RATE>(xv, rv, iv, a.i != nullptr, rate, d, u);
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = fmaf(d[v], h[v], u[v]);

@@ -48,28 +48,38 @@ namespace lru {
 constexpr int NT = 256;     // threads of a workgroup
 constexpr int CH = 128;     // channels of its tile
 
-__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+constexpr float LOG2E = 1.44269504f;
 
-// e^z and o = 1 - e^z for z <= 0. Where e^z is near 1, o comes from the series
-// (the next term is below 2^-25 of it at -0.1, where 1 - e^z is off by 2^-20.6
-// at most) and e^z from o.
-__device__ __forceinline__ float decay(float z, float *o) {
-    float p = fmaf(z, 1.0f / 5, 1.0f);
-    p = fmaf(z * 0.25f, p, 1.0f);
-    p = fmaf(z * (1.0f / 3), p, 1.0f);
-    p = fmaf(z * 0.5f, p, 1.0f);
-    const float e = fast_exp(z);
-    *o = z > -0.1f ? -z * p : 1.0f - e;
-    return z > -0.1f ? 1.0f - *o : e;
-}
-
-// sigma(v) and 1 - sigma(v)
-__device__ __forceinline__ float sigmoid2(float v, float *other) {
-    const float t = fast_exp(-fabsf(v)), d = __builtin_amdgcn_rcpf(1.0f + t), q = t * d;
-    *other = v >= 0.f ? q : d;
-    return v >= 0.f ? d : q;
-}
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * LOG2E); }
 __device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.0f + fast_exp(-v)); }
+// sigma(v) and 1 - sigma(v) = e^-v sigma(v), which is 1 where e^-v is out of the reciprocal's range
+__device__ __forceinline__ float sigmoid2(float v, float *other) {
+    const float t = fast_exp(-v), d = __builtin_amdgcn_rcpf(1.0f + t);
+    *other = t > 1e37f ? 1.0f : t * d;
+    return d;
+}
+
+// 2^z and o = 1 - 2^z for z <= 0. Where 2^z is near 1, o comes from the series of
+// 1 - e^(z ln 2) (the next term is below 2^-25 of it at -0.14, where 1 - 2^z is
+// off by 2^-20.6 at most) and 2^z from o.
+__device__ __forceinline__ float decay(float z, float *o) {
+    float p = fmaf(z, -1.33335581e-3f, -9.61812911e-3f);
+    p = fmaf(z, p, -5.55041087e-2f);
+    p = fmaf(z, p, -2.40226507e-1f);
+    p = fmaf(z, p, -6.93147181e-1f);
+    const float e = __builtin_amdgcn_exp2f(z);
+    const bool near = z > -0.14f;
+    *o = near ? z * p : 1.0f - e;
+    return near ? 1.0f - *o : e;
+}
+
+// V channels' rates, times log2(e); at any address (a few bytes, once a thread)
+template <int V> __device__ __forceinline__ void load_rate(const float *p, float (&rate)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) rate[v] = p[v];
+#pragma unroll
+    for (int v = 0; v < V; ++v) rate[v] *= LOG2E;
+}
 
 // What a token's gate comes to.
 struct Gate {
@@ -78,12 +88,12 @@ struct Gate {
     float g, ng; // with a rate: sigma(r), 1 - sigma(r)
 };
 
-// Rates are >= 0. A closed gate (r = -infinity) gives a = 1, o = s = 0.
-template <bool RATE> __device__ __forceinline__ Gate gate(float r, float rate) {
+// Rates are >= 0, and come times log2(e). A closed gate (r = -infinity) gives a = 1, o = s = 0.
+template <bool RATE> __device__ __forceinline__ Gate gate(float r, float rate2) {
     Gate k;
     if constexpr (RATE) {
         k.g = sigmoid2(r, &k.ng);
-        k.a = decay(-rate * k.g, &k.o);
+        k.a = decay(-rate2 * k.g, &k.o);
         k.s = __builtin_amdgcn_sqrtf(k.o * (2.0f - k.o));
     } else {
         k.a = sigmoid2(r, &k.o);

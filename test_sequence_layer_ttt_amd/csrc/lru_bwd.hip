@@ -48,7 +48,8 @@ __global__ __launch_bounds__(NT) void lru_bwd_shares(LruBwdArgs g) {
     const int t0 = tile * BT + run * U, t1 = min(t0 + U, n);
     float A[V], H[V], K[V], rate[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = K[v] = 0.f, rate[v] = RATE && c < a.D ? a.rate[c + v] : 0.f;
+    for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = K[v] = 0.f, rate[v] = 0.f;
+    if (RATE && c < a.D) load_rate<V>(a.rate + c, rate);
     if (c < a.D && t0 < t1) {
         const Rows<T> p(g, b, c);
         for (int t = t0; t < t1; ++t) {
@@ -133,7 +134,8 @@ __global__ __launch_bounds__(NT) void lru_bwd_grads(LruBwdArgs g) {
     float xv[U][V], dv[U][V], gi[U][V], ni[U][V];
     Gate k[U][V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = K[v] = 0.f, rate[v] = RATE && in ? a.rate[c + v] : 0.f;
+    for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = K[v] = 0.f, rate[v] = 0.f;
+    if (RATE && in) load_rate<V>(a.rate + c, rate);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int t = t0 + u;
@@ -224,7 +226,7 @@ __global__ __launch_bounds__(NT) void lru_bwd_grads(LruBwdArgs g) {
                 const float slope = q.s > 0.f ? q.a * q.a * __builtin_amdgcn_rcpf(q.s) : 0.f;
                 l = G * fmaf(q.a, hp[u][v], -e * x * slope);
                 dr[v] = fmaf(-l, q.g, dr[v]);
-                orr[v] = -l * rate[v] * q.g * q.ng;
+                orr[v] = -l * (rate[v] * 0.693147181f) * q.g * q.ng;
             } else {
                 l = G * q.a * (hp[u][v] - e * x);
                 orr[v] = l * q.o;
