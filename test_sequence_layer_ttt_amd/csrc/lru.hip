@@ -36,9 +36,11 @@ __device__ __forceinline__ void token(const float (&x)[V], const float (&r)[V], 
 // state behind it. So the order of the sums is fixed, and a prompt of n tiles is a
 // chain of n / GROUP links.
 //
-// Tiles wait for tiles: each takes its place in line by a counter as it starts,
-// all channels of a tile's tokens before the next tile's, so that whatever a
-// tile waits for has started before it and waits for earlier ones alone. A
+// Tiles wait for tiles of their own column (a sequence's 128 channels): each takes
+// its place by the column's counter as it starts, so that whatever a tile waits
+// for has started before it and waits for earlier ones alone. A counter for each
+// column, on lines of their own: one for all cost 8 ns a tile, one after the other.
+// A
 // published value carries its own flag: a word is ready where it is not all
 // ones (cleared to that before; a NaN of this very pattern is published as
 // another NaN). Words are written and read as single atomics at the scope of
@@ -54,14 +56,15 @@ struct Plan {
 };
 Plan plan(int B, int L, int D);
 
-// workspace: the counter, then the tiles' (A, H) [B][tiles][D], then the states behind groups [B][groups][D]
+// workspace: the columns' counters, then the tiles' (A, H) [B][tiles][D], then the states behind groups [B][groups][D]
+constexpr int LINE = 16;  // words
 struct Words {
-    uint32_t *ticket;
+    uint32_t *place;
     uint64_t *share;
     uint32_t *state;
-    __device__ __forceinline__ Words(float *ws, int64_t shares)
-        : ticket(reinterpret_cast<uint32_t *>(ws)), share(reinterpret_cast<uint64_t *>(ws + 4)),
-          state(reinterpret_cast<uint32_t *>(ws + 4 + 2 * shares)) {}
+    __device__ __forceinline__ Words(float *ws, int64_t columns, int64_t shares)
+        : place(reinterpret_cast<uint32_t *>(ws)), share(reinterpret_cast<uint64_t *>(ws + LINE * columns)),
+          state(reinterpret_cast<uint32_t *>(ws + LINE * columns + 2 * shares)) {}
 };
 template <typename W> __device__ __forceinline__ W peek(const W *p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -90,24 +93,23 @@ __global__ __launch_bounds__(NT) void lru_scan(LruArgs a, int nch, int ngr) {
     __shared__ float sfirst[CH];
     __shared__ uint32_t place;
     const int lane = threadIdx.x % CL, run = threadIdx.x / CL;
-    int b = blockIdx.z, k = blockIdx.x, cb = blockIdx.y;
-    const Words words(a.ws, static_cast<int64_t>(a.B) * nch * a.D);
-    if constexpr (MANY) {
-        if (threadIdx.x == 0) place = atomicAdd(words.ticket, 1u) + 1;  // from all ones on
-        __syncthreads();
-        const uint32_t ncb = gridDim.y, t = place;
-        cb = static_cast<int>(t % ncb);
-        b = static_cast<int>(t / ncb % a.B);
-        k = static_cast<int>(t / ncb / a.B);
-    }
+    // MANY: a grid of columns (the faster) by tiles; else of channels by sequences. Workgroups
+    // go to the XCDs round robin: each round starts a column further, so that an XCD does not
+    // keep to a few columns, whose lines lie in few of its L2's channels (32k prompt: 102 -> 95 us).
+    const int ncb = (a.D + CH - 1) / CH, ncol = ncb * a.B;
+    const int column = MANY ? (blockIdx.x + blockIdx.x / ncol) % ncol : 0;
+    const int cb = MANY ? column % ncb : blockIdx.x, b = MANY ? column / ncb : blockIdx.y;
+    const Words words(a.ws, static_cast<int64_t>(ncb) * a.B, static_cast<int64_t>(a.B) * nch * a.D);
+    if (MANY && threadIdx.x == 0) place = atomicAdd(words.place + LINE * column, 1u) + 1;  // from all ones on
     const int c0 = cb * CH, c = c0 + lane * V;
     const int n = live_tokens(a.lens, b, a.L);
-    const int t0 = (k * TG + run) * U;
     float A[V], H[V], At[U][V], Ht[U][V], rate[V];
     const bool in = c < a.D;
 #pragma unroll
     for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = 0.f, rate[v] = 0.f;
     if (RATE && in) load_rate<V>(a.rate + c, rate);
+    if constexpr (MANY) __syncthreads();
+    const int k = MANY ? static_cast<int>(place) : 0, t0 = (k * TG + run) * U;
     const T *x = static_cast<const T *>(a.x) + b * a.xb + c, *r = static_cast<const T *>(a.r) + b * a.rb + c;
     const T *ig = a.i ? static_cast<const T *>(a.i) + b * a.ib + c : nullptr;
     const bool some = in && t0 < n;
@@ -201,7 +203,7 @@ __global__ __launch_bounds__(NT) void lru_scan(LruArgs a, int nch, int ngr) {
         if (t < n) {
 #pragma unroll
             for (int v = 0; v < V; ++v) o[v] = fmaf(At[u][v], first[v], Ht[u][v]);
-            IO::store(y + t * a.yt, o);
+            stream_store<T, V>(y + t * a.yt, o);
         } else if (t < a.L) {
             IO::store(y + t * a.yt, o);
         }
@@ -259,14 +261,16 @@ Plan plan(int B, int L, int D) {
 
 template <typename T, int V, int U, bool RATE> hipError_t scan(const LruArgs &a, const Plan &p, hipStream_t s) {
     const int nch = static_cast<int>(p.tiles), ngr = static_cast<int>(p.groups);
-    const dim3 grid(nch, (a.D + CH - 1) / CH, a.B);
+    const int ncb = (a.D + CH - 1) / CH;
     if (nch > 1) {
+        const dim3 grid(static_cast<unsigned>(nch) * ncb * a.B);
+
         const int64_t words = lru_forward_floats(a.B, a.L, a.D) / 4;
         hipLaunchKernelGGL(lru_clear, dim3(static_cast<unsigned>((words + NT - 1) / NT)), dim3(NT), 0, s,
                            reinterpret_cast<uint4 *>(a.ws), words);
         hipLaunchKernelGGL((lru_scan<T, V, U, RATE, true>), grid, dim3(NT), 0, s, a, nch, ngr);
     } else {
-        hipLaunchKernelGGL((lru_scan<T, V, U, RATE, false>), grid, dim3(NT), 0, s, a, nch, ngr);
+        hipLaunchKernelGGL((lru_scan<T, V, U, RATE, false>), dim3(ncb, a.B), dim3(NT), 0, s, a, nch, ngr);
     }
     return hipGetLastError();
 }
@@ -306,8 +310,9 @@ template <typename T> hipError_t step_t(const LruArgs &a, hipStream_t s) {
 
 int64_t lru_forward_floats(int B, int L, int D) {
     const Plan p = plan(B, L, D);
+    const int64_t columns = (static_cast<int64_t>(D) + CH - 1) / CH * B;
     // in whole 16 bytes
-    return p.tiles > 1 ? (4 + (2 * p.tiles + p.groups) * B * D + 3) / 4 * 4 : 0;
+    return p.tiles > 1 ? (LINE * columns + (2 * p.tiles + p.groups) * B * D + 3) / 4 * 4 : 0;
 }
 hipError_t launch_lru_forward(const LruArgs &a, hipStream_t s) {
     return a.io ? forward_t<bf16_t>(a, s) : forward_t<float>(a, s);

@@ -87,6 +87,21 @@ __device__ __forceinline__ void vec_load(const T *p, float (&x)[V]) {
     VecIO<T, V>::unpack(VecIO<T, V>::raw(p), x);
 }
 
+// A store of 16 bytes that the chip's L2 need not keep: outputs larger than it, which only a
+// later kernel reads.
+template <typename T, int V> __device__ __forceinline__ void stream_store(T *p, const float (&x)[V]) {
+    typedef __attribute__((ext_vector_type(4))) unsigned u4;
+    if constexpr (V == 8 && sizeof(T) == 2) {
+        const u4 v = {tile::pack2(x[0], x[1]), tile::pack2(x[2], x[3]), tile::pack2(x[4], x[5]), tile::pack2(x[6], x[7])};
+        __builtin_nontemporal_store(v, reinterpret_cast<u4 *>(p));
+    } else if constexpr (V == 4 && sizeof(T) == 4) {
+        const u4 v = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+        __builtin_nontemporal_store(v, reinterpret_cast<u4 *>(p));
+    } else {
+        VecIO<T, V>::store(p, x);
+    }
+}
+
 // 1 / (1 + e^-s): e^-s overflows to infinity for very negative s and the
 // quotient is then 0, which is the limit.
 __device__ __forceinline__ float sigmoid_f(float s) { return __builtin_amdgcn_rcpf(1.0f + __expf(-s)); }
