@@ -157,6 +157,7 @@ View rows(const void *p, const char *name, int64_t n, int64_t inner, const int64
 int64_t padded(int K) { return (static_cast<int64_t>(K) + 127) / 128 * 128; }
 
 int quantised(int M, int K, int io, const void *x, int64_t xr, void *workspace, ttt::I8Args *a, hipStream_t stream) {
+    if (ttt::i8_features_in_one(*a)) return launched(ttt::launch_i8_features(*a, io, x, xr, stream));
     int8_t *q = static_cast<int8_t *>(workspace);
     float *scale = reinterpret_cast<float *>(q + static_cast<int64_t>(M) * padded(K));
     a->x = q;

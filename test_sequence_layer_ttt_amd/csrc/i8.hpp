@@ -35,5 +35,8 @@ struct I8Args {
 
 hipError_t launch_i8_quantize(const I8QuantArgs &a, hipStream_t stream);
 hipError_t launch_i8_project(const I8Args &a, hipStream_t stream);
+// from features x [M,K] of io, rows of xr (a.x, a.xr, a.xs unused), where in_one says so
+bool i8_features_in_one(const I8Args &a);
+hipError_t launch_i8_features(const I8Args &a, int io, const void *x, int64_t xr, hipStream_t stream);
 
 }  // namespace ttt

@@ -4,8 +4,8 @@
 // sum in fp32 and one rounding to y's type. Computed transposed, w as the A
 // operand of the 16x16x64 MFMA, so that a lane's four accumulators are four
 // consecutive features of one token.
-#include "i8.hpp"
-#include "tile.hpp"
+#include "i8_scale.hpp"
+#include "vec.hpp"
 
 namespace ttt {
 namespace {
@@ -39,35 +39,38 @@ __device__ __forceinline__ i32x4 load16(const int8_t *row, int k, int K) {
     return i32x4{static_cast<int>(d[0]), static_cast<int>(d[1]), static_cast<int>(d[2]), static_cast<int>(d[3])};
 }
 
-// features n .. n + 3 of token m
-__device__ __forceinline__ void store4(const I8Args &a, int m, int n, i32x4 acc) {
-    if (m >= a.M || n >= a.N) return;
-    const float sx = a.xs[m];
+// features n .. n + 3 of token m, whose scale is sx
+__device__ __forceinline__ void store4(const I8Args &a, int m, int n, float sx, i32x4 acc) {
     float o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int f = min(n + e, a.N - 1);
-        o[e] = static_cast<float>(acc[e]) * sx * a.ws[f];
-        if (a.bias) o[e] += a.bias[f];
+        o[e] = fmaf(static_cast<float>(acc[e]) * sx, a.ws[f], a.bias ? a.bias[f] : 0.f);
     }
-    if (a.H) {  // N is a multiple of 64: four features of one head
-        const int HD = a.H * 64, v = n / HD, hj = n - v * HD, b = m / a.L, t = m - b * a.L;
-        uint16_t *out = static_cast<uint16_t *>(v == 0 ? a.v[0] : v == 1 ? a.v[1] : a.v[2]);
-        out += ((static_cast<int64_t>(b) * a.H + hj / 64) * a.L + t) * 64 + hj % 64;
-        *reinterpret_cast<uint2 *>(out) = make_uint2(tile::pack2(o[0], o[1]), tile::pack2(o[2], o[3]));
-        return;
-    }
-    const int64_t at = m * a.yr + n;
+    const bool vec = a.vec && n + 4 <= a.N;
     if (a.out_io) {
-        uint16_t *y = static_cast<uint16_t *>(a.y) + at;
+        uint16_t *y = static_cast<uint16_t *>(a.y) + (m * a.yr + n);
+        if (a.H) {  // N is a multiple of 64: four features of one head
+            const int HD = a.H * 64, v = n / HD, hj = n - v * HD, b = m / a.L, t = m - b * a.L;
+            y = static_cast<uint16_t *>(v == 0 ? a.v[0] : v == 1 ? a.v[1] : a.v[2]);
+            y += ((static_cast<int64_t>(b) * a.H + hj / 64) * a.L + t) * 64 + hj % 64;
+        }
+        if (vec) {
+            *reinterpret_cast<uint2 *>(y) = make_uint2(tile::pack2(o[0], o[1]), tile::pack2(o[2], o[3]));
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (n + e < a.N) y[e] = f32_to_bf16(o[e]);
+            for (int e = 0; e < 4; ++e)
+                if (n + e < a.N) y[e] = f32_to_bf16(o[e]);
+        }
     } else {
-        float *y = static_cast<float *>(a.y) + at;
+        float *y = static_cast<float *>(a.y) + (m * a.yr + n);
+        if (vec) {
+            *reinterpret_cast<float4 *>(y) = make_float4(o[0], o[1], o[2], o[3]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (n + e < a.N) y[e] = o[e];
+            for (int e = 0; e < 4; ++e)
+                if (n + e < a.N) y[e] = o[e];
+        }
     }
 }
 
@@ -109,7 +112,125 @@ __global__ __launch_bounds__(256) void i8_any(I8Args a) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) store4(a, m0 + wt + 16 * j + c, n0 + wf + 16 * i + 4 * g, acc[i][j]);
+        for (int j = 0; j < 2; ++j) {
+            const int m = m0 + wt + 16 * j + c, n = n0 + wf + 16 * i + 4 * g;
+            if (m < a.M && n < a.N) store4(a, m, n, a.xs[m], acc[i][j]);
+        }
+}
+
+// Few tokens (M <= 16 MT): bound by reading w, and by latency. A workgroup takes
+// 16 features and all tokens; its 8 waves split K, each reads its part of w
+// straight into the MFMA's layout (lane (g, c): bytes 16 g .. of row c), and LDS
+// joins their sums. All of a wave's loads are asked for before the first product
+// (up to AHEAD contraction steps).
+constexpr int FW = 8, AHEAD = 4;
+
+// 16 bytes of a row from k on, zeros past K; whole chunks at 16-byte addresses or any
+template <bool CHUNKS> __device__ __forceinline__ i32x4 row16(const int8_t *row, int k, int K) {
+    if constexpr (CHUNKS)
+        return k < K ? *reinterpret_cast<const i32x4 *>(row + k) : i32x4{0, 0, 0, 0};
+    else
+        return load16(row, k, K);
+}
+
+// the waves' sums, and the outputs
+template <int MT> __device__ __forceinline__ void join(const I8Args &a, int n0, const i32x4 (&acc)[MT], i32x4 (*red)[MT][64],
+                                                       const float *xs) {
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) red[w][t][lane] = acc[t];
+    __syncthreads();
+    for (int t = w; t < MT; t += FW) {
+        i32x4 s = red[0][t][lane];
+#pragma unroll
+        for (int i = 1; i < FW; ++i) s += red[i][t][lane];
+        const int m = 16 * t + (lane & 15), n = n0 + 4 * (lane >> 4);
+        if (m < a.M && n < a.N) store4(a, m, n, xs[m], s);
+    }
+}
+
+template <int MT, bool CHUNKS> __global__ __launch_bounds__(64 * FW) void i8_few(I8Args a) {
+    __shared__ i32x4 red[FW][MT][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+    const int n0 = blockIdx.x * 16;
+    const int steps = (a.K + 63) / 64, per = (steps + FW - 1) / FW;
+    const int s0 = w * per, s1 = min(s0 + per, steps);
+    const int8_t *pw = a.w + static_cast<int64_t>(min(n0 + c, a.N - 1)) * a.wr;
+    const int8_t *px[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) px[t] = a.x + static_cast<int64_t>(min(16 * t + c, a.M - 1)) * a.xr;
+    i32x4 acc[MT] = {};
+    for (int s = s0; s < s1; s += AHEAD) {
+        i32x4 fw[AHEAD], fx[AHEAD][MT];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int k = s + i < s1 ? (s + i) * 64 + 16 * g : a.K;
+            fw[i] = row16<CHUNKS>(pw, k, a.K);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) fx[i][t] = row16<CHUNKS>(px[t], k, a.K);
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) acc[t] = mfma_i8(fw[i], fx[i][t], acc[t]);
+    }
+    join<MT>(a, n0, acc, red, a.xs);
+}
+
+// The same from features, for M <= 16: every workgroup quantises all rows into its
+// LDS (rows of `stride` bytes), W threads a row; that is M K values read from the
+// chip's caches and one launch less. Its first loads of w are under way meanwhile.
+template <typename T, int V, bool CHUNKS>
+__global__ __launch_bounds__(64 * FW) void i8_few_features(I8Args a, const T *x, int64_t xr, int W, int stride) {
+    typedef VecIO<T, V> IO;
+    extern __shared__ __attribute__((aligned(16))) int8_t sq[];
+    __shared__ i32x4 red[FW][1][64];
+    __shared__ uint32_t most[16];
+    __shared__ float scale[16];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+    const int n0 = blockIdx.x * 16;
+    const int steps = (a.K + 63) / 64, per = (steps + FW - 1) / FW;
+    const int s0 = w * per, s1 = min(s0 + per, steps);
+    const int8_t *pw = a.w + static_cast<int64_t>(min(n0 + c, a.N - 1)) * a.wr;
+    i32x4 fw[AHEAD];
+    auto ask = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) fw[i] = row16<CHUNKS>(pw, s + i < s1 ? (s + i) * 64 + 16 * g : a.K, a.K);
+    };
+    ask(s0);
+    if (threadIdx.x < 16) most[threadIdx.x] = 0;
+    __syncthreads();
+    const int at = threadIdx.x % W, first = threadIdx.x / W, rows = 64 * FW / W;
+    for (int m = first; m < a.M; m += rows) {  // the bits of the row's largest |x|
+        uint32_t mine = 0;
+        for (int k = at * V; k < a.K; k += W * V) {
+            float v[V];
+            vec_load<T, V>(x + m * xr + k, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) mine = max(mine, __float_as_uint(v[e]) & 0x7fffffffu);
+        }
+        atomicMax(&most[m], mine);
+    }
+    __syncthreads();
+    for (int m = first; m < a.M; m += rows) {
+        const Scale s(most[m]);
+        if (at == 0) scale[m] = s.s;
+        for (int k = at * V; k < a.K; k += W * V) {
+            float v[V];
+            vec_load<T, V>(x + m * xr + k, v);
+            s.put<V>(v, sq + m * stride + k);
+        }
+    }
+    __syncthreads();
+    const int8_t *px = sq + min(c, a.M - 1) * stride + 16 * g;  // past K: w's zeros
+    i32x4 acc[1] = {};
+    for (int s = s0; s < s1; s += AHEAD) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (s + i < s1) acc[0] = mfma_i8(fw[i], *reinterpret_cast<const i32x4 *>(px + (s + i) * 64), acc[0]);
+        if (s + AHEAD < s1) ask(s + AHEAD);
+    }
+    join<1>(a, n0, acc, red, scale);
 }
 
 // Where logical chunk j of row r of a half lies among its eight: j ^ key(r).
@@ -360,18 +481,52 @@ template <bool TAIL> __global__ __launch_bounds__(512, 2) void i8_big(I8Args a, 
     }
 }
 
+// bytes of a row of K in LDS: whole steps, and 16 more so that rows start in other banks
+inline int few_stride(int K) { return (K + 63) / 64 * 64 + 16; }
+
 bool aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// whole 16-byte chunks, at 16-byte addresses
+bool chunked(const int8_t *p, int64_t stride, int K) { return K % 16 == 0 && stride % 16 == 0 && aligned(p); }
+
+void outputs(I8Args &a) { a.vec = a.H || (aligned(a.y) && a.yr * (a.out_io ? 2 : 4) % 16 == 0); }
+
+template <int MT> hipError_t few(const I8Args &a, hipStream_t s) {
+    const dim3 grid((a.N + 15) / 16);
+    if (chunked(a.x, a.xr, a.K) && chunked(a.w, a.wr, a.K))
+        hipLaunchKernelGGL((i8_few<MT, true>), grid, dim3(64 * FW), 0, s, a);
+    else
+        hipLaunchKernelGGL((i8_few<MT, false>), grid, dim3(64 * FW), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t few_features(const I8Args &a, const void *in, int64_t xr, hipStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    const T *x = static_cast<const T *>(in);
+    const bool vec = a.K % V == 0 && xr % V == 0 && aligned(x), chunks = chunked(a.w, a.wr, a.K);
+    int W = 64 * FW;  // threads a row
+    while (W > 64 && (64 * FW / W) < a.M) W /= 2;
+    const int stride = few_stride(a.K);
+    const dim3 grid((a.N + 15) / 16);
+    const size_t lds = static_cast<size_t>(a.M) * stride;
+    if (vec && chunks)
+        hipLaunchKernelGGL((i8_few_features<T, V, true>), grid, dim3(64 * FW), lds, s, a, x, xr, W, stride);
+    else
+        hipLaunchKernelGGL((i8_few_features<T, 1, false>), grid, dim3(64 * FW), lds, s, a, x, xr, W, stride);
+    return hipGetLastError();
+}
 
 }  // namespace
 
 hipError_t launch_i8_project(const I8Args &in, hipStream_t s) {
     I8Args a = in;
-    a.vec = a.H || (aligned(a.y) && a.yr * (a.out_io ? 2 : 4) % 16 == 0);
-    // whole 16-byte chunks, and a tile's offsets in 32 bits
-    const bool chunks = a.K % 16 == 0 && a.xr % 16 == 0 && a.wr % 16 == 0 && aligned(a.x) && aligned(a.w) &&
-                        a.xr < (1 << 23) && a.wr < (1 << 23);
+    outputs(a);
+    if (a.M <= 16) return few<1>(a, s);
+    if (a.M <= 32) return few<2>(a, s);
+    if (a.M <= 64) return few<4>(a, s);
+    const bool big = chunked(a.x, a.xr, a.K) && chunked(a.w, a.wr, a.K) && a.xr < (1 << 23) && a.wr < (1 << 23);  // offsets in 32 bits
     const int nfb = (a.N + BT - 1) / BT, ntb = (a.M + BT - 1) / BT;
-    if (chunks && static_cast<int64_t>(nfb) * ntb >= 4) {
+    if (big) {
         const dim3 grid(static_cast<unsigned>(nfb * ntb));
         if (a.K % BK)
             hipLaunchKernelGGL(i8_big<true>, grid, dim3(512), 0, s, a, nfb, ntb);
@@ -382,6 +537,15 @@ hipError_t launch_i8_project(const I8Args &in, hipStream_t s) {
     const int64_t tiles = (static_cast<int64_t>(a.N) + GT - 1) / GT * ((static_cast<int64_t>(a.M) + GT - 1) / GT);
     hipLaunchKernelGGL(i8_any, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, s, a);
     return hipGetLastError();
+}
+
+// Up to 16 rows whose bytes fit beside the sums in 64 KB: one launch from the features.
+bool i8_features_in_one(const I8Args &a) { return a.M <= 16 && static_cast<int64_t>(a.M) * few_stride(a.K) <= 48 * 1024; }
+
+hipError_t launch_i8_features(const I8Args &in, int io, const void *x, int64_t xr, hipStream_t s) {
+    I8Args a = in;
+    outputs(a);
+    return io ? few_features<bf16_t>(a, x, xr, s) : few_features<float>(a, x, xr, s);
 }
 
 }  // namespace ttt
