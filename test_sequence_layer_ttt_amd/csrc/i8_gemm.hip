@@ -39,14 +39,29 @@ __device__ __forceinline__ i32x4 load16(const int8_t *row, int k, int K) {
     return i32x4{static_cast<int>(d[0]), static_cast<int>(d[1]), static_cast<int>(d[2]), static_cast<int>(d[3])};
 }
 
+// E features' scales and biases, asked for before they are needed (without a
+// branch, which would wait for them).
+template <int E> struct Features {
+    float ws[E], bias[E];
+    __device__ __forceinline__ Features(const I8Args &a, int n) {
+        const float *b = a.bias ? a.bias : a.ws;
+        const float with = a.bias ? 1.f : 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int f = min(n + e, a.N - 1);
+            ws[e] = a.ws[f];
+            bias[e] = b[f];
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) bias[e] = with != 0.f ? bias[e] : 0.f;
+    }
+};
+
 // features n .. n + 3 of token m, whose scale is sx
-__device__ __forceinline__ void store4(const I8Args &a, int m, int n, float sx, i32x4 acc) {
+__device__ __forceinline__ void store4(const I8Args &a, int m, int n, float sx, const Features<4> &f, i32x4 acc) {
     float o[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int f = min(n + e, a.N - 1);
-        o[e] = fmaf(static_cast<float>(acc[e]) * sx, a.ws[f], a.bias ? a.bias[f] : 0.f);
-    }
+    for (int e = 0; e < 4; ++e) o[e] = fmaf(static_cast<float>(acc[e]) * sx, f.ws[e], f.bias[e]);
     const bool vec = a.vec && n + 4 <= a.N;
     if (a.out_io) {
         uint16_t *y = static_cast<uint16_t *>(a.y) + (m * a.yr + n);
@@ -114,7 +129,7 @@ __global__ __launch_bounds__(256) void i8_any(I8Args a) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int m = m0 + wt + 16 * j + c, n = n0 + wf + 16 * i + 4 * g;
-            if (m < a.M && n < a.N) store4(a, m, n, a.xs[m], acc[i][j]);
+            if (m < a.M && n < a.N) store4(a, m, n, a.xs[m], Features<4>(a, n), acc[i][j]);
         }
 }
 
@@ -133,48 +148,56 @@ template <bool CHUNKS> __device__ __forceinline__ i32x4 row16(const int8_t *row,
         return load16(row, k, K);
 }
 
-// the waves' sums, and the outputs
-template <int MT> __device__ __forceinline__ void join(const I8Args &a, int n0, const i32x4 (&acc)[MT], i32x4 (*red)[MT][64],
-                                                       const float *xs) {
+// The waves' sums of NT tiles; wave w < NT gets tile w's.
+template <int NT> __device__ __forceinline__ i32x4 join(const i32x4 (&acc)[NT], i32x4 (*red)[NT][64]) {
+    static_assert(NT <= FW, "a tile for each wave at most");
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
-    for (int t = 0; t < MT; ++t) red[w][t][lane] = acc[t];
+    for (int t = 0; t < NT; ++t) red[w][t][lane] = acc[t];
     __syncthreads();
-    for (int t = w; t < MT; t += FW) {
-        i32x4 s = red[0][t][lane];
+    i32x4 s = {};
+    if (w < NT) {
 #pragma unroll
-        for (int i = 1; i < FW; ++i) s += red[i][t][lane];
-        const int m = 16 * t + (lane & 15), n = n0 + 4 * (lane >> 4);
-        if (m < a.M && n < a.N) store4(a, m, n, xs[m], s);
+        for (int i = 0; i < FW; ++i) s += red[i][w][lane];
     }
+    return s;
 }
 
-template <int MT, bool CHUNKS> __global__ __launch_bounds__(64 * FW) void i8_few(I8Args a) {
-    __shared__ i32x4 red[FW][MT][64];
+// FT x MT tiles of 16 features x 16 tokens
+template <int FT, int MT, bool CHUNKS> __global__ __launch_bounds__(64 * FW) void i8_few(I8Args a) {
+    __shared__ i32x4 red[FW][FT * MT][64];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
-    const int n0 = blockIdx.x * 16;
+    const int n0 = blockIdx.x * 16 * FT;
     const int steps = (a.K + 63) / 64, per = (steps + FW - 1) / FW;
     const int s0 = w * per, s1 = min(s0 + per, steps);
-    const int8_t *pw = a.w + static_cast<int64_t>(min(n0 + c, a.N - 1)) * a.wr;
-    const int8_t *px[MT];
+    const int8_t *pw[FT], *px[MT];
+#pragma unroll
+    for (int f = 0; f < FT; ++f) pw[f] = a.w + static_cast<int64_t>(min(n0 + 16 * f + c, a.N - 1)) * a.wr;
 #pragma unroll
     for (int t = 0; t < MT; ++t) px[t] = a.x + static_cast<int64_t>(min(16 * t + c, a.M - 1)) * a.xr;
-    i32x4 acc[MT] = {};
+    const int n = n0 + 16 * (w / MT) + 4 * g, m = 16 * (w % MT) + c;  // the wave's outputs, w < FT MT
+    const Features<4> four(a, n);
+    const float sx = a.xs[min(m, a.M - 1)];
+    i32x4 acc[FT * MT] = {};
     for (int s = s0; s < s1; s += AHEAD) {
-        i32x4 fw[AHEAD], fx[AHEAD][MT];
+        i32x4 fw[AHEAD][FT], fx[AHEAD][MT];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int k = s + i < s1 ? (s + i) * 64 + 16 * g : a.K;
-            fw[i] = row16<CHUNKS>(pw, k, a.K);
+#pragma unroll
+            for (int f = 0; f < FT; ++f) fw[i][f] = row16<CHUNKS>(pw[f], k, a.K);
 #pragma unroll
             for (int t = 0; t < MT; ++t) fx[i][t] = row16<CHUNKS>(px[t], k, a.K);
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
-            for (int t = 0; t < MT; ++t) acc[t] = mfma_i8(fw[i], fx[i][t], acc[t]);
+            for (int f = 0; f < FT; ++f)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) acc[f * MT + t] = mfma_i8(fw[i][f], fx[i][t], acc[f * MT + t]);
     }
-    join<MT>(a, n0, acc, red, a.xs);
+    const i32x4 sum = join<FT * MT>(acc, red);
+    if (w < FT * MT && m < a.M && n < a.N) store4(a, m, n, sx, four, sum);
 }
 
 // The same from features, for M <= 16: every workgroup quantises all rows into its
@@ -182,7 +205,6 @@ template <int MT, bool CHUNKS> __global__ __launch_bounds__(64 * FW) void i8_few
 // chip's caches and one launch less. Its first loads of w are under way meanwhile.
 template <typename T, int V, bool CHUNKS>
 __global__ __launch_bounds__(64 * FW) void i8_few_features(I8Args a, const T *x, int64_t xr, int W, int stride) {
-    typedef VecIO<T, V> IO;
     extern __shared__ __attribute__((aligned(16))) int8_t sq[];
     __shared__ i32x4 red[FW][1][64];
     __shared__ uint32_t most[16];
@@ -198,6 +220,8 @@ __global__ __launch_bounds__(64 * FW) void i8_few_features(I8Args a, const T *x,
         for (int i = 0; i < AHEAD; ++i) fw[i] = row16<CHUNKS>(pw, s + i < s1 ? (s + i) * 64 + 16 * g : a.K, a.K);
     };
     ask(s0);
+    const int n = n0 + 4 * g;
+    const Features<4> four(a, n);
     if (threadIdx.x < 16) most[threadIdx.x] = 0;
     __syncthreads();
     const int at = threadIdx.x % W, first = threadIdx.x / W, rows = 64 * FW / W;
@@ -230,7 +254,8 @@ __global__ __launch_bounds__(64 * FW) void i8_few_features(I8Args a, const T *x,
             if (s + i < s1) acc[0] = mfma_i8(fw[i], *reinterpret_cast<const i32x4 *>(px + (s + i) * 64), acc[0]);
         if (s + AHEAD < s1) ask(s + AHEAD);
     }
-    join<1>(a, n0, acc, red, scale);
+    const i32x4 sum = join<1>(acc, red);
+    if (w == 0 && c < a.M && n < a.N) store4(a, c, n, scale[c], four, sum);
 }
 
 // Where logical chunk j of row r of a half lies among its eight: j ^ key(r).
@@ -250,13 +275,7 @@ __device__ __forceinline__ void tile_of(int id, int nfb, int ntb, int *fb, int *
 // A lane's 16 consecutive features from n on, of the tokens that `each` puts.
 template <typename F> __device__ __forceinline__ void store_rows(const I8Args &a, int n, F each) {
     if (n >= a.N) return;
-    float ws[16], bias[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        const int f = min(n + e, a.N - 1);
-        ws[e] = a.ws[f];
-        bias[e] = a.bias ? a.bias[f] : 0.f;
-    }
+    const Features<16> f(a, n);
     const bool vec = a.vec && n + 16 <= a.N;
     each([&](int m, auto acc) {
         if (m >= a.M) return;
@@ -266,7 +285,7 @@ template <typename F> __device__ __forceinline__ void store_rows(const I8Args &a
         for (int t = 0; t < 4; ++t) {
             const i32x4 v = acc(t);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[4 * t + e] = fmaf(static_cast<float>(v[e]) * sx, ws[4 * t + e], bias[4 * t + e]);
+            for (int e = 0; e < 4; ++e) o[4 * t + e] = fmaf(static_cast<float>(v[e]) * sx, f.ws[4 * t + e], f.bias[4 * t + e]);
         }
         uint16_t *y16;
         if (a.H) {  // 16 features of one head
@@ -491,12 +510,12 @@ bool chunked(const int8_t *p, int64_t stride, int K) { return K % 16 == 0 && str
 
 void outputs(I8Args &a) { a.vec = a.H || (aligned(a.y) && a.yr * (a.out_io ? 2 : 4) % 16 == 0); }
 
-template <int MT> hipError_t few(const I8Args &a, hipStream_t s) {
-    const dim3 grid((a.N + 15) / 16);
+template <int FT, int MT> hipError_t few(const I8Args &a, hipStream_t s) {
+    const dim3 grid((a.N + 16 * FT - 1) / (16 * FT));
     if (chunked(a.x, a.xr, a.K) && chunked(a.w, a.wr, a.K))
-        hipLaunchKernelGGL((i8_few<MT, true>), grid, dim3(64 * FW), 0, s, a);
+        hipLaunchKernelGGL((i8_few<FT, MT, true>), grid, dim3(64 * FW), 0, s, a);
     else
-        hipLaunchKernelGGL((i8_few<MT, false>), grid, dim3(64 * FW), 0, s, a);
+        hipLaunchKernelGGL((i8_few<FT, MT, false>), grid, dim3(64 * FW), 0, s, a);
     return hipGetLastError();
 }
 
@@ -521,9 +540,9 @@ template <typename T> hipError_t few_features(const I8Args &a, const void *in, i
 hipError_t launch_i8_project(const I8Args &in, hipStream_t s) {
     I8Args a = in;
     outputs(a);
-    if (a.M <= 16) return few<1>(a, s);
-    if (a.M <= 32) return few<2>(a, s);
-    if (a.M <= 64) return few<4>(a, s);
+    if (a.M <= 16) return few<1, 1>(a, s);
+    if (a.M <= 32) return few<1, 2>(a, s);
+    if (a.M <= 64) return a.N >= 4096 ? few<2, 4>(a, s) : few<1, 4>(a, s);
     const bool big = chunked(a.x, a.xr, a.K) && chunked(a.w, a.wr, a.K) && a.xr < (1 << 23) && a.wr < (1 << 23);  // offsets in 32 bits
     const int nfb = (a.N + BT - 1) / BT, ntb = (a.M + BT - 1) / BT;
     if (big) {
