@@ -26,12 +26,25 @@ __device__ __forceinline__ int live_tokens(const int *lens, int b, int L) {
     return lens ? max(0, min(lens[b], L)) : L;
 }
 
-template <typename T> struct Rows {
-    const T *x, *r, *i, *dy;
-    __device__ __forceinline__ Rows(const LruBwdArgs &g, int b, int c)
-        : x(static_cast<const T *>(g.f.x) + b * g.f.xb + c), r(static_cast<const T *>(g.f.r) + b * g.f.rb + c),
-          i(g.f.i ? static_cast<const T *>(g.f.i) + b * g.f.ib + c : nullptr),
-          dy(static_cast<const T *>(g.dy) + b * g.dyb + c) {}
+// U tokens of V channels as stored, all asked for at once; rows past the
+// sequence's end are read from its last.
+template <typename T, int V, int U> struct Tokens {
+    typename VecIO<T, V>::Raw x[U], r[U], i[U], dy[U];
+    bool gated;
+    __device__ __forceinline__ Tokens(const LruBwdArgs &g, int b, int c, int t0, int n) : gated(g.f.i != nullptr) {
+        const LruArgs &a = g.f;
+        const T *px = static_cast<const T *>(a.x) + b * a.xb + c, *pr = static_cast<const T *>(a.r) + b * a.rb + c,
+                *pd = static_cast<const T *>(g.dy) + b * g.dyb + c, *pi = static_cast<const T *>(a.i) + b * a.ib + c;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t t = min(t0 + u, n - 1);
+            x[u] = VecIO<T, V>::raw(px + t * a.xt);
+            r[u] = VecIO<T, V>::raw(pr + t * a.rt);
+            dy[u] = VecIO<T, V>::raw(pd + t * g.dyt);
+            if (gated) i[u] = VecIO<T, V>::raw(pi + t * a.it);
+        }
+    }
+    Tokens() = default;
 };
 
 // Each tile's decay A, its own share H of the state behind it and its own
@@ -45,25 +58,27 @@ __global__ __launch_bounds__(NT) void lru_bwd_shares(LruBwdArgs g) {
     const int lane = threadIdx.x % CL, run = threadIdx.x / CL;
     const int b = blockIdx.z, tile = blockIdx.x, c0 = blockIdx.y * CH, c = c0 + lane * V;
     const int n = live_tokens(a.lens, b, a.L);
-    const int t0 = tile * BT + run * U, t1 = min(t0 + U, n);
+    const int t0 = tile * BT + run * U;
     float A[V], H[V], K[V], rate[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = K[v] = 0.f, rate[v] = 0.f;
     if (RATE && c < a.D) load_rate<V>(a.rate + c, rate);
-    if (c < a.D && t0 < t1) {
-        const Rows<T> p(g, b, c);
-        for (int t = t0; t < t1; ++t) {
+    if (c < a.D && t0 < n) {
+        const Tokens<T, V, U> p(g, b, c, t0, n);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t0 + u >= n) break;
             float xv[V], rv[V], iv[V] = {}, dv[V];
-            vec_load<T, V>(p.x + t * a.xt, xv);
-            vec_load<T, V>(p.r + t * a.rt, rv);
-            vec_load<T, V>(p.dy + t * g.dyt, dv);
-            if (p.i) vec_load<T, V>(p.i + t * a.it, iv);
+            VecIO<T, V>::unpack(p.x[u], xv);
+            VecIO<T, V>::unpack(p.r[u], rv);
+            VecIO<T, V>::unpack(p.dy[u], dv);
+            if (p.gated) VecIO<T, V>::unpack(p.i[u], iv);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const Gate k = gate<RATE>(rv[v], rate[v]);
-                float u = k.s * xv[v];
-                if (p.i) u *= sigmoid(iv[v]);
-                H[v] = fmaf(k.a, H[v], u);
+                float w = k.s * xv[v];
+                if (p.gated) w *= sigmoid(iv[v]);
+                H[v] = fmaf(k.a, H[v], w);
                 A[v] *= k.a;
                 K[v] = fmaf(A[v], dv[v], K[v]);
             }
@@ -92,28 +107,58 @@ __global__ __launch_bounds__(NT) void lru_bwd_shares(LruBwdArgs g) {
     }
 }
 
-// The state before each tile over its H, and what flows into it from behind over its K.
-__global__ __launch_bounds__(NT) void lru_bwd_carry(LruBwdArgs g) {
+// The state before each tile over its H (z = 0), and what flows into it from
+// behind over its K (z = 1, the tiles from the last on). 32 channels by 16 runs of
+// tiles: a run's (A, H) from its tiles, the runs before it from LDS, then its tiles
+// again.
+constexpr int CC = 32, CR = 16;
+
+__global__ __launch_bounds__(CC *CR) void lru_bwd_carry(LruBwdArgs g) {
+    __shared__ float2 sm[CR][CC];
     const LruArgs &a = g.f;
-    const int c = blockIdx.x * NT + threadIdx.x, b = blockIdx.y, n = tiles(a.L);
-    if (c >= a.D) return;
-    const int64_t row = static_cast<int64_t>(b) * a.D + c, D = a.D;
-    float *w = a.ws + static_cast<int64_t>(b) * n * 3 * D + c;
-    if (blockIdx.z == 0) {
-        float h = a.state ? a.state[row] : 0.f;
-        for (int k = 0; k < n; ++k, w += 3 * D) {
-            const float A = w[0], H = w[D];
-            w[D] = h;
-            h = fmaf(A, h, H);
+    const int lane = threadIdx.x % CC, run = threadIdx.x / CC, b = blockIdx.y, n = tiles(a.L);
+    const int c = blockIdx.x * CC + lane, per = (n + CR - 1) / CR, k0 = min(run * per, n), k1 = min(k0 + per, n);
+    const int64_t D = a.D, row = b * D + c;
+    const bool back = blockIdx.z != 0, in = c < D;
+    const int64_t step = back ? -3 * D : 3 * D;
+    float *w = a.ws + (static_cast<int64_t>(b) * n + (back ? n - 1 - k0 : k0)) * 3 * D + c;
+    const int64_t h = back ? 2 * D : D;
+    constexpr int AHEAD = 8;
+    float2 own = make_float2(1.f, 0.f);
+    if (in) {
+        for (int k = k0; k < k1; k += AHEAD) {
+            float A[AHEAD], H[AHEAD];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const float *p = w + (min(k + u, k1 - 1) - k0) * step;
+                A[u] = p[0];
+                H[u] = p[h];
+            }
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                if (k + u < k1) own = make_float2(own.x * A[u], fmaf(A[u], own.y, H[u]));
         }
-    } else {
-        float q = g.dstate_out ? g.dstate_out[row] : 0.f;
-        w += 3 * D * (n - 1);
-        for (int k = 0; k < n; ++k, w -= 3 * D) {
-            const float A = w[0], K = w[2 * D];
-            w[2 * D] = q;
-            q = fmaf(A, q, K);
+    }
+    sm[run][lane] = own;
+    __syncthreads();
+    if (!in) return;
+    const float *from = back ? g.dstate_out : a.state;
+    float q = from ? from[row] : 0.f;
+    for (int i = 0; i < run; ++i) q = fmaf(sm[i][lane].x, q, sm[i][lane].y);
+    for (int k = k0; k < k1; k += AHEAD) {
+        float A[AHEAD], H[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const float *p = w + (min(k + u, k1 - 1) - k0) * step;
+            A[u] = p[0];
+            H[u] = p[h];
         }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (k + u < k1) {
+                w[(k + u - k0) * step + h] = q;
+                q = fmaf(A[u], q, H[u]);
+            }
     }
 }
 
@@ -129,40 +174,36 @@ __global__ __launch_bounds__(NT) void lru_bwd_grads(LruBwdArgs g) {
     const int n = live_tokens(a.lens, b, a.L), nt = tiles(a.L);
     const int t0 = tile * BT + run * U;
     const bool in = c < a.D;
-    const Rows<T> p(g, b, c);
-    float A[V], H[V], K[V], rate[V];
-    float xv[U][V], dv[U][V], gi[U][V], ni[U][V];
-    Gate k[U][V];
+    // held from here to the way back: the rows as stored, and of each value the decay, the scale
+    // and the state before it; the gates' own values are cheaper formed again
+    float A[V], H[V], K[V], rate[V], da[U][V], ds[U][V], hp[U][V];
+    Tokens<T, V, U> p;
 #pragma unroll
     for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = K[v] = 0.f, rate[v] = 0.f;
+    const bool some = in && t0 < n;
     if (RATE && in) load_rate<V>(a.rate + c, rate);
+    if (some) p = Tokens<T, V, U>(g, b, c, t0, n);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int t = t0 + u;
-        if (in && t < n) {
-            float rv[V], iv[V] = {};
-            vec_load<T, V>(p.x + t * a.xt, xv[u]);
-            vec_load<T, V>(p.r + t * a.rt, rv);
-            vec_load<T, V>(p.dy + t * g.dyt, dv[u]);
-            if (p.i) vec_load<T, V>(p.i + t * a.it, iv);
+#pragma unroll
+        for (int v = 0; v < V; ++v) hp[u][v] = H[v], da[u][v] = 1.f, ds[u][v] = 0.f;
+        if (some && t0 + u < n) {
+            float xv[V], rv[V], iv[V] = {}, dv[V];
+            IO::unpack(p.x[u], xv);
+            IO::unpack(p.r[u], rv);
+            IO::unpack(p.dy[u], dv);
+            if (p.gated) IO::unpack(p.i[u], iv);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                k[u][v] = gate<RATE>(rv[v], rate[v]);
-                gi[u][v] = 1.f, ni[u][v] = 0.f;
-                if (p.i) gi[u][v] = sigmoid2(iv[v], &ni[u][v]);
+                const Gate k = gate<RATE>(rv[v], rate[v]);
+                da[u][v] = k.a;
+                ds[u][v] = k.s;
+                float w = k.s * xv[v];
+                if (p.gated) w *= sigmoid(iv[v]);
+                H[v] = fmaf(k.a, H[v], w);
+                A[v] *= k.a;
+                K[v] = fmaf(A[v], dv[v], K[v]);
             }
-        } else {  // leaves the state and the gradients as they are
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                k[u][v] = Gate{1.f, 0.f, 0.f, 0.f, 0.f};
-                xv[u][v] = dv[u][v] = gi[u][v] = ni[u][v] = 0.f;
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            H[v] = fmaf(k[u][v].a, H[v], k[u][v].s * gi[u][v] * xv[u][v]);
-            A[v] *= k[u][v].a;
-            K[v] = fmaf(A[v], dv[u][v], K[v]);
         }
     }
 #pragma unroll
@@ -193,18 +234,16 @@ __global__ __launch_bounds__(NT) void lru_bwd_grads(LruBwdArgs g) {
         }
     }
     __syncthreads();
-    float hp[U][V], dr[V] = {};
+    float dr[V] = {};
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        H[v] = sm[run][lane * V + v].y;
+        const float first = sm[run][lane * V + v].y;
+        float P = 1.f;
         K[v] = smk[run][lane * V + v];
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            hp[u][v] = H[v];
-            H[v] = fmaf(k[u][v].a, H[v], k[u][v].s * gi[u][v] * xv[u][v]);
+        for (int u = 0; u < U; ++u) {  // the state before each token, from the run's own share
+            hp[u][v] = fmaf(P, first, hp[u][v]);
+            P *= da[u][v];
         }
     }
     T *dx = static_cast<T *>(g.dx) + b * g.dxb + c, *drp = static_cast<T *>(g.dr) + b * g.drb + c;
@@ -212,30 +251,42 @@ __global__ __launch_bounds__(NT) void lru_bwd_grads(LruBwdArgs g) {
 #pragma unroll
     for (int u = U - 1; u >= 0; --u) {
         const int t = t0 + u;
-        float ox[V], orr[V], oi[V];
+        float ox[V] = {}, orr[V] = {}, oi[V] = {};
+        if (some && t < n) {
+            float xv[V], rv[V], iv[V] = {}, dv[V];
+            IO::unpack(p.x[u], xv);
+            IO::unpack(p.dy[u], dv);
+            if (RATE) IO::unpack(p.r[u], rv);
+            if (p.gated) IO::unpack(p.i[u], iv);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const Gate q = k[u][v];
-            const float G = dv[u][v] + K[v], x = xv[u][v], e = gi[u][v];
-            K[v] = q.a * G;
-            const float gs = G * q.s;
-            ox[v] = gs * e;
-            oi[v] = gs * x * e * ni[u][v];
-            float l;
-            if constexpr (RATE) {
-                const float slope = q.s > 0.f ? q.a * q.a * __builtin_amdgcn_rcpf(q.s) : 0.f;
-                l = G * fmaf(q.a, hp[u][v], -e * x * slope);
-                dr[v] = fmaf(-l, q.g, dr[v]);
-                orr[v] = -l * (rate[v] * 0.693147181f) * q.g * q.ng;
-            } else {
-                l = G * q.a * (hp[u][v] - e * x);
-                orr[v] = l * q.o;
+            for (int v = 0; v < V; ++v) {
+                const float at = da[u][v], st = ds[u][v], G = dv[v] + K[v], gs = G * st;
+                K[v] = at * G;
+                float x = xv[v];  // sigma(i) x
+                ox[v] = gs;
+                if (p.gated) {
+                    float ne;
+                    const float e = sigmoid2(iv[v], &ne);
+                    x *= e;
+                    ox[v] = gs * e;
+                    oi[v] = gs * x * ne;
+                }
+                if constexpr (RATE) {
+                    float ng;
+                    const float q = sigmoid2(rv[v], &ng);
+                    const float slope = st > 0.f ? at * at * __builtin_amdgcn_rcpf(st) : 0.f;
+                    const float lg = G * fmaf(at, hp[u][v], -x * slope) * q;
+                    dr[v] -= lg;
+                    orr[v] = -lg * (rate[v] * 0.693147181f) * ng;
+                } else {
+                    orr[v] = G * at * (hp[u][v] - x) * st;
+                }
             }
         }
         if (in && t < a.L) {
-            IO::store(dx + t * g.dxt, ox);
-            IO::store(drp + t * g.drt, orr);
-            if (di) IO::store(di + t * g.dit, oi);
+            stream_store<T, V>(dx + t * g.dxt, ox);
+            stream_store<T, V>(drp + t * g.drt, orr);
+            if (di) stream_store<T, V>(di + t * g.dit, oi);
         }
     }
     if (in && g.dstate && tile == 0 && run == 0) {
@@ -277,7 +328,7 @@ template <typename T, int V, bool RATE> hipError_t backward(const LruBwdArgs &g,
         const dim3 grid(nt, (a.D + CH - 1) / CH, a.B);
         if (nt > 1) {
             hipLaunchKernelGGL((lru_bwd_shares<T, V, RATE>), grid, dim3(NT), 0, s, g);
-            hipLaunchKernelGGL(lru_bwd_carry, dim3((a.D + NT - 1) / NT, a.B, 2), dim3(NT), 0, s, g);
+            hipLaunchKernelGGL(lru_bwd_carry, dim3((a.D + CC - 1) / CC, a.B, 2), dim3(CC * CR), 0, s, g);
         }
         hipLaunchKernelGGL((lru_bwd_grads<T, V, RATE>), grid, dim3(NT), 0, s, g);
     }
