@@ -272,54 +272,47 @@ __device__ __forceinline__ void tile_of(int id, int nfb, int ntb, int *fb, int *
     *tb = k / n;
 }
 
-// A lane's 16 consecutive features from n on, of the tokens that `each` puts.
-template <typename F> __device__ __forceinline__ void store_rows(const I8Args &a, int n, F each) {
-    if (n >= a.N) return;
-    const Features<16> f(a, n);
+// A lane's 16 consecutive features n .. of token m, four accumulators acc(0 .. 3).
+template <typename F> __device__ __forceinline__ void store16(const I8Args &a, int m, int n, float sx, const Features<16> &f, F acc) {
+    if (m >= a.M || n >= a.N) return;
     const bool vec = a.vec && n + 16 <= a.N;
-    each([&](int m, auto acc) {
-        if (m >= a.M) return;
-        const float sx = a.xs[m];
-        float o[16];
+    float o[16];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const i32x4 v = acc(t);
+    for (int t = 0; t < 4; ++t) {
+        const i32x4 v = acc(t);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[4 * t + e] = fmaf(static_cast<float>(v[e]) * sx, f.ws[4 * t + e], f.bias[4 * t + e]);
-        }
-        uint16_t *y16;
+        for (int e = 0; e < 4; ++e) o[4 * t + e] = fmaf(static_cast<float>(v[e]) * sx, f.ws[4 * t + e], f.bias[4 * t + e]);
+    }
+    if (a.out_io) {
+        uint16_t *y = static_cast<uint16_t *>(a.y) + (m * a.yr + n);
         if (a.H) {  // 16 features of one head
             const int HD = a.H * 64, v = n / HD, hj = n - v * HD, b = m / a.L, t = m - b * a.L;
-            y16 = static_cast<uint16_t *>(v == 0 ? a.v[0] : v == 1 ? a.v[1] : a.v[2]);
-            y16 += ((static_cast<int64_t>(b) * a.H + hj / 64) * a.L + t) * 64 + hj % 64;
-        } else {
-            y16 = static_cast<uint16_t *>(a.y) + (m * a.yr + n);
+            y = static_cast<uint16_t *>(v == 0 ? a.v[0] : v == 1 ? a.v[1] : a.v[2]);
+            y += ((static_cast<int64_t>(b) * a.H + hj / 64) * a.L + t) * 64 + hj % 64;
         }
-        if (a.out_io) {
-            if (vec) {
+        if (vec) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    reinterpret_cast<uint4 *>(y16)[h] =
-                        make_uint4(tile::pack2(o[8 * h], o[8 * h + 1]), tile::pack2(o[8 * h + 2], o[8 * h + 3]),
-                                   tile::pack2(o[8 * h + 4], o[8 * h + 5]), tile::pack2(o[8 * h + 6], o[8 * h + 7]));
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (n + e < a.N) y16[e] = f32_to_bf16(o[e]);
-            }
+            for (int h = 0; h < 2; ++h)
+                reinterpret_cast<uint4 *>(y)[h] =
+                    make_uint4(tile::pack2(o[8 * h], o[8 * h + 1]), tile::pack2(o[8 * h + 2], o[8 * h + 3]),
+                               tile::pack2(o[8 * h + 4], o[8 * h + 5]), tile::pack2(o[8 * h + 6], o[8 * h + 7]));
         } else {
-            float *y = static_cast<float *>(a.y) + (m * a.yr + n);
-            if (vec) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    reinterpret_cast<float4 *>(y)[t] = make_float4(o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (n + e < a.N) y[e] = o[e];
-            }
+            for (int e = 0; e < 16; ++e)
+                if (n + e < a.N) y[e] = f32_to_bf16(o[e]);
         }
-    });
+    } else {
+        float *y = static_cast<float *>(a.y) + (m * a.yr + n);
+        if (vec) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                reinterpret_cast<float4 *>(y)[t] = make_float4(o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (n + e < a.N) y[e] = o[e];
+        }
+    }
 }
 
 // Large products: a workgroup of 8 waves takes 256 features x 256 tokens.
@@ -486,18 +479,22 @@ template <bool TAIL> __global__ __launch_bounds__(512, 2) void i8_big(I8Args a, 
         if (k + 1 < nk) step(k + 1, 1);
     }
     if (!wr) section_end();
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // the loads behind the last step
-
+    // all scales at once, with the loads behind the last step
+    const Features<16> f[2] = {{a, n0 + 64 * wr + 16 * g}, {a, n0 + 128 + 64 * wr + 16 * g}};
+    float sx[2][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int n = n0 + 128 * i + 64 * wr + 16 * g;  // the lane's 16 features
-        store_rows(a, n, [&](auto put) {
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+        for (int s = 0; s < 2; ++s) sx[j][s] = a.xs[min(m0 + 128 * j + 32 * wc + 16 * s + c, a.M - 1)];
+    __builtin_amdgcn_s_waitcnt(0x0F70);
 #pragma unroll
-                for (int s = 0; s < 2; ++s) put(m0 + 128 * j + 32 * wc + 16 * s + c, [&](int t) { return acc[i][j][t][s]; });
-        });
-    }
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                store16(a, m0 + 128 * j + 32 * wc + 16 * s + c, n0 + 128 * i + 64 * wr + 16 * g, sx[j][s], f[i],
+                        [&](int t) { return acc[i][j][t][s]; });
 }
 
 // bytes of a row of K in LDS: whole steps, and 16 more so that rows start in other banks

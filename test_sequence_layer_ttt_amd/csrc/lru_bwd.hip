@@ -14,13 +14,15 @@ namespace {
 
 using namespace lru;
 
-constexpr int BT = 64;  // tokens of a tile
-
-template <int V> struct Tile {
-    static constexpr int CL = CH / V, TG = NT / CL, U = BT / TG;
-};
-
-inline __host__ __device__ int tiles(int L) { return (L + BT - 1) / BT; }
+// A tile's tokens: 64 where that leaves four workgroups for each compute unit, 32 or
+// 16 otherwise, and 32 at most for widths that no vector divides (a thread's run is
+// twice as long there).
+int tile_tokens(int B, int L, int D) {
+    const int64_t wide = (static_cast<int64_t>(D) + CH - 1) / CH * B;
+    int t = D % 4 ? 32 : 64;
+    while (t > 16 && wide * ((L + t - 1) / t) < 1024) t /= 2;
+    return t;
+}
 
 __device__ __forceinline__ int live_tokens(const int *lens, int b, int L) {
     return lens ? max(0, min(lens[b], L)) : L;
@@ -49,16 +51,16 @@ template <typename T, int V, int U> struct Tokens {
 
 // Each tile's decay A, its own share H of the state behind it and its own
 // share K = sum A_t dy_t of what flows out before it: ws[b][tile][3][D].
-template <typename T, int V, bool RATE>
-__global__ __launch_bounds__(NT) void lru_bwd_shares(LruBwdArgs g) {
-    constexpr int TG = Tile<V>::TG, CL = Tile<V>::CL, U = Tile<V>::U;
+template <typename T, int V, int U, bool RATE>
+__global__ __launch_bounds__(NT) void lru_bwd_shares(LruBwdArgs g, int nt) {
+    constexpr int CL = CH / V, TG = NT / CL;  // lanes along the channels, runs of tokens
     __shared__ float2 sm[TG][CH];
     __shared__ float smk[TG][CH];
     const LruArgs &a = g.f;
     const int lane = threadIdx.x % CL, run = threadIdx.x / CL;
     const int b = blockIdx.z, tile = blockIdx.x, c0 = blockIdx.y * CH, c = c0 + lane * V;
     const int n = live_tokens(a.lens, b, a.L);
-    const int t0 = tile * BT + run * U;
+    const int t0 = (tile * TG + run) * U;
     float A[V], H[V], K[V], rate[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = K[v] = 0.f, rate[v] = 0.f;
@@ -67,7 +69,7 @@ __global__ __launch_bounds__(NT) void lru_bwd_shares(LruBwdArgs g) {
         const Tokens<T, V, U> p(g, b, c, t0, n);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (t0 + u >= n) break;
+            if (t0 + u >= n) continue;
             float xv[V], rv[V], iv[V] = {}, dv[V];
             VecIO<T, V>::unpack(p.x[u], xv);
             VecIO<T, V>::unpack(p.r[u], rv);
@@ -100,7 +102,7 @@ __global__ __launch_bounds__(NT) void lru_bwd_shares(LruBwdArgs g) {
             k = fmaf(all.x, smk[q][threadIdx.x], k);
             all = make_float2(all.x * s.x, fmaf(s.x, all.y, s.y));
         }
-        float *w = a.ws + (static_cast<int64_t>(b) * tiles(a.L) + tile) * 3 * a.D + cc;
+        float *w = a.ws + (static_cast<int64_t>(b) * nt + tile) * 3 * a.D + cc;
         w[0] = all.x;
         w[a.D] = all.y;
         w[2 * static_cast<int64_t>(a.D)] = k;
@@ -113,10 +115,10 @@ __global__ __launch_bounds__(NT) void lru_bwd_shares(LruBwdArgs g) {
 // again.
 constexpr int CC = 32, CR = 16;
 
-__global__ __launch_bounds__(CC *CR) void lru_bwd_carry(LruBwdArgs g) {
+__global__ __launch_bounds__(CC *CR) void lru_bwd_carry(LruBwdArgs g, int n) {
     __shared__ float2 sm[CR][CC];
     const LruArgs &a = g.f;
-    const int lane = threadIdx.x % CC, run = threadIdx.x / CC, b = blockIdx.y, n = tiles(a.L);
+    const int lane = threadIdx.x % CC, run = threadIdx.x / CC, b = blockIdx.y;
     const int c = blockIdx.x * CC + lane, per = (n + CR - 1) / CR, k0 = min(run * per, n), k1 = min(k0 + per, n);
     const int64_t D = a.D, row = b * D + c;
     const bool back = blockIdx.z != 0, in = c < D;
@@ -162,17 +164,17 @@ __global__ __launch_bounds__(CC *CR) void lru_bwd_carry(LruBwdArgs g) {
     }
 }
 
-template <typename T, int V, bool RATE>
-__global__ __launch_bounds__(NT) void lru_bwd_grads(LruBwdArgs g) {
+template <typename T, int V, int U, bool RATE>
+__global__ __launch_bounds__(NT) void lru_bwd_grads(LruBwdArgs g, int nt) {
     typedef VecIO<T, V> IO;
-    constexpr int TG = Tile<V>::TG, CL = Tile<V>::CL, U = Tile<V>::U;
+    constexpr int CL = CH / V, TG = NT / CL;
     __shared__ float2 sm[TG][CH];
     __shared__ float smk[TG][CH];
     const LruArgs &a = g.f;
     const int lane = threadIdx.x % CL, run = threadIdx.x / CL;
     const int b = blockIdx.z, tile = blockIdx.x, c0 = blockIdx.y * CH, c = c0 + lane * V;
-    const int n = live_tokens(a.lens, b, a.L), nt = tiles(a.L);
-    const int t0 = tile * BT + run * U;
+    const int n = live_tokens(a.lens, b, a.L);
+    const int t0 = (tile * TG + run) * U;
     const bool in = c < a.D;
     // held from here to the way back: the rows as stored, and of each value the decay, the scale
     // and the state before it; the gates' own values are cheaper formed again
@@ -316,21 +318,32 @@ __global__ __launch_bounds__(NT) void lru_bwd_pass(LruBwdArgs g) {
 
 bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
-template <typename T, int V, bool RATE> hipError_t backward(const LruBwdArgs &g, hipStream_t s) {
+template <typename T, int V, int U, bool RATE> void tiled(const LruBwdArgs &g, int nt, hipStream_t s) {
     const LruArgs &a = g.f;
-    const int nt = tiles(a.L);
+    const dim3 grid(nt, (a.D + CH - 1) / CH, a.B);
+    if (nt > 1) {
+        hipLaunchKernelGGL((lru_bwd_shares<T, V, U, RATE>), grid, dim3(NT), 0, s, g, nt);
+        hipLaunchKernelGGL(lru_bwd_carry, dim3((a.D + CC - 1) / CC, a.B, 2), dim3(CC * CR), 0, s, g, nt);
+    }
+    hipLaunchKernelGGL((lru_bwd_grads<T, V, U, RATE>), grid, dim3(NT), 0, s, g, nt);
+}
+
+template <typename T, int V, bool RATE> hipError_t backward(const LruBwdArgs &g, hipStream_t s) {
+    constexpr int TG = NT / (CH / V);
+    const LruArgs &a = g.f;
+    const int tokens = tile_tokens(a.B, a.L, a.D), nt = (a.L + tokens - 1) / tokens;
     const int64_t rows = static_cast<int64_t>(a.B) * nt;
     if (!nt) {
         const int64_t n = static_cast<int64_t>(a.B) * a.D;
         if (g.dstate && n)
             hipLaunchKernelGGL(lru_bwd_pass, dim3(static_cast<unsigned>((n + NT - 1) / NT)), dim3(NT), 0, s, g);
     } else if (a.B) {
-        const dim3 grid(nt, (a.D + CH - 1) / CH, a.B);
-        if (nt > 1) {
-            hipLaunchKernelGGL((lru_bwd_shares<T, V, RATE>), grid, dim3(NT), 0, s, g);
-            hipLaunchKernelGGL(lru_bwd_carry, dim3((a.D + CC - 1) / CC, a.B, 2), dim3(CC * CR), 0, s, g);
-        }
-        hipLaunchKernelGGL((lru_bwd_grads<T, V, RATE>), grid, dim3(NT), 0, s, g);
+        if (tokens == 64)
+            tiled<T, V, 64 / TG, RATE>(g, nt, s);
+        else if (tokens == 32)
+            tiled<T, V, 32 / TG, RATE>(g, nt, s);
+        else
+            tiled<T, V, 16 / TG, RATE>(g, nt, s);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !RATE) return e;
@@ -352,7 +365,8 @@ template <typename T> hipError_t backward_t(const LruBwdArgs &g, hipStream_t s) 
 }  // namespace
 
 int64_t lru_backward_floats(int B, int L, int D) {
-    const int64_t n = tiles(L);
+    const int t = tile_tokens(B, L, D);
+    const int64_t n = (static_cast<int64_t>(L) + t - 1) / t;
     return (n > 1 ? 4 : 1) * n * B * D;
 }
 hipError_t launch_lru_backward(const LruBwdArgs &g, hipStream_t s) {
