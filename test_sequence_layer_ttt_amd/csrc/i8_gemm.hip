@@ -19,22 +19,29 @@ __device__ __forceinline__ i32x4 mfma_i8(i32x4 a, i32x4 b, i32x4 c) {
 // Bytes k .. k + 15 of a row of K at any address, zeros from K on: the aligned
 // words that hold one of them, shifted together. Every word that is read holds
 // a byte of the row.
+typedef __attribute__((ext_vector_type(4), aligned(4))) uint32_t word4;
+
 __device__ __forceinline__ i32x4 load16(const int8_t *row, int k, int K) {
     uint32_t d[5] = {};
-    if (k < K) {
-        const uintptr_t p = reinterpret_cast<uintptr_t>(row + k), end = reinterpret_cast<uintptr_t>(row + K);
-        const uint32_t *q = reinterpret_cast<const uint32_t *>(p & ~static_cast<uintptr_t>(3));
+    const uintptr_t p = reinterpret_cast<uintptr_t>(row + k);
+    const uint32_t *q = reinterpret_cast<const uint32_t *>(p & ~static_cast<uintptr_t>(3));
+    const uint32_t sh = static_cast<uint32_t>(p & 3);
+    if (k + 20 <= K) {  // all five words
+        const word4 v = *reinterpret_cast<const word4 *>(q);
+        d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
+        d[4] = q[4];
+    } else if (k < K) {
+        const uintptr_t end = reinterpret_cast<uintptr_t>(row + K);
 #pragma unroll
         for (int j = 0; j < 5; ++j)
             if (reinterpret_cast<uintptr_t>(q + j) < end) d[j] = q[j];
-        const uint32_t sh = static_cast<uint32_t>(p & 3);
-        const int live = K - k;
+    }
+    const int live = K - k;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t v = __builtin_amdgcn_alignbyte(d[j + 1], d[j], sh);
-            const int n = live - 4 * j;
-            d[j] = n >= 4 ? v : n <= 0 ? 0u : v & ((1u << (8 * n)) - 1);
-        }
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t v = __builtin_amdgcn_alignbyte(d[j + 1], d[j], sh);
+        const int n = live - 4 * j;
+        d[j] = n >= 4 ? v : n <= 0 ? 0u : v & ((1u << (8 * n)) - 1);
     }
     return i32x4{static_cast<int>(d[0]), static_cast<int>(d[1]), static_cast<int>(d[2]), static_cast<int>(d[3])};
 }
@@ -57,6 +64,20 @@ template <int E> struct Features {
     }
 };
 
+// feature n of token m as one of the layer's views
+__device__ __forceinline__ uint16_t *view_at(const I8Args &a, int m, int n) {
+    const int HD = a.H * 64, v = n / HD, hj = n - v * HD, b = m / a.L, t = m - b * a.L;
+    uint16_t *y = static_cast<uint16_t *>(v == 0 ? a.v[0] : v == 1 ? a.v[1] : a.v[2]);
+    return y + ((static_cast<int64_t>(b) * a.H + hj / 64) * a.L + t) * 64 + hj % 64;
+}
+
+__device__ __forceinline__ void store1(const I8Args &a, int m, int n, float o) {
+    if (!a.out_io)
+        static_cast<float *>(a.y)[m * a.yr + n] = o;
+    else
+        *(a.H ? view_at(a, m, n) : static_cast<uint16_t *>(a.y) + (m * a.yr + n)) = f32_to_bf16(o);
+}
+
 // features n .. n + 3 of token m, whose scale is sx
 __device__ __forceinline__ void store4(const I8Args &a, int m, int n, float sx, const Features<4> &f, i32x4 acc) {
     float o[4];
@@ -64,12 +85,8 @@ __device__ __forceinline__ void store4(const I8Args &a, int m, int n, float sx, 
     for (int e = 0; e < 4; ++e) o[e] = fmaf(static_cast<float>(acc[e]) * sx, f.ws[e], f.bias[e]);
     const bool vec = a.vec && n + 4 <= a.N;
     if (a.out_io) {
-        uint16_t *y = static_cast<uint16_t *>(a.y) + (m * a.yr + n);
-        if (a.H) {  // N is a multiple of 64: four features of one head
-            const int HD = a.H * 64, v = n / HD, hj = n - v * HD, b = m / a.L, t = m - b * a.L;
-            y = static_cast<uint16_t *>(v == 0 ? a.v[0] : v == 1 ? a.v[1] : a.v[2]);
-            y += ((static_cast<int64_t>(b) * a.H + hj / 64) * a.L + t) * 64 + hj % 64;
-        }
+        // N is a multiple of 64 there: four features of one head
+        uint16_t *y = a.H ? view_at(a, m, n) : static_cast<uint16_t *>(a.y) + (m * a.yr + n);
         if (vec) {
             *reinterpret_cast<uint2 *>(y) = make_uint2(tile::pack2(o[0], o[1]), tile::pack2(o[2], o[3]));
         } else {
@@ -90,47 +107,74 @@ __device__ __forceinline__ void store4(const I8Args &a, int m, int n, float sx, 
 }
 
 // Any sizes, strides and addresses: a workgroup takes 64 features x 64 tokens,
-// a wave 32 x 32 of them, contraction steps of 64 bytes through LDS. Rows of
-// 80 bytes: the 16 rows of a fragment read lie in distinct banks.
-constexpr int GT = 64, GK = 64, GS = 80;
+// a wave 32 x 32 of them, contraction steps of 256 bytes through LDS, the next
+// step's rows on their way in registers (bound by their latency: steps of 64 bytes
+// took 25.8 us where these take 15, 1551 x 771 x 1037). Rows of 272 bytes: the rows
+// of a fragment read lie in distinct banks.
+constexpr int GT = 64, GK = 256, GS = GK + 16;
 
 __global__ __launch_bounds__(256) void i8_any(I8Args a) {
     __shared__ __attribute__((aligned(16))) int8_t sw[GT * GS], sx[GT * GS];
     const int nf = (a.N + GT - 1) / GT;
     const int n0 = static_cast<int>(blockIdx.x % nf) * GT, m0 = static_cast<int>(blockIdx.x / nf) * GT;
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, c = lane & 15;
-    const int row = tid >> 2, part = (tid & 3) * 16;
-    // rows behind the last are read from it; their outputs are not stored
-    const int8_t *pw = a.w + static_cast<int64_t>(min(n0 + row, a.N - 1)) * a.wr;
-    const int8_t *px = a.x + static_cast<int64_t>(min(m0 + row, a.M - 1)) * a.xr;
+    const int row = tid >> 4, part = (tid & 15) * 16;  // rows row, row + 16, ..
+    const int8_t *pw[4], *px[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // rows behind the last are read from it; their outputs are not stored
+        pw[i] = a.w + static_cast<int64_t>(min(n0 + row + 16 * i, a.N - 1)) * a.wr;
+        px[i] = a.x + static_cast<int64_t>(min(m0 + row + 16 * i, a.M - 1)) * a.xr;
+    }
     const int wf = (w & 1) * 32, wt = (w >> 1) * 32;
-    i32x4 acc[2][2] = {};
-    i32x4 nw = load16(pw, part, a.K), nx = load16(px, part, a.K);
-    for (int k = 0; k < a.K; k += GK) {
-        *reinterpret_cast<i32x4 *>(&sw[row * GS + part]) = nw;
-        *reinterpret_cast<i32x4 *>(&sx[row * GS + part]) = nx;
-        __syncthreads();
-        nw = load16(pw, k + GK + part, a.K);
-        nx = load16(px, k + GK + part, a.K);
-        i32x4 fw[2], fx[2];
+    i32x4 acc[2][2] = {}, nw[4], nx[4];
+    auto fetch = [&](int k) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            fw[i] = *reinterpret_cast<const i32x4 *>(&sw[(wf + 16 * i + c) * GS + 16 * g]);
-            fx[i] = *reinterpret_cast<const i32x4 *>(&sx[(wt + 16 * i + c) * GS + 16 * g]);
+        for (int i = 0; i < 4; ++i) {
+            nw[i] = load16(pw[i], k + part, a.K);
+            nx[i] = load16(px[i], k + part, a.K);
         }
+    };
+    fetch(0);
+    for (int k = 0; k < a.K; k += GK) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<i32x4 *>(&sw[(row + 16 * i) * GS + part]) = nw[i];
+            *reinterpret_cast<i32x4 *>(&sx[(row + 16 * i) * GS + part]) = nx[i];
+        }
+        __syncthreads();
+        fetch(k + GK);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) acc[i][j] = mfma_i8(fw[i], fx[j], acc[i][j]);
+        for (int kk = 0; kk < GK / 64; ++kk) {
+            i32x4 fw[2], fx[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                fw[i] = *reinterpret_cast<const i32x4 *>(&sw[(wf + 16 * i + c) * GS + 64 * kk + 16 * g]);
+                fx[i] = *reinterpret_cast<const i32x4 *>(&sx[(wt + 16 * i + c) * GS + 64 * kk + 16 * g]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = mfma_i8(fx[j], fw[i], acc[i][j]);
+        }
         __syncthreads();
     }
+    // x as the A operand here: a lane has four tokens of one feature, so that stores of single
+    // elements lie 16 together
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+        const int n = n0 + wf + 16 * i + c;
+        const Features<1> f(a, n);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int m = m0 + wt + 16 * j + c, n = n0 + wf + 16 * i + 4 * g;
-            if (m < a.M && n < a.N) store4(a, m, n, a.xs[m], Features<4>(a, n), acc[i][j]);
+            float sx[4];
+            const int m = m0 + wt + 16 * j + 4 * g;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sx[e] = a.xs[min(m + e, a.M - 1)];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (m + e < a.M && n < a.N) store1(a, m + e, n, fmaf(static_cast<float>(acc[i][j][e]) * sx[e], f.ws[0], f.bias[0]));
         }
+    }
 }
 
 // Few tokens (M <= 16 MT): bound by reading w, and by latency. A workgroup takes
@@ -259,7 +303,7 @@ __global__ __launch_bounds__(64 * FW) void i8_few_features(I8Args a, const T *x,
 }
 
 // Where logical chunk j of row r of a half lies among its eight: j ^ key(r).
-__device__ __forceinline__ int keyA(int r) { return (r & 3) | ((r >> 2) & 4); }
+__device__ __forceinline__ int keyA(int r) { return (r & 3) | ((r >> 1) & 4); }
 
 // Workgroup id -> tile. Workgroups go to the 8 XCDs round robin; each XCD takes
 // a run of tiles, by fours of feature blocks over all token blocks, so that the
@@ -272,45 +316,46 @@ __device__ __forceinline__ void tile_of(int id, int nfb, int ntb, int *fb, int *
     *tb = k / n;
 }
 
-// A lane's 16 consecutive features n .. of token m, four accumulators acc(0 .. 3).
-template <typename F> __device__ __forceinline__ void store16(const I8Args &a, int m, int n, float sx, const Features<16> &f, F acc) {
+struct Lanes {
+    Features<8> h[2];
+    __device__ __forceinline__ Lanes(const I8Args &a, int n) : h{{a, n}, {a, n + 32}} {}
+};
+
+// A lane's 16 features of token m, n .. n + 7 and n + 32 .. n + 39: four accumulators acc(0 .. 3).
+template <typename F> __device__ __forceinline__ void store16(const I8Args &a, int m, int n, float sx, const Lanes &f, F acc) {
     if (m >= a.M || n >= a.N) return;
-    const bool vec = a.vec && n + 16 <= a.N;
+    const bool vec = a.vec && n + 40 <= a.N;
     float o[16];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         const i32x4 v = acc(t);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[4 * t + e] = fmaf(static_cast<float>(v[e]) * sx, f.ws[4 * t + e], f.bias[4 * t + e]);
+        for (int e = 0; e < 4; ++e) o[4 * t + e] = fmaf(static_cast<float>(v[e]) * sx, f.h[t / 2].ws[4 * (t % 2) + e], f.h[t / 2].bias[4 * (t % 2) + e]);
     }
     if (a.out_io) {
-        uint16_t *y = static_cast<uint16_t *>(a.y) + (m * a.yr + n);
-        if (a.H) {  // 16 features of one head
-            const int HD = a.H * 64, v = n / HD, hj = n - v * HD, b = m / a.L, t = m - b * a.L;
-            y = static_cast<uint16_t *>(v == 0 ? a.v[0] : v == 1 ? a.v[1] : a.v[2]);
-            y += ((static_cast<int64_t>(b) * a.H + hj / 64) * a.L + t) * 64 + hj % 64;
-        }
+        // N is a multiple of 64 there: all of one head
+        uint16_t *y = a.H ? view_at(a, m, n) : static_cast<uint16_t *>(a.y) + (m * a.yr + n);
         if (vec) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                reinterpret_cast<uint4 *>(y)[h] =
+                *reinterpret_cast<uint4 *>(y + 32 * h) =
                     make_uint4(tile::pack2(o[8 * h], o[8 * h + 1]), tile::pack2(o[8 * h + 2], o[8 * h + 3]),
                                tile::pack2(o[8 * h + 4], o[8 * h + 5]), tile::pack2(o[8 * h + 6], o[8 * h + 7]));
         } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                if (n + e < a.N) y[e] = f32_to_bf16(o[e]);
+                if (n + 32 * (e / 8) + e % 8 < a.N) y[32 * (e / 8) + e % 8] = f32_to_bf16(o[e]);
         }
     } else {
         float *y = static_cast<float *>(a.y) + (m * a.yr + n);
         if (vec) {
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-                reinterpret_cast<float4 *>(y)[t] = make_float4(o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]);
+                *reinterpret_cast<float4 *>(y + 32 * (t / 2) + 4 * (t % 2)) = make_float4(o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]);
         } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                if (n + e < a.N) y[e] = o[e];
+                if (n + 32 * (e / 8) + e % 8 < a.N) y[32 * (e / 8) + e % 8] = o[e];
         }
     }
 }
@@ -333,8 +378,9 @@ template <typename F> __device__ __forceinline__ void store16(const I8Args &a, i
 //    may be filled again;
 //  * rows of 128 bytes, 16-byte chunk j of row r at j ^ key(r): 8 distinct
 //    places for the 8 rows that a fragment read touches at once. A's MFMA row
-//    4 g + e of tile t is feature 16 g + 4 t + e, so that a lane ends up with 16
-//    consecutive features of a token (32 bytes of bf16) and four lanes with 64;
+//    4 g + e of tile t is feature 32 (t / 2) + 8 g + 4 (t % 2) + e, so that a lane
+//    ends up with twice 8 consecutive features of a token (16 bytes of bf16) and a
+//    store of four lanes with 64 bytes;
 //  * past K the chunks are read again from the last one and A's are taken as
 //    zeros; rows past the end are read from the last one and not stored.
 constexpr int BT = 256, BK = 128;
@@ -392,12 +438,12 @@ template <bool TAIL> __global__ __launch_bounds__(512, 2) void i8_big(I8Args a, 
                                                      kk * BK, 0, 0);
         }
     };
-    const int ra = 64 * wr + 16 * (c >> 2) + (c & 3);  // A's row of tile 0 (tile t: + 4 t)
+    const int ra = 64 * wr + 8 * (c >> 2) + (c & 3);  // A's row of tile 0
     const int rb = 32 * wc + c;                         // B's row of tile 0 (tile s: + 16 s)
     const int8_t *pa[2], *pb[2];
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-        pa[kk] = &sm[0][0][0][ra * BK + 16 * ((4 * kk + g) ^ (c & 7))];  // keyA(ra + 4 t) = c & 7
+        pa[kk] = &sm[0][0][0][ra * BK + 16 * ((4 * kk + g) ^ (c & 7))];  // keyA of A's rows is c & 7
         pb[kk] = &sm[1][0][0][rb * BK + 16 * ((4 * kk + g) ^ (c & 7))];
     }
     auto read_a = [&](int stage, int h, i32x4 (&f)[2][4]) {
@@ -405,7 +451,7 @@ template <bool TAIL> __global__ __launch_bounds__(512, 2) void i8_big(I8Args a, 
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-                f[kk][t] = *reinterpret_cast<const i32x4 *>(pa[kk] + (2 * stage + h) * 128 * BK + 4 * t * BK);
+                f[kk][t] = *reinterpret_cast<const i32x4 *>(pa[kk] + (2 * stage + h) * 128 * BK + (32 * (t / 2) + 4 * (t % 2)) * BK);
     };
     auto read_b = [&](int stage, int h, i32x4 (&f)[2][2]) {
 #pragma unroll
@@ -480,7 +526,7 @@ template <bool TAIL> __global__ __launch_bounds__(512, 2) void i8_big(I8Args a, 
     }
     if (!wr) section_end();
     // all scales at once, with the loads behind the last step
-    const Features<16> f[2] = {{a, n0 + 64 * wr + 16 * g}, {a, n0 + 128 + 64 * wr + 16 * g}};
+    const Lanes f[2] = {{a, n0 + 64 * wr + 8 * g}, {a, n0 + 128 + 64 * wr + 8 * g}};
     float sx[2][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -493,7 +539,7 @@ template <bool TAIL> __global__ __launch_bounds__(512, 2) void i8_big(I8Args a, 
         for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                store16(a, m0 + 128 * j + 32 * wc + 16 * s + c, n0 + 128 * i + 64 * wr + 16 * g, sx[j][s], f[i],
+                store16(a, m0 + 128 * j + 32 * wc + 16 * s + c, n0 + 128 * i + 64 * wr + 8 * g, sx[j][s], f[i],
                         [&](int t) { return acc[i][j][t][s]; });
 }
 
