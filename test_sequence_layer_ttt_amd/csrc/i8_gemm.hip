@@ -7,6 +7,9 @@
 #include "i8_scale.hpp"
 #include "vec.hpp"
 
+#include <algorithm>
+#include <type_traits>
+
 namespace ttt {
 namespace {
 
@@ -135,6 +138,12 @@ __global__ __launch_bounds__(256) void i8_any(I8Args a) {
         }
     };
     fetch(0);
+    const Features<1> f[2] = {{a, n0 + wf + c}, {a, n0 + wf + 16 + c}};
+    float scale[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) scale[j][e] = a.xs[min(m0 + wt + 16 * j + 4 * g + e, a.M - 1)];
     for (int k = 0; k < a.K; k += GK) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -161,20 +170,14 @@ __global__ __launch_bounds__(256) void i8_any(I8Args a) {
     // x as the A operand here: a lane has four tokens of one feature, so that stores of single
     // elements lie 16 together
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int n = n0 + wf + 16 * i + c;
-        const Features<1> f(a, n);
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float sx[4];
-            const int m = m0 + wt + 16 * j + 4 * g;
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sx[e] = a.xs[min(m + e, a.M - 1)];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (m + e < a.M && n < a.N) store1(a, m + e, n, fmaf(static_cast<float>(acc[i][j][e]) * sx[e], f.ws[0], f.bias[0]));
-        }
-    }
+            for (int e = 0; e < 4; ++e) {
+                const int m = m0 + wt + 16 * j + 4 * g + e, n = n0 + wf + 16 * i + c;
+                if (m < a.M && n < a.N) store1(a, m, n, fmaf(static_cast<float>(acc[i][j][e]) * scale[j][e], f[i].ws[0], f[i].bias[0]));
+            }
 }
 
 // Few tokens (M <= 16 MT): bound by reading w, and by latency. A workgroup takes
@@ -302,8 +305,17 @@ __global__ __launch_bounds__(64 * FW) void i8_few_features(I8Args a, const T *x,
     if (w == 0 && c < a.M && n < a.N) store4(a, c, n, scale[c], four, sum);
 }
 
-// Where logical chunk j of row r of a half lies among its eight: j ^ key(r).
-__device__ __forceinline__ int keyA(int r) { return (r & 3) | ((r >> 1) & 4); }
+// Where logical chunk j of row r of a half lies among its eight: j ^ key(r). A's
+// rows are a wave's TA MFMA tiles by pairs, 8 consecutive features of each pair to a
+// lane; the last of an odd number of tiles goes by fours.
+template <int TA> __device__ __forceinline__ int keyA(int r) {
+    const int q = r % (16 * TA);
+    return TA % 2 && q >= 16 * (TA - 1) ? q & 7 : (q & 3) | ((q >> 1) & 4);
+}
+// the row of MFMA row c of tile t, from a wave's first
+template <int TA> constexpr __device__ __forceinline__ int rowA(int t, int c) {
+    return TA % 2 && t == TA - 1 ? 16 * t + c : 32 * (t / 2) + 8 * (c >> 2) + 4 * (t % 2) + (c & 3);
+}
 
 // Workgroup id -> tile. Workgroups go to the 8 XCDs round robin; each XCD takes
 // a run of tiles, by fours of feature blocks over all token blocks, so that the
@@ -316,74 +328,65 @@ __device__ __forceinline__ void tile_of(int id, int nfb, int ntb, int *fb, int *
     *tb = k / n;
 }
 
-struct Lanes {
-    Features<8> h[2];
-    __device__ __forceinline__ Lanes(const I8Args &a, int n) : h{{a, n}, {a, n + 32}} {}
-};
-
-// A lane's 16 features of token m, n .. n + 7 and n + 32 .. n + 39: four accumulators acc(0 .. 3).
-template <typename F> __device__ __forceinline__ void store16(const I8Args &a, int m, int n, float sx, const Lanes &f, F acc) {
+// G = 8 or 4 consecutive features n .. of token m, whose scale is sx
+template <int G>
+__device__ __forceinline__ void store_run(const I8Args &a, int m, int n, float sx, const Features<G> &f, const i32x4 (&acc)[G / 4]) {
     if (m >= a.M || n >= a.N) return;
-    const bool vec = a.vec && n + 40 <= a.N;
-    float o[16];
+    float o[G];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const i32x4 v = acc(t);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[4 * t + e] = fmaf(static_cast<float>(v[e]) * sx, f.h[t / 2].ws[4 * (t % 2) + e], f.h[t / 2].bias[4 * (t % 2) + e]);
-    }
+    for (int e = 0; e < G; ++e) o[e] = fmaf(static_cast<float>(acc[e / 4][e % 4]) * sx, f.ws[e], f.bias[e]);
+    const bool vec = a.vec && n + G <= a.N;
     if (a.out_io) {
         // N is a multiple of 64 there: all of one head
         uint16_t *y = a.H ? view_at(a, m, n) : static_cast<uint16_t *>(a.y) + (m * a.yr + n);
         if (vec) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<uint4 *>(y + 32 * h) =
-                    make_uint4(tile::pack2(o[8 * h], o[8 * h + 1]), tile::pack2(o[8 * h + 2], o[8 * h + 3]),
-                               tile::pack2(o[8 * h + 4], o[8 * h + 5]), tile::pack2(o[8 * h + 6], o[8 * h + 7]));
+            VecIO<bf16_t, G>::store(y, o);
         } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (n + 32 * (e / 8) + e % 8 < a.N) y[32 * (e / 8) + e % 8] = f32_to_bf16(o[e]);
+            for (int e = 0; e < G; ++e)
+                if (n + e < a.N) y[e] = f32_to_bf16(o[e]);
         }
     } else {
         float *y = static_cast<float *>(a.y) + (m * a.yr + n);
         if (vec) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-                *reinterpret_cast<float4 *>(y + 32 * (t / 2) + 4 * (t % 2)) = make_float4(o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]);
+            VecIO<float, G>::store(y, o);
         } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (n + 32 * (e / 8) + e % 8 < a.N) y[32 * (e / 8) + e % 8] = o[e];
+            for (int e = 0; e < G; ++e)
+                if (n + e < a.N) y[e] = o[e];
         }
     }
 }
 
-// Large products: a workgroup of 8 waves takes 256 features x 256 tokens.
-// Contraction steps of 128 bytes; both operands lie in LDS in halves of 128
-// rows, two stages of 64 KB, filled by direct global-to-LDS loads.
-//  * a wave (wr, wc) takes 64 x 32 of each of the four quadrants (a half of the
-//    features by a half of the tokens): 4 x 2 MFMA tiles, and walks them as
+// Large products: a workgroup of 8 waves takes 2 HA features x 2 HB tokens, 256 x
+// 256 where there are tiles enough. Contraction steps of 128 bytes; both operands
+// lie in LDS in halves of HA and HB rows, two stages, filled by direct
+// global-to-LDS loads.
+//  * a wave (wr, wc) takes HA / 2 x HB / 4 of each of the four quadrants (a half of
+//    the features by a half of the tokens): TA x TB MFMA tiles, and walks them as
 //    (0,0), (1,0), (1,1), (0,1), so that a step reads every fragment once;
 //  * a quadrant is two sections: M reads the fragments that it or the next
-//    quadrant lacks (8 or 4 of 1 KB) and asks for the half of two steps ahead
-//    whose place was read last, C is its 16 products. A barrier ends each
+//    quadrant lacks (2 TA or 2 TB of 1 KB) and asks for the half of two steps ahead
+//    whose place was read last, C is its 2 TA TB products. A barrier ends each
 //    section, and the waves 4 .. 7 run one section behind the waves 0 .. 3: on
 //    each SIMD one wave multiplies while the other one reads;
-//  * a half is asked for 7 M sections before it is read: s_waitcnt vmcnt(12) at
-//    the end of M leaves the 12 younger loads in flight. That wait and the one
-//    for the section's own LDS reads stand before the section's barrier, so
-//    behind it every wave's loads have landed, and the place of what was read
-//    may be filled again;
+//  * a half is asked for 7 M sections before it is read (in QA or QB loads of a
+//    wave): s_waitcnt vmcnt at the end of M leaves the younger ones, 12 of them for
+//    256 x 256, in flight. That wait and the one for the section's own LDS reads
+//    stand before the section's barrier, so behind it every wave's loads have
+//    landed, and the place of what was read may be filled again;
 //  * rows of 128 bytes, 16-byte chunk j of row r at j ^ key(r): 8 distinct
-//    places for the 8 rows that a fragment read touches at once. A's MFMA row
-//    4 g + e of tile t is feature 32 (t / 2) + 8 g + 4 (t % 2) + e, so that a lane
-//    ends up with twice 8 consecutive features of a token (16 bytes of bf16) and a
-//    store of four lanes with 64 bytes;
-//  * past K the chunks are read again from the last one and A's are taken as
-//    zeros; rows past the end are read from the last one and not stored.
-constexpr int BT = 256, BK = 128;
+//    places for the 8 rows that a fragment read touches at once. A's rows go to
+//    MFMA rows so that a lane ends up with 8 consecutive features of a token (16
+//    bytes of bf16) and a store of four lanes with 64 bytes;
+//  * past K (TAIL) the last chunk is read again and A's is taken as zeros; rows past
+//    the end are read from the last one and not stored.
+// 16384 x 2048 x 6144: 178 us, 2.3 POP/s (a large library product in 8 bits: 2.1); a
+// step takes 1.4 us, 0.97 with operands of zeros where 0.86 is the matrix cores' own
+// at 2.4 GHz: what bounds it is the clock that the card holds under this load. A tile
+// costs 7 to 9 us besides its steps (first loads, stores); walking over tiles with
+// one workgroup a compute unit, the next tile's loads ahead, took as long.
+constexpr int BK = 128;
 
 typedef __attribute__((address_space(3))) void lds_void;
 
@@ -401,123 +404,141 @@ __device__ __forceinline__ void section_end() {  // barrier alone: no wait
     fence();
 }
 
-template <bool TAIL> __global__ __launch_bounds__(512, 2) void i8_big(I8Args a, int nfb, int ntb) {
-    // halves of A, then of B, each for both stages: 64 KB that one address reaches
-    __shared__ __attribute__((aligned(16))) int8_t sm[2][2][2][128 * BK];
+template <int HA, int HB, bool TAIL> __global__ __launch_bounds__(512, 2) void i8_big(I8Args a, int nfb, int ntb) {
+    constexpr int TA = HA / 32, TB = HB / 64;
+    constexpr int QA = (HA + 63) / 64, QB = (HB + 63) / 64;  // loads of a wave for a half, 8 rows each
+    // [stage][half] of A, then of B: up to 64 KB each that one address reaches. One array: told two
+    // apart, the compiler sees which loads to LDS a read may meet and waits for them all.
+    constexpr int LA = HA * BK, LB = HB * BK;
+    __shared__ __attribute__((aligned(16))) int8_t sm[4 * LA + 4 * LB];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, c = lane & 15;
     const int wr = w >> 2, wc = w & 3;
     int fb, tb;
     tile_of(blockIdx.x, nfb, ntb, &fb, &tb);
-    const int n0 = fb * BT, m0 = tb * BT;
+    const int n0 = fb * 2 * HA, m0 = tb * 2 * HB;
     const int nk = (a.K + BK - 1) / BK, tail = TAIL ? a.K % BK : 0;  // a multiple of 16
 
-    // loads: a wave's instruction q fills rows 16 w + 8 q .. + 7 of a half
+    // loads: a wave's instruction q fills rows 8 (Q w + q) .. + 7 of a half (with HA = 96 the last
+    // four of the sixteen rows that are asked for beyond it are others again)
     const auto baseA = buffer(a.w + static_cast<int64_t>(n0) * a.wr), baseB = buffer(a.x + static_cast<int64_t>(m0) * a.xr);
-    uint32_t off[4][2];  // of A0, A1, B0, B1 from their base
     const int rl = lane >> 3, pc = lane & 7;
-#pragma unroll
-    for (int h = 0; h < 4; ++h)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int r = 16 * w + 8 * q + rl;
-            const int ch = pc ^ (h < 2 ? keyA(r) : r & 7);
-            const int row = min((h & 1) * 128 + r, (h < 2 ? a.N - n0 : a.M - m0) - 1);
-            off[h][q] = static_cast<uint32_t>(row) * static_cast<uint32_t>(h < 2 ? a.wr : a.xr) + 16 * ch;
-        }
-    auto ask = [&](int k, int stage, int h) {
-        const int kk = k < nk ? k : 0;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            uint32_t o = off[h][q];
-            if (TAIL && kk == nk - 1) {
-                const int r = 16 * w + 8 * q + rl, ch = pc ^ (h < 2 ? keyA(r) : r & 7);
-                o -= 16 * max(ch - (tail / 16 - 1), 0);
-            }
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(h < 2 ? baseA : baseB,
-                                                     (lds_void *)&sm[h >> 1][stage][h & 1][(16 * w + 8 * q) * BK], 16, o,
-                                                     kk * BK, 0, 0);
-        }
+    auto first = [&](bool isA, int q) { return isA ? 8 * (QA * w + q) % HA : 8 * (QB * w + q) % HB; };
+    auto chunk = [&](bool isA, int q) {
+        const int r = first(isA, q) + rl;
+        return pc ^ (isA ? keyA<TA>(r) : r & 7);
     };
-    const int ra = 64 * wr + 8 * (c >> 2) + (c & 3);  // A's row of tile 0
-    const int rb = 32 * wc + c;                         // B's row of tile 0 (tile s: + 16 s)
-    const int8_t *pa[2], *pb[2];
+    uint32_t offA[2][QA], offB[2][QB];  // of the halves' rows from their base
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-        pa[kk] = &sm[0][0][0][ra * BK + 16 * ((4 * kk + g) ^ (c & 7))];  // keyA of A's rows is c & 7
-        pb[kk] = &sm[1][0][0][rb * BK + 16 * ((4 * kk + g) ^ (c & 7))];
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int q = 0; q < QA; ++q)
+            offA[h][q] = static_cast<uint32_t>(min(h * HA + first(true, q) + rl, a.N - n0 - 1)) * static_cast<uint32_t>(a.wr) +
+                         16 * chunk(true, q);
+#pragma unroll
+        for (int q = 0; q < QB; ++q)
+            offB[h][q] = static_cast<uint32_t>(min(h * HB + first(false, q) + rl, a.M - m0 - 1)) * static_cast<uint32_t>(a.xr) +
+                         16 * chunk(false, q);
     }
-    auto read_a = [&](int stage, int h, i32x4 (&f)[2][4]) {
+    auto ask = [&](int k, int stage, bool isA, int h) {
+        const int kk = k < nk ? k : 0;  // behind the last step: the first again
+#pragma unroll
+        for (int q = 0; q < (isA ? QA : QB); ++q) {
+            uint32_t o = isA ? offA[h][q < QA ? q : 0] : offB[h][q < QB ? q : 0];
+            if (TAIL && kk == nk - 1) o -= 16 * max(chunk(isA, q) - (tail / 16 - 1), 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                isA ? baseA : baseB,
+                (lds_void *)&sm[isA ? (2 * stage + h) * LA + first(true, q) * BK : 4 * LA + (2 * stage + h) * LB + first(false, q) * BK],
+                16, o, kk * BK, 0, 0);
+        }
+    };
+    const int8_t *pa[2], *pl[2], *pb[2];  // A's tiles by pairs, its last of an odd number, B's
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {  // the keys of MFMA rows c are c & 7
+        const int j = 16 * ((4 * kk + g) ^ (c & 7));
+        pa[kk] = &sm[(16 * TA * wr + rowA<TA>(0, c)) * BK + j];
+        pl[kk] = &sm[(16 * TA * wr + c) * BK + j];
+        pb[kk] = &sm[4 * LA + (16 * TB * wc + c) * BK + j];
+    }
+    auto read_a = [&](int stage, int h, i32x4 (&f)[2][TA]) {
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-                f[kk][t] = *reinterpret_cast<const i32x4 *>(pa[kk] + (2 * stage + h) * 128 * BK + (32 * (t / 2) + 4 * (t % 2)) * BK);
+            for (int t = 0; t < TA; ++t) {
+                const bool last = TA % 2 && t == TA - 1;
+                f[kk][t] = *reinterpret_cast<const i32x4 *>((last ? pl[kk] : pa[kk]) + (2 * stage + h) * LA +
+                                                            (last ? 16 * t : rowA<TA>(t, 0)) * BK);
+            }
     };
-    auto read_b = [&](int stage, int h, i32x4 (&f)[2][2]) {
+    auto read_b = [&](int stage, int h, i32x4 (&f)[2][TB]) {
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-                f[kk][s] = *reinterpret_cast<const i32x4 *>(pb[kk] + (2 * stage + h) * 128 * BK + 16 * s * BK);
+            for (int s = 0; s < TB; ++s)
+                f[kk][s] = *reinterpret_cast<const i32x4 *>(pb[kk] + (2 * stage + h) * LB + 16 * s * BK);
     };
-    auto cut = [&](int k, i32x4 (&f)[2][4]) {  // past K
+    auto cut = [&](int k, i32x4 (&f)[2][TA]) {  // past K
         if (TAIL && k == nk - 1) {
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                for (int t = 0; t < TA; ++t)
                     if (16 * (4 * kk + g) >= tail) f[kk][t] = i32x4{0, 0, 0, 0};
         }
     };
-    i32x4 acc[2][2][4][2] = {};  // quadrant (A half, B half), tiles
-    auto multiply = [&](i32x4 (&q)[4][2], const i32x4 (&fa)[2][4], const i32x4 (&fb_)[2][2]) {
+    i32x4 acc[2][2][TA][TB] = {};  // quadrant (A half, B half), tiles
+    auto multiply = [&](i32x4 (&q)[TA][TB], const i32x4 (&fa)[2][TA], const i32x4 (&fb_)[2][TB]) {
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < TA; ++t)
 #pragma unroll
-                for (int s = 0; s < 2; ++s) q[t][s] = mfma_i8(fa[kk][t], fb_[kk][s], q[t][s]);
+                for (int s = 0; s < TB; ++s) q[t][s] = mfma_i8(fa[kk][t], fb_[kk][s], q[t][s]);
         __builtin_amdgcn_s_setprio(0);
         section_end();
     };
-    auto m_end = [&] {
+    // `young`: the loads asked for after the half that the next section reads
+    auto m_end = [&](auto young) {
         fence();
-        __builtin_amdgcn_s_waitcnt(0x0F70 | 12);  // vmcnt(12)
-        __builtin_amdgcn_s_waitcnt(0xC07F);       // lgkmcnt(0)
+        __builtin_amdgcn_s_waitcnt(0x0F70 | decltype(young)::value);  // vmcnt
+        __builtin_amdgcn_s_waitcnt(0xC07F);                           // lgkmcnt(0)
         section_end();
     };
-    i32x4 a0[2][4], a1[2][4], b0[2][2], b1[2][2];
-    // A0 A1 B0 B1 are halves 0 1 2 3, asked for in the order 2 0 1 3
+    static_assert(4 * QA + 2 * QB <= 15 && 2 * QA + 4 * QB <= 15, "counts of the low field");
+    typedef std::integral_constant<int, 2 * QA + 4 * QB> Young0;
+    typedef std::integral_constant<int, 3 * QA + 3 * QB> Young1;
+    typedef std::integral_constant<int, 4 * QA + 2 * QB> Young2;
+    i32x4 a0[2][TA], a1[2][TA], b0[2][TB], b1[2][TB];
+    // the order of asking: B0 A0 A1 B1
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        ask(k, k, 2);
-        ask(k, k, 0);
-        ask(k, k, 1);
-        ask(k, k, 3);
+        ask(k, k, false, 0);
+        ask(k, k, true, 0);
+        ask(k, k, true, 1);
+        ask(k, k, false, 1);
     }
-    m_end();  // the first halves 2 and 0
+    m_end(Young1{});  // the first B0 and A0
     read_b(0, 0, b0);
-    m_end();
+    m_end(Young1{});
     if (wr) section_end();
     auto step = [&](int k, int stage) {
         read_a(stage, 0, a0);
-        ask(k + 2, stage, 2);
+        ask(k + 2, stage, false, 0);
         cut(k, a0);
-        m_end();
+        m_end(Young0{});  // A1
         multiply(acc[0][0], a0, b0);
         read_a(stage, 1, a1);
-        ask(k + 2, stage, 0);
+        ask(k + 2, stage, true, 0);
         cut(k, a1);
-        m_end();
+        m_end(Young1{});  // B1
         multiply(acc[1][0], a1, b0);
         read_b(stage, 1, b1);
-        ask(k + 2, stage, 1);
-        m_end();
+        ask(k + 2, stage, true, 1);
+        m_end(Young2{});  // the next step's B0
         multiply(acc[1][1], a1, b1);
         read_b(stage ^ 1, 0, b0);
-        ask(k + 2, stage, 3);
-        m_end();
+        ask(k + 2, stage, false, 1);
+        m_end(Young1{});  // and A0
         multiply(acc[0][1], a0, b1);
     };
     for (int k = 0; k < nk; k += 2) {
@@ -526,21 +547,40 @@ template <bool TAIL> __global__ __launch_bounds__(512, 2) void i8_big(I8Args a, 
     }
     if (!wr) section_end();
     // all scales at once, with the loads behind the last step
-    const Lanes f[2] = {{a, n0 + 64 * wr + 8 * g}, {a, n0 + 128 + 64 * wr + 8 * g}};
-    float sx[2][2];
+    float sx[2][TB];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) sx[j][s] = a.xs[min(m0 + 128 * j + 32 * wc + 16 * s + c, a.M - 1)];
+        for (int s = 0; s < TB; ++s) sx[j][s] = a.xs[min(m0 + HB * j + 16 * TB * wc + 16 * s + c, a.M - 1)];
+    const int nw = n0 + 16 * TA * wr;
+    // by pairs of tiles (the second pair, where there is one), and an odd tile's
+    const Features<8> p0[2] = {Features<8>(a, nw + 8 * g), Features<8>(a, nw + HA + 8 * g)};
+    const Features<8> p1[2] = {Features<8>(a, nw + 32 + 8 * g), Features<8>(a, nw + HA + 32 + 8 * g)};
+    const Features<4> odd[2] = {Features<4>(a, nw + 16 * (TA - 1) + 4 * g), Features<4>(a, nw + HA + 16 * (TA - 1) + 4 * g)};
     __builtin_amdgcn_s_waitcnt(0x0F70);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < TB; ++s)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                store16(a, m0 + 128 * j + 32 * wc + 16 * s + c, n0 + 128 * i + 64 * wr + 8 * g, sx[j][s], f[i],
-                        [&](int t) { return acc[i][j][t][s]; });
+            for (int i = 0; i < 2; ++i) {
+                const int m = m0 + HB * j + 16 * TB * wc + 16 * s + c, n = nw + HA * i;
+#pragma unroll
+                for (int p = 0; p < TA / 2; ++p)
+                    store_run<8>(a, m, n + 32 * p + 8 * g, sx[j][s], p ? p1[i] : p0[i], {acc[i][j][2 * p][s], acc[i][j][2 * p + 1][s]});
+                if constexpr (TA % 2 != 0)
+                    store_run<4>(a, m, n + 16 * (TA - 1) + 4 * g, sx[j][s], odd[i], {acc[i][j][TA - 1][s]});
+            }
+}
+
+template <int HA, int HB> hipError_t big(const I8Args &a, hipStream_t s) {
+    const int nfb = (a.N + 2 * HA - 1) / (2 * HA), ntb = (a.M + 2 * HB - 1) / (2 * HB);
+    const dim3 grid(static_cast<unsigned>(nfb * ntb));
+    if (a.K % BK)
+        hipLaunchKernelGGL((i8_big<HA, HB, true>), grid, dim3(512), 0, s, a, nfb, ntb);
+    else
+        hipLaunchKernelGGL((i8_big<HA, HB, false>), grid, dim3(512), 0, s, a, nfb, ntb);
+    return hipGetLastError();
 }
 
 // bytes of a row of K in LDS: whole steps, and 16 more so that rows start in other banks
@@ -586,15 +626,31 @@ hipError_t launch_i8_project(const I8Args &in, hipStream_t s) {
     if (a.M <= 16) return few<1, 1>(a, s);
     if (a.M <= 32) return few<1, 2>(a, s);
     if (a.M <= 64) return a.N >= 4096 ? few<2, 4>(a, s) : few<1, 4>(a, s);
-    const bool big = chunked(a.x, a.xr, a.K) && chunked(a.w, a.wr, a.K) && a.xr < (1 << 23) && a.wr < (1 << 23);  // offsets in 32 bits
-    const int nfb = (a.N + BT - 1) / BT, ntb = (a.M + BT - 1) / BT;
-    if (big) {
-        const dim3 grid(static_cast<unsigned>(nfb * ntb));
-        if (a.K % BK)
-            hipLaunchKernelGGL(i8_big<true>, grid, dim3(512), 0, s, a, nfb, ntb);
-        else
-            hipLaunchKernelGGL(i8_big<false>, grid, dim3(512), 0, s, a, nfb, ntb);
-        return hipGetLastError();
+    const bool whole = chunked(a.x, a.xr, a.K) && chunked(a.w, a.wr, a.K) && a.xr < (1 << 23) && a.wr < (1 << 23);  // offsets in 32 bits
+    if (whole) {
+        // The tile shape whose rounds over the compute units take the least, by a step's time and a
+        // tile's own (us, fitted to the measurements) in a full round and, for the last, alone on the
+        // chip and in between. The smallest runs twice on a compute unit. Largest to smallest shape, 8192
+        // tokens x 2304 features: K = 768 31.5, 30.2, 30.9, 28.7 us, K = 4096 89.6, 81.1, 89.3, 86.7;
+        // 4096 x 4096 x 4096 58.0, 85.7, 74.8, 78.8; 4096 x 2048 x 4096 44.2, 42.2, 34.8, 36.8; 500 x 768 x 768
+        // 13.4, 12.6, 9.2, 7.4.
+        int dev = 0, ncu = 0;
+        hipError_t e = hipGetDevice(&dev);
+        if (e == hipSuccess) e = hipDeviceGetAttribute(&ncu, hipDeviceAttributeMultiprocessorCount, dev);
+        if (e != hipSuccess) return e;
+        const int steps = (a.K + BK - 1) / BK;
+        struct Time { float step, tile; };
+        struct Time { float step, tile; };
+        auto us = [&](int f, int t, int at_once, Time full, Time alone) {
+            const int64_t tiles = static_cast<int64_t>((a.N + f - 1) / f) * ((a.M + t - 1) / t);
+            const float round = full.step * steps + full.tile, least = alone.step * steps + alone.tile;
+            const int64_t rest = tiles % at_once;
+            return static_cast<float>(tiles / at_once) * round + (rest ? least + (round - least) * rest / at_once : 0.f);
+        };
+        const float t0 = us(256, 256, ncu, {1.45f, 7.f}, {.89f, 6.f}), t1 = us(192, 256, ncu, {1.f, 7.6f}, {.82f, 6.5f}),
+                    t2 = us(128, 256, ncu, {.75f, 4.5f}, {.63f, 4.2f}), t3 = us(128, 128, 2 * ncu, {.74f, 4.9f}, {.51f, 3.5f});
+        const float least = std::min(std::min(t0, t1), std::min(t2, t3));
+        return least == t0 ? big<128, 128>(a, s) : least == t1 ? big<96, 128>(a, s) : least == t2 ? big<64, 128>(a, s) : big<64, 64>(a, s);
     }
     const int64_t tiles = (static_cast<int64_t>(a.N) + GT - 1) / GT * ((static_cast<int64_t>(a.M) + GT - 1) / GT);
     hipLaunchKernelGGL(i8_any, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, s, a);

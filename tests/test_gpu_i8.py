@@ -125,6 +125,19 @@ def test_project(case):
     assert torch.equal(wide[:, 3:3 + N], y) and bool((wide[:, :3] == 7).all()) and bool((wide[:, 3 + N:] == 7).all())
 
 
+# sizes that go by each tile shape, in whole steps of K and not, with ragged edges
+TILES = [(4090, 256, 4090, BF), (4081, 208, 4094, F32), (2040, 128, 6136, BF), (2033, 512, 6136, BF), (1990, 272, 6130, F32), (2033, 400, 6136, BF),
+         (3850, 256, 2040, BF), (4080, 80, 2030, BF), (1000, 512, 768, BF), (700, 48, 900, F32)]
+
+
+@pytest.mark.parametrize("M,K,N,dt", TILES)
+def test_project_by_each_tile_shape(M, K, N, dt):
+    x, xs, w, ws, b = _operands(M, K, N, 12, bias=True)
+    y = ttt.ttt_i8_project(x, xs, w, ws, b, dtype=dt)
+    _check(y, x, xs, w, ws, b, "y")
+    assert torch.equal(ttt.ttt_i8_project(x, xs, w, ws, b, dtype=dt), y)
+
+
 def test_project_at_the_ends_of_its_range():
     """The longest contraction of the lowest values: a sum of 2^30."""
     K = 65536
