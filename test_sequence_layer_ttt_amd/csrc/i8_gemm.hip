@@ -640,7 +640,6 @@ hipError_t launch_i8_project(const I8Args &in, hipStream_t s) {
         if (e != hipSuccess) return e;
         const int steps = (a.K + BK - 1) / BK;
         struct Time { float step, tile; };
-        struct Time { float step, tile; };
         auto us = [&](int f, int t, int at_once, Time full, Time alone) {
             const int64_t tiles = static_cast<int64_t>((a.N + f - 1) / f) * ((a.M + t - 1) / t);
             const float round = full.step * steps + full.tile, least = alone.step * steps + alone.tile;
