@@ -722,8 +722,9 @@ int ttt_lru_backward_workspace(int B, int L, int D, size_t *bytes);
  *   1 <= K <= TTT_I8_MAX_K; 0 <= M, N <= TTT_I8_MAX_ROWS (N: features);
  *   ceil(M/64)*ceil(N/64) at most TTT_I8_MAX_TILES.
  * Rows of 8-bit values may have a stride (x_strides and the like: one number,
- * the row stride) and any address; rows of K a multiple of 16 on 16-byte
- * boundaries go the fastest way.
+ * the row stride) and any address. With M > 64, rows that are not whole 16-byte
+ * chunks at 16-byte addresses (K and the stride multiples of 16), or are 8 MB and
+ * more apart, are laid out anew in the workspace first.
  *
  * ttt_i8_quantize: rows of x [M,K] io as q [M,K] and scale [M] fp32,
  *     scale = max |x| / 127,   q = x / scale to the nearest whole number (ties
@@ -742,29 +743,36 @@ int ttt_i8_quantize(int M, int K, int io, const void *x, const int64_t *x_stride
  * x [M,K], w [N,K] (output-major, as ttt_qkv_project's theta), any 8-bit
  * values; x_scale [M], w_scale [N], bias [N] fp32 (bias may be NULL); y [M,N]
  * out_io, row-strided. The sum is exact; scales, bias and the sum's conversion
- * are fp32, y is rounded once.
+ * are fp32, y is rounded once. The workspace holds ttt_i8_project_workspace's
+ * bytes for these operands (0 where both are read as they stand), 16-byte
+ * aligned; calls that share one must not overlap.
  */
 int ttt_i8_project(int M, int K, int N, int out_io, const int8_t *x, const int64_t *x_strides,
                    const float *x_scale, const int8_t *w, const int64_t *w_strides,
                    const float *w_scale, const float *bias, void *y, const int64_t *y_strides,
-                   hipStream_t stream);
+                   void *workspace, size_t workspace_bytes, hipStream_t stream);
+int ttt_i8_project_workspace(int M, int K, int N, const int8_t *x, const int64_t *x_strides,
+                             const int8_t *w, const int64_t *w_strides, size_t *bytes);
 
 /*
  * ttt_i8_project of x's quantised rows (ttt_i8_quantize's values), x and y in
  * io. The workspace holds ttt_i8_linear_workspace's bytes, 16-byte aligned (the
- * quantised rows and their scales); calls that share one must not overlap.
+ * quantised rows and their scales, and w's rows where they are laid out anew);
+ * calls that share one must not overlap. Up to 16 rows that fit a compute unit's
+ * LDS take one launch.
  */
 int ttt_i8_linear(int M, int K, int N, int io, const void *x, const int64_t *x_strides,
                   const int8_t *w, const int64_t *w_strides, const float *w_scale,
                   const float *bias, void *y, const int64_t *y_strides, void *workspace,
                   size_t workspace_bytes, hipStream_t stream);
-int ttt_i8_linear_workspace(int M, int K, size_t *bytes);
+int ttt_i8_linear_workspace(int M, int K, int N, const int8_t *w, const int64_t *w_strides,
+                            size_t *bytes);
 
 /*
  * ttt_qkv_project with theta [3,H*d,d_model] in 8 bits, theta_scale [3,H*d]
  * fp32, X [B,L,d_model] bf16 quantised token by token: XQ, XK, XV [B,H,L,d]
  * bf16, 16-byte aligned; d = 64. Workspace: ttt_i8_linear_workspace(B*L,
- * d_model).
+ * d_model, 3*H*d, theta, NULL).
  */
 int ttt_qkv_project_i8(int B, int L, int d_model, int H, int d, const void *X,
                        const int8_t *theta, const float *theta_scale, void *XQ, void *XK,

@@ -94,12 +94,13 @@ def load():
     lib.ttt_lru_backward.argtypes = [_i] * 4 + [_P] * 21 + [size, _P]
     lib.ttt_lru_backward_workspace.argtypes = [_i] * 3 + [ctypes.POINTER(size)]
     lib.ttt_i8_quantize.argtypes = [_i] * 3 + [_P] * 5 + [_P]
-    lib.ttt_i8_project.argtypes = [_i] * 4 + [_P] * 9 + [_P]
+    lib.ttt_i8_project.argtypes = [_i] * 4 + [_P] * 10 + [size, _P]
+    lib.ttt_i8_project_workspace.argtypes = [_i] * 3 + [_P] * 4 + [ctypes.POINTER(size)]
     lib.ttt_i8_linear.argtypes = [_i] * 4 + [_P] * 9 + [size, _P]
-    lib.ttt_i8_linear_workspace.argtypes = [_i] * 2 + [ctypes.POINTER(size)]
+    lib.ttt_i8_linear_workspace.argtypes = [_i] * 3 + [_P] * 2 + [ctypes.POINTER(size)]
     lib.ttt_qkv_project_i8.argtypes = [_i] * 5 + [_P] * 7 + [size, _P]
     for name in ("ttt_lru_forward", "ttt_lru_forward_workspace", "ttt_lru_step", "ttt_lru_backward",
-                 "ttt_lru_backward_workspace", "ttt_i8_quantize", "ttt_i8_project", "ttt_i8_linear",
+                 "ttt_lru_backward_workspace", "ttt_i8_quantize", "ttt_i8_project", "ttt_i8_project_workspace", "ttt_i8_linear",
                  "ttt_i8_linear_workspace", "ttt_qkv_project_i8"):
         getattr(lib, name).restype = _i
     for name in ("ttt_ssm_forward", "ttt_ssm_forward_workspace", "ttt_ssm_step", "ttt_ssm_backward",

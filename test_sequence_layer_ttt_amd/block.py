@@ -67,12 +67,12 @@ def _on(stream, operand, fn, *args):
         return fn(*args)
 
 
-def _need(name: str, *args: int) -> int:
+def _need(name: str, *args: int, pointers=()) -> int:
     for v in args:
         if not -2**31 <= v < 2**31:  # ctypes would cut it to 32 bits
             raise ValueError(f"size {v} is too large")
     n = ctypes.c_size_t(0)
-    _lib.check(getattr(_lib.load(), name)(*args, ctypes.byref(n)))
+    _lib.check(getattr(_lib.load(), name)(*args, *pointers, ctypes.byref(n)))
     return n.value
 
 
@@ -236,7 +236,21 @@ def ttt_i8_quantize(x, q=None, scale=None, stream=None):
     return _native.i8_quantize(*args)
 
 
-def ttt_i8_project(x, x_scale, w, w_scale, bias=None, dtype=torch.bfloat16, y=None, stream=None):
+def _rows(t) -> tuple:
+    """Address and row stride of a matrix, as the workspace queries take them."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int8 or t.dim() < 1:
+        raise TypeError("rows must be an int8 torch.Tensor")
+    stride = t.stride(-2) if t.dim() > 1 and t.numel() > t.size(-1) else t.size(-1)
+    return t.data_ptr() or None, ctypes.byref(ctypes.c_int64(stride))
+
+
+def ttt_i8_project_workspace(M: int, x, w) -> int:
+    """Bytes of device workspace ttt_i8_project needs for M rows of x and the
+    weight w [N,K]: 0 unless M > 64 and rows are not whole 16-byte chunks."""
+    return _need("ttt_i8_project_workspace", M, w.shape[-1], w.shape[0], pointers=(*_rows(x), *_rows(w)))
+
+
+def ttt_i8_project(x, x_scale, w, w_scale, bias=None, dtype=torch.bfloat16, y=None, workspace=None, stream=None):
     """y[...,n] = x_scale[...] w_scale[n] sum_k x[...,k] w[n,k] (+ bias[n]): x
     [...,K] int8 with x_scale [...] fp32 for each row, w [N,K] int8 with w_scale
     [N] and bias [N] fp32; the sum is exact. y [...,N] in `dtype`, bf16 or fp32.
@@ -244,15 +258,16 @@ def ttt_i8_project(x, x_scale, w, w_scale, bias=None, dtype=torch.bfloat16, y=No
     io = {torch.bfloat16: _lib.TTT_BF16, torch.float32: _lib.TTT_F32}.get(dtype)
     if io is None:
         raise TypeError(f"dtype {dtype} not supported")
-    args = (x, x_scale, w, w_scale, bias, io, y)
+    args = (x, x_scale, w, w_scale, bias, io, y, workspace)
     if stream is not None:
         return _on(stream, x, _native.i8_project, *args)
     return _native.i8_project(*args)
 
 
-def ttt_i8_linear_workspace(M: int, K: int) -> int:
-    """Bytes of device workspace ttt_i8_linear needs for M rows of K."""
-    return _need("ttt_i8_linear_workspace", M, K)
+def ttt_i8_linear_workspace(M: int, w) -> int:
+    """Bytes of device workspace ttt_i8_linear needs for M rows and the weight w
+    [N,K] (ttt_qkv_project_i8 for B L rows and theta as [3 H 64, d_model])."""
+    return _need("ttt_i8_linear_workspace", M, w.shape[-1], w.shape[0], pointers=_rows(w))
 
 
 def ttt_i8_linear(x, w, w_scale, bias=None, y=None, workspace=None, stream=None):

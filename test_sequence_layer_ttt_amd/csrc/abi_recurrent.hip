@@ -153,19 +153,45 @@ View rows(const void *p, const char *name, int64_t n, int64_t inner, const int64
     return view(p, name, n, 1, 1, inner, strides, 1, es);
 }
 
-// the quantised rows behind a call from features: whole 128-byte lines, then the scales
+// rows in whole 128-byte lines
 int64_t padded(int K) { return (static_cast<int64_t>(K) + 127) / 128 * 128; }
 
-int quantised(int M, int K, int io, const void *x, int64_t xr, void *workspace, ttt::I8Args *a, hipStream_t stream) {
+// The product, operands that it cannot take as they stand laid out anew in `room` (x first) before.
+hipError_t project(ttt::I8Args a, bool px, bool pw, int8_t *room, hipStream_t stream) {
+    const int pad = static_cast<int>(padded(a.K));
+    int8_t *x = room, *w = room + (px ? static_cast<int64_t>(a.M) * pad : 0);
+    if (px || pw) {
+        const ttt::I8PadArgs p{{px ? a.M : 0, pw ? a.N : 0}, {a.x, a.w}, {a.xr, a.wr}, {x, w}, a.K, pad};
+        const hipError_t e = ttt::launch_i8_pad(p, stream);
+        if (e != hipSuccess) return e;
+        if (px) a.x = x, a.xr = pad;
+        if (pw) a.w = w, a.wr = pad;
+        a.K = (a.K + 15) / 16 * 16;  // zeros of w, at least, behind a K that is no multiple
+    }
+    return ttt::launch_i8_project(a, stream);
+}
+
+// A product of features: the workspace holds the quantised rows, their scales and, where w's rows
+// cannot be taken as they stand, these.
+size_t features_bytes(int M, int K, int N) {
+    return static_cast<size_t>(M) * padded(K) + (static_cast<size_t>(M) + 3) / 4 * 16 + static_cast<size_t>(N) * padded(K);
+}
+bool unaligned_w(const ttt::I8Args &a) {
+    bool x, w;
+    ttt::i8_unaligned(a, &x, &w);
+    return w;
+}
+int features(int io, const void *x, int64_t xr, void *workspace, ttt::I8Args *a, hipStream_t stream) {
     if (ttt::i8_features_in_one(*a)) return launched(ttt::launch_i8_features(*a, io, x, xr, stream));
+    const int64_t pad = padded(a->K);
     int8_t *q = static_cast<int8_t *>(workspace);
-    float *scale = reinterpret_cast<float *>(q + static_cast<int64_t>(M) * padded(K));
+    float *scale = reinterpret_cast<float *>(q + a->M * pad);
     a->x = q;
-    a->xr = padded(K);
+    a->xr = pad;
     a->xs = scale;
-    const ttt::I8QuantArgs qa{M, K, io, x, xr, q, padded(K), scale};
-    const hipError_t e = ttt::launch_i8_quantize(qa, stream);
-    return launched(e == hipSuccess ? ttt::launch_i8_project(*a, stream) : e);
+    const hipError_t e = ttt::launch_i8_quantize({a->M, a->K, io, x, xr, q, pad, scale}, stream);
+    // whole lines of their own: with K no multiple of 16 the bytes behind a row meet zeros of w
+    return launched(e == hipSuccess ? project(*a, false, unaligned_w(*a), q + a->M * pad + (a->M + 3) / 4 * 16, stream) : e);
 }
 
 }  // namespace
@@ -185,29 +211,48 @@ int ttt_i8_quantize(int M, int K, int io, const void *x, const int64_t *x_stride
     return launched(ttt::launch_i8_quantize({M, K, io, x, vx.sb, q, vq.sb, scale}, stream));
 }
 
+int ttt_i8_project_workspace(int M, int K, int N, const int8_t *x, const int64_t *x_strides, const int8_t *w,
+                             const int64_t *w_strides, size_t *bytes) {
+    int st;
+    if ((st = i8_sizes(M, K, N))) return st;
+    if (!bytes) return fail(TTT_E_NULL, "bytes is NULL");
+    ttt::I8Args a{M, K, N, 0, x, x_strides ? x_strides[0] : K, nullptr, w, w_strides ? w_strides[0] : K};
+    bool px, pw;
+    ttt::i8_unaligned(a, &px, &pw);
+    *bytes = M && N ? ((px ? static_cast<size_t>(M) : 0) + (pw ? N : 0)) * padded(K) : 0;
+    return ok();
+}
+
 int ttt_i8_project(int M, int K, int N, int out_io, const int8_t *x, const int64_t *x_strides, const float *x_scale,
                    const int8_t *w, const int64_t *w_strides, const float *w_scale, const float *bias, void *y,
-                   const int64_t *y_strides, hipStream_t stream) {
+                   const int64_t *y_strides, void *workspace, size_t workspace_bytes, hipStream_t stream) {
     int st;
     if ((st = i8_sizes(M, K, N))) return st;
     if (out_io != TTT_F32 && out_io != TTT_BF16)
         return fail(TTT_E_DTYPE, "output dtype %d is not TTT_F32/TTT_BF16", out_io);
     const View vx = rows(x, "x", M, K, x_strides, 1), vw = rows(w, "w", N, K, w_strides, 1),
                vy = rows(y, "y", M, N, y_strides, esize(out_io));
+    const ttt::I8Args a{M, K, N, out_io, x, vx.sb, x_scale, w, vw.sb, w_scale, bias, y, vy.sb};
+    bool px, pw;
+    ttt::i8_unaligned(a, &px, &pw);
+    size_t need;
+    if ((st = ttt_i8_project_workspace(M, K, N, x, x_strides, w, w_strides, &need))) return st;
     Views v;
     if ((st = v.add_in(vx)) || (st = v.add_in(flat(x_scale, "x_scale", M, 4))) || (st = v.add_in(vw)) ||
         (st = v.add_in(flat(w_scale, "w_scale", N, 4))) || (st = v.add_in(flat(bias, "bias", bias ? N : 0, 4))) ||
-        (st = v.add_out(vy)) || (st = v.alias()))
+        (st = v.add_out(vy)) || (st = scratch(workspace, workspace_bytes, need)) ||
+        (st = v.add_out(flat(need ? workspace : nullptr, "workspace", static_cast<int64_t>(need / 4), 4))) || (st = v.alias()))
         return st;
     if (!M || !N) return ok();
-    return launched(ttt::launch_i8_project({M, K, N, out_io, x, vx.sb, x_scale, w, vw.sb, w_scale, bias, y, vy.sb}, stream));
+    return launched(project(a, px, pw, static_cast<int8_t *>(workspace), stream));
 }
 
-int ttt_i8_linear_workspace(int M, int K, size_t *bytes) {
+int ttt_i8_linear_workspace(int M, int K, int N, const int8_t *w, const int64_t *w_strides, size_t *bytes) {
     int st;
-    if ((st = i8_sizes(M, K, 0))) return st;
+    if ((st = i8_sizes(M, K, N))) return st;
     if (!bytes) return fail(TTT_E_NULL, "bytes is NULL");
-    *bytes = static_cast<size_t>(M) * (padded(K) + sizeof(float));
+    const ttt::I8Args a{M, K, N, 0, nullptr, K, nullptr, w, w_strides ? w_strides[0] : K};
+    *bytes = features_bytes(M, K, unaligned_w(a) ? N : 0);
     return ok();
 }
 
@@ -216,10 +261,12 @@ int ttt_i8_linear(int M, int K, int N, int io, const void *x, const int64_t *x_s
                   void *workspace, size_t workspace_bytes, hipStream_t stream) {
     int st;
     size_t need;
-    if ((st = i8_sizes(M, K, N)) || (st = ttt_i8_linear_workspace(M, K, &need))) return st;
+    if ((st = i8_sizes(M, K, N))) return st;
     if (io != TTT_F32 && io != TTT_BF16) return fail(TTT_E_DTYPE, "io dtype %d is not TTT_F32/TTT_BF16", io);
     const View vx = rows(x, "x", M, K, x_strides, esize(io)), vw = rows(w, "w", N, K, w_strides, 1),
                vy = rows(y, "y", M, N, y_strides, esize(io));
+    ttt::I8Args a{M, K, N, io, nullptr, 0, nullptr, w, vw.sb, w_scale, bias, y, vy.sb};
+    if ((st = ttt_i8_linear_workspace(M, K, N, w, w_strides, &need))) return st;
     Views v;
     if ((st = v.add_in(vx)) || (st = v.add_in(vw)) || (st = v.add_in(flat(w_scale, "w_scale", N, 4))) ||
         (st = v.add_in(flat(bias, "bias", bias ? N : 0, 4))) || (st = v.add_out(vy)))
@@ -227,8 +274,7 @@ int ttt_i8_linear(int M, int K, int N, int io, const void *x, const int64_t *x_s
     if ((st = scratch(workspace, workspace_bytes, need)) ||
         (st = v.add_out(flat(workspace, "workspace", static_cast<int64_t>(need / 4), 4))) || (st = v.alias())) return st;
     if (!M || !N) return ok();
-    ttt::I8Args a{M, K, N, io, nullptr, 0, nullptr, w, vw.sb, w_scale, bias, y, vy.sb};
-    return quantised(M, K, io, x, vx.sb, workspace, &a, stream);
+    return features(io, x, vx.sb, workspace, &a, stream);
 }
 
 int ttt_qkv_project_i8(int B, int L, int d_model, int H, int d, const void *X, const int8_t *theta,
@@ -240,9 +286,10 @@ int ttt_qkv_project_i8(int B, int L, int d_model, int H, int d, const void *X, c
     const int64_t M = static_cast<int64_t>(B) * L, N = 192 * static_cast<int64_t>(H);
     if (M > TTT_I8_MAX_ROWS || N > TTT_I8_MAX_ROWS) return fail(TTT_E_SHAPE, "B*L or 3*H*d exceeds %d", TTT_I8_MAX_ROWS);
     size_t need;
-    if ((st = i8_sizes(static_cast<int>(M), d_model, static_cast<int>(N))) ||
-        (st = ttt_i8_linear_workspace(static_cast<int>(M), d_model, &need)))
-        return st;
+    if ((st = i8_sizes(static_cast<int>(M), d_model, static_cast<int>(N)))) return st;
+    ttt::I8Args a{static_cast<int>(M), d_model, static_cast<int>(N), TTT_BF16, nullptr, 0, nullptr, theta, d_model,
+                  theta_scale, nullptr, nullptr, 0, L, H, {XQ, XK, XV}};
+    if ((st = ttt_i8_linear_workspace(a.M, a.K, a.N, theta, nullptr, &need))) return st;
     void *out[3] = {XQ, XK, XV};
     const char *names[3] = {"XQ", "XK", "XV"};
     Views v;
@@ -257,9 +304,7 @@ int ttt_qkv_project_i8(int B, int L, int d_model, int H, int d, const void *X, c
     if ((st = scratch(workspace, workspace_bytes, need)) ||
         (st = v.add_out(flat(workspace, "workspace", static_cast<int64_t>(need / 4), 4))) || (st = v.alias())) return st;
     if (!M || !N) return ok();
-    ttt::I8Args a{static_cast<int>(M), d_model, static_cast<int>(N), TTT_BF16, nullptr, 0, nullptr, theta, d_model,
-                  theta_scale, nullptr, nullptr, 0, L, H, {XQ, XK, XV}};
-    return quantised(a.M, a.K, TTT_BF16, X, d_model, workspace, &a, stream);
+    return features(TTT_BF16, X, d_model, workspace, &a, stream);
 }
 
 }  // extern "C"

@@ -675,7 +675,7 @@ struct I8Weight {
           bias(opt<const float>(pb, "bias", {w.M}, at::kFloat, k)) {}
 };
 
-// x, x_scale, w, w_scale, bias, bf16, y
+// x, x_scale, w, w_scale, bias, bf16, y, workspace
 PyObject *i8_project(PyObject *const *a) {
     const Tensor &x = tensor(a[0], "x");
     const Kind k = on_device(x, "x", at::kChar);
@@ -685,9 +685,13 @@ PyObject *i8_project(PyObject *const *a) {
     const int io = number(a[5]);
     const Tensor y = output(a[6], "y", r.with(w.w.M), io == TTT_BF16 ? at::kBFloat16 : at::kFloat, k, false);
     const RowsOf ry(y, "y");
+    const int8_t *px = static_cast<const int8_t *>(ptr(x)), *pw = static_cast<const int8_t *>(ptr(w.w.t));
+    size_t need = 0;
+    done(ttt_i8_project_workspace(r.M, r.K, w.w.M, px, &r.stride, pw, &w.w.stride, &need));
+    const Workspace ws(a[7], need, k);
     call(k, [&](hipStream_t s) {
-        return ttt_i8_project(r.M, r.K, w.w.M, io, static_cast<const int8_t *>(ptr(x)), &r.stride, xs,
-                              static_cast<const int8_t *>(ptr(w.w.t)), &w.w.stride, w.scale, w.bias, ptr(y), &ry.stride, s);
+        return ttt_i8_project(r.M, r.K, w.w.M, io, px, &r.stride, xs, pw, &w.w.stride, w.scale, w.bias, ptr(y), &ry.stride,
+                              ws.p, ws.bytes, s);
     });
     written(a[6], y);
     return THPVariable_Wrap(y);
@@ -701,11 +705,12 @@ PyObject *i8_linear(PyObject *const *a) {
     const I8Weight w(a[1], a[2], a[3], r.K, k);
     const Tensor y = output(a[4], "y", r.with(w.w.M), k.dt, k, false);
     const RowsOf ry(y, "y");
+    const int8_t *pw = static_cast<const int8_t *>(ptr(w.w.t));
     size_t need = 0;
-    done(ttt_i8_linear_workspace(r.M, r.K, &need));
+    done(ttt_i8_linear_workspace(r.M, r.K, w.w.M, pw, &w.w.stride, &need));
     const Workspace ws(a[5], need, k);
     call(k, [&](hipStream_t s) {
-        return ttt_i8_linear(r.M, r.K, w.w.M, k.io, ptr(x), &r.stride, static_cast<const int8_t *>(ptr(w.w.t)), &w.w.stride,
+        return ttt_i8_linear(r.M, r.K, w.w.M, k.io, ptr(x), &r.stride, pw, &w.w.stride,
                              w.scale, w.bias, ptr(y), &ry.stride, ws.p, ws.bytes, s);
     });
     written(a[4], y);
@@ -731,10 +736,11 @@ PyObject *qkv_project_i8(PyObject *const *a) {
     for (int i = 0; i < 3; ++i)
         out[i] = output(a[4] == Py_None ? Py_None : PyTuple_GET_ITEM(a[4], i), names[i], {B, H, L, 64}, at::kBFloat16, k);
     size_t need = 0;
-    done(ttt_i8_linear_workspace(size(static_cast<int64_t>(B) * L, "B*L"), dm, &need));
+    const int8_t *pt = static_cast<const int8_t *>(ptr(th));
+    done(ttt_i8_linear_workspace(size(static_cast<int64_t>(B) * L, "B*L"), dm, size(3 * hd, "3*H*64"), pt, nullptr, &need));
     const Workspace ws(a[5], need, k);
     call(k, [&](hipStream_t s) {
-        return ttt_qkv_project_i8(B, L, dm, H, 64, ptr(x), static_cast<const int8_t *>(ptr(th)),
+        return ttt_qkv_project_i8(B, L, dm, H, 64, ptr(x), pt,
                                   static_cast<const float *>(ptr(ts)), ptr(out[0]), ptr(out[1]), ptr(out[2]), ws.p, ws.bytes, s);
     });
     PyObject *r = PyTuple_New(3);
@@ -763,7 +769,7 @@ PyObject *init(PyObject *const *a) {
 PyMethodDef methods[] = {METHOD(init, 1), METHOD(conv_forward, 8), METHOD(conv_step, 6), METHOD(conv_backward, 10),
                          METHOD(ssm_forward, 12), METHOD(ssm_step, 9), METHOD(ssm_backward, 13), METHOD(block_norm, 14),
                          METHOD(block_norm_backward, 16), METHOD(lru_forward, 9), METHOD(lru_step, 6),
-                         METHOD(lru_backward, 10), METHOD(i8_quantize, 3), METHOD(i8_project, 7), METHOD(i8_linear, 6),
+                         METHOD(lru_backward, 10), METHOD(i8_quantize, 3), METHOD(i8_project, 8), METHOD(i8_linear, 6),
                          METHOD(qkv_project_i8, 6), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -33,6 +33,19 @@ struct I8Args {
     bool vec = false;  // y in 16-byte accesses (set by the launch)
 };
 
+// rows of K bytes, two operands' (rows 0: none), into rows of `pad` (a multiple of 128) with zeros behind
+struct I8PadArgs {
+    int rows[2];
+    const int8_t *src[2];
+    int64_t stride[2];
+    int8_t *dst[2];
+    int K, pad;
+};
+
+// Which operands launch_i8_project cannot take as they stand: with M > 64, rows that are not whole
+// 16-byte chunks at 16-byte addresses, or 8 MB and more apart.
+void i8_unaligned(const I8Args &a, bool *x, bool *w);
+hipError_t launch_i8_pad(const I8PadArgs &a, hipStream_t stream);
 hipError_t launch_i8_quantize(const I8QuantArgs &a, hipStream_t stream);
 hipError_t launch_i8_project(const I8Args &a, hipStream_t stream);
 // from features x [M,K] of io, rows of xr (a.x, a.xr, a.xs unused), where in_one says so

@@ -74,13 +74,6 @@ __device__ __forceinline__ uint16_t *view_at(const I8Args &a, int m, int n) {
     return y + ((static_cast<int64_t>(b) * a.H + hj / 64) * a.L + t) * 64 + hj % 64;
 }
 
-__device__ __forceinline__ void store1(const I8Args &a, int m, int n, float o) {
-    if (!a.out_io)
-        static_cast<float *>(a.y)[m * a.yr + n] = o;
-    else
-        *(a.H ? view_at(a, m, n) : static_cast<uint16_t *>(a.y) + (m * a.yr + n)) = f32_to_bf16(o);
-}
-
 // features n .. n + 3 of token m, whose scale is sx
 __device__ __forceinline__ void store4(const I8Args &a, int m, int n, float sx, const Features<4> &f, i32x4 acc) {
     float o[4];
@@ -109,75 +102,19 @@ __device__ __forceinline__ void store4(const I8Args &a, int m, int n, float sx, 
     }
 }
 
-// Any sizes, strides and addresses: a workgroup takes 64 features x 64 tokens,
-// a wave 32 x 32 of them, contraction steps of 256 bytes through LDS, the next
-// step's rows on their way in registers (bound by their latency: steps of 64 bytes
-// took 25.8 us where these take 15, 1551 x 771 x 1037). Rows of 272 bytes: the rows
-// of a fragment read lie in distinct banks.
-constexpr int GT = 64, GK = 256, GS = GK + 16;
-
-__global__ __launch_bounds__(256) void i8_any(I8Args a) {
-    __shared__ __attribute__((aligned(16))) int8_t sw[GT * GS], sx[GT * GS];
-    const int nf = (a.N + GT - 1) / GT;
-    const int n0 = static_cast<int>(blockIdx.x % nf) * GT, m0 = static_cast<int>(blockIdx.x / nf) * GT;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, g = lane >> 4, c = lane & 15;
-    const int row = tid >> 4, part = (tid & 15) * 16;  // rows row, row + 16, ..
-    const int8_t *pw[4], *px[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // rows behind the last are read from it; their outputs are not stored
-        pw[i] = a.w + static_cast<int64_t>(min(n0 + row + 16 * i, a.N - 1)) * a.wr;
-        px[i] = a.x + static_cast<int64_t>(min(m0 + row + 16 * i, a.M - 1)) * a.xr;
-    }
-    const int wf = (w & 1) * 32, wt = (w >> 1) * 32;
-    i32x4 acc[2][2] = {}, nw[4], nx[4];
-    auto fetch = [&](int k) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            nw[i] = load16(pw[i], k + part, a.K);
-            nx[i] = load16(px[i], k + part, a.K);
-        }
-    };
-    fetch(0);
-    const Features<1> f[2] = {{a, n0 + wf + c}, {a, n0 + wf + 16 + c}};
-    float scale[2][4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) scale[j][e] = a.xs[min(m0 + wt + 16 * j + 4 * g + e, a.M - 1)];
-    for (int k = 0; k < a.K; k += GK) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            *reinterpret_cast<i32x4 *>(&sw[(row + 16 * i) * GS + part]) = nw[i];
-            *reinterpret_cast<i32x4 *>(&sx[(row + 16 * i) * GS + part]) = nx[i];
-        }
-        __syncthreads();
-        fetch(k + GK);
-#pragma unroll
-        for (int kk = 0; kk < GK / 64; ++kk) {
-            i32x4 fw[2], fx[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                fw[i] = *reinterpret_cast<const i32x4 *>(&sw[(wf + 16 * i + c) * GS + 64 * kk + 16 * g]);
-                fx[i] = *reinterpret_cast<const i32x4 *>(&sx[(wt + 16 * i + c) * GS + 64 * kk + 16 * g]);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = mfma_i8(fx[j], fw[i], acc[i][j]);
-        }
-        __syncthreads();
-    }
-    // x as the A operand here: a lane has four tokens of one feature, so that stores of single
-    // elements lie 16 together
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int m = m0 + wt + 16 * j + 4 * g + e, n = n0 + wf + 16 * i + c;
-                if (m < a.M && n < a.N) store1(a, m, n, fmaf(static_cast<float>(acc[i][j][e]) * scale[j][e], f[i].ws[0], f[i].bias[0]));
-            }
+// Rows of K bytes at any address as rows of whole 128-byte lines, zeros past K: for
+// operands that the large products could not read 16 bytes at a time. A wave a row.
+// 16384 and 2048 rows of 2047: 16 us and the product 62, where reading them as they
+// stand for each tile took 305; 1551 and 1037 rows of 771: 4.3 and 13, and 17.
+__global__ __launch_bounds__(256) void i8_pad(I8PadArgs a) {
+    const int lane = threadIdx.x & 63;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    const int second = row >= a.rows[0];
+    if (second) row -= a.rows[0];
+    if (row >= a.rows[second]) return;
+    const int8_t *src = a.src[second] + row * a.stride[second];
+    int8_t *dst = a.dst[second] + row * a.pad;
+    for (int k = lane * 16; k < a.pad; k += 1024) *reinterpret_cast<i32x4 *>(dst + k) = load16(src, k, a.K);
 }
 
 // Few tokens (M <= 16 MT): bound by reading w, and by latency. A workgroup takes
@@ -328,14 +265,14 @@ __device__ __forceinline__ void tile_of(int id, int nfb, int ntb, int *fb, int *
     *tb = k / n;
 }
 
-// G = 8 or 4 consecutive features n .. of token m, whose scale is sx
+// G = 8 or 4 consecutive features n .. of token m, whose scale is sx, where a.vec
 template <int G>
 __device__ __forceinline__ void store_run(const I8Args &a, int m, int n, float sx, const Features<G> &f, const i32x4 (&acc)[G / 4]) {
     if (m >= a.M || n >= a.N) return;
     float o[G];
 #pragma unroll
     for (int e = 0; e < G; ++e) o[e] = fmaf(static_cast<float>(acc[e / 4][e % 4]) * sx, f.ws[e], f.bias[e]);
-    const bool vec = a.vec && n + G <= a.N;
+    const bool vec = n + G <= a.N;
     if (a.out_io) {
         // N is a multiple of 64 there: all of one head
         uint16_t *y = a.H ? view_at(a, m, n) : static_cast<uint16_t *>(a.y) + (m * a.yr + n);
@@ -397,6 +334,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const int8_t *p) {
 __device__ __forceinline__ void fence() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void wave_order() {  // a wave's LDS accesses in the order that is written
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
 }
 __device__ __forceinline__ void section_end() {  // barrier alone: no wait
     fence();
@@ -558,6 +499,43 @@ template <int HA, int HB, bool TAIL> __global__ __launch_bounds__(512, 2) void i
     const Features<8> p1[2] = {Features<8>(a, nw + 32 + 8 * g), Features<8>(a, nw + HA + 32 + 8 * g)};
     const Features<4> odd[2] = {Features<4>(a, nw + 16 * (TA - 1) + 4 * g), Features<4>(a, nw + HA + 16 * (TA - 1) + 4 * g)};
     __builtin_amdgcn_s_waitcnt(0x0F70);
+    if (!a.vec) {  // outputs one by one: by way of LDS, so that a wave's lie side by side
+        constexpr int F = 16 * TA, S = F + 4;
+        __syncthreads();  // all waves' loads have landed
+        float *const t = reinterpret_cast<float *>(sm) + w * 16 * S;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int s = 0; s < TB; ++s)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float *row = t + c * S;
+#pragma unroll
+                    for (int q = 0; q < TA; ++q) {
+                        const bool last = TA % 2 && q == TA - 1;
+                        const Features<8> &f = q / 2 ? p1[i] : p0[i];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            row[last ? 16 * q + 4 * g + e : 32 * (q / 2) + 8 * g + 4 * (q % 2) + e] =
+                                fmaf(static_cast<float>(acc[i][j][q][s][e]) * sx[j][s], last ? odd[i].ws[e] : f.ws[4 * (q % 2) + e],
+                                     last ? odd[i].bias[e] : f.bias[4 * (q % 2) + e]);
+                    }
+                    wave_order();
+#pragma unroll
+                    for (int e = 0; e < 16 * F / 64; ++e) {
+                        const int at = 64 * e + lane, m = m0 + HB * j + 16 * TB * wc + 16 * s + at / F, n = nw + HA * i + at % F;
+                        const float o = t[at / F * S + at % F];
+                        if (m < a.M && n < a.N) {
+                            if (a.out_io)
+                                static_cast<uint16_t *>(a.y)[m * a.yr + n] = f32_to_bf16(o);
+                            else
+                                static_cast<float *>(a.y)[m * a.yr + n] = o;
+                        }
+                    }
+                    wave_order();
+                }
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -591,6 +569,9 @@ bool aligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 // whole 16-byte chunks, at 16-byte addresses
 bool chunked(const int8_t *p, int64_t stride, int K) { return K % 16 == 0 && stride % 16 == 0 && aligned(p); }
 
+// and a tile's offsets in 32 bits
+bool tileable(const int8_t *p, int64_t stride, int K) { return chunked(p, stride, K) && stride < (1 << 23); }
+
 void outputs(I8Args &a) { a.vec = a.H || (aligned(a.y) && a.yr * (a.out_io ? 2 : 4) % 16 == 0); }
 
 template <int FT, int MT> hipError_t few(const I8Args &a, hipStream_t s) {
@@ -620,40 +601,46 @@ template <typename T> hipError_t few_features(const I8Args &a, const void *in, i
 
 }  // namespace
 
+void i8_unaligned(const I8Args &a, bool *x, bool *w) {
+    *x = a.M > 64 && !tileable(a.x, a.xr, a.K);
+    *w = a.M > 64 && !tileable(a.w, a.wr, a.K);
+}
+
+hipError_t launch_i8_pad(const I8PadArgs &a, hipStream_t s) {
+    const int64_t rows = static_cast<int64_t>(a.rows[0]) + a.rows[1];
+    if (!rows) return hipSuccess;
+    hipLaunchKernelGGL(i8_pad, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_i8_project(const I8Args &in, hipStream_t s) {
     I8Args a = in;
     outputs(a);
     if (a.M <= 16) return few<1, 1>(a, s);
     if (a.M <= 32) return few<1, 2>(a, s);
     if (a.M <= 64) return a.N >= 4096 ? few<2, 4>(a, s) : few<1, 4>(a, s);
-    const bool whole = chunked(a.x, a.xr, a.K) && chunked(a.w, a.wr, a.K) && a.xr < (1 << 23) && a.wr < (1 << 23);  // offsets in 32 bits
-    if (whole) {
-        // The tile shape whose rounds over the compute units take the least, by a step's time and a
-        // tile's own (us, fitted to the measurements) in a full round and, for the last, alone on the
-        // chip and in between. The smallest runs twice on a compute unit. Largest to smallest shape, 8192
-        // tokens x 2304 features: K = 768 31.5, 30.2, 30.9, 28.7 us, K = 4096 89.6, 81.1, 89.3, 86.7;
-        // 4096 x 4096 x 4096 58.0, 85.7, 74.8, 78.8; 4096 x 2048 x 4096 44.2, 42.2, 34.8, 36.8; 500 x 768 x 768
-        // 13.4, 12.6, 9.2, 7.4.
-        int dev = 0, ncu = 0;
-        hipError_t e = hipGetDevice(&dev);
-        if (e == hipSuccess) e = hipDeviceGetAttribute(&ncu, hipDeviceAttributeMultiprocessorCount, dev);
-        if (e != hipSuccess) return e;
-        const int steps = (a.K + BK - 1) / BK;
-        struct Time { float step, tile; };
-        auto us = [&](int f, int t, int at_once, Time full, Time alone) {
-            const int64_t tiles = static_cast<int64_t>((a.N + f - 1) / f) * ((a.M + t - 1) / t);
-            const float round = full.step * steps + full.tile, least = alone.step * steps + alone.tile;
-            const int64_t rest = tiles % at_once;
-            return static_cast<float>(tiles / at_once) * round + (rest ? least + (round - least) * rest / at_once : 0.f);
-        };
-        const float t0 = us(256, 256, ncu, {1.45f, 7.f}, {.89f, 6.f}), t1 = us(192, 256, ncu, {1.f, 7.6f}, {.82f, 6.5f}),
-                    t2 = us(128, 256, ncu, {.75f, 4.5f}, {.63f, 4.2f}), t3 = us(128, 128, 2 * ncu, {.74f, 4.9f}, {.51f, 3.5f});
-        const float least = std::min(std::min(t0, t1), std::min(t2, t3));
-        return least == t0 ? big<128, 128>(a, s) : least == t1 ? big<96, 128>(a, s) : least == t2 ? big<64, 128>(a, s) : big<64, 64>(a, s);
-    }
-    const int64_t tiles = (static_cast<int64_t>(a.N) + GT - 1) / GT * ((static_cast<int64_t>(a.M) + GT - 1) / GT);
-    hipLaunchKernelGGL(i8_any, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, s, a);
-    return hipGetLastError();
+    // The tile shape whose rounds over the compute units take the least, by a step's time and a
+    // tile's own (us, fitted to the measurements) in a full round and, for the last, alone on the
+    // chip and in between. The smallest runs twice on a compute unit. Largest to smallest shape, 8192
+    // tokens x 2304 features: K = 768 31.5, 30.2, 30.9, 28.7 us, K = 4096 89.6, 81.1, 89.3, 86.7;
+    // 4096 x 4096 x 4096 58.0, 85.7, 74.8, 78.8; 4096 x 2048 x 4096 44.2, 42.2, 34.8, 36.8; 500 x 768 x 768
+    // 13.4, 12.6, 9.2, 7.4.
+    int dev = 0, ncu = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e == hipSuccess) e = hipDeviceGetAttribute(&ncu, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e != hipSuccess) return e;
+    const int steps = (a.K + BK - 1) / BK;
+    struct Time { float step, tile; };
+    auto us = [&](int f, int t, int at_once, Time full, Time alone) {
+        const int64_t tiles = static_cast<int64_t>((a.N + f - 1) / f) * ((a.M + t - 1) / t);
+        const float round = full.step * steps + full.tile, least = alone.step * steps + alone.tile;
+        const int64_t rest = tiles % at_once;
+        return static_cast<float>(tiles / at_once) * round + (rest ? least + (round - least) * rest / at_once : 0.f);
+    };
+    const float t0 = us(256, 256, ncu, {1.45f, 7.f}, {.89f, 6.f}), t1 = us(192, 256, ncu, {1.f, 7.6f}, {.82f, 6.5f}),
+                t2 = us(128, 256, ncu, {.75f, 4.5f}, {.63f, 4.2f}), t3 = us(128, 128, 2 * ncu, {.74f, 4.9f}, {.51f, 3.5f});
+    const float least = std::min(std::min(t0, t1), std::min(t2, t3));
+    return least == t0 ? big<128, 128>(a, s) : least == t1 ? big<96, 128>(a, s) : least == t2 ? big<64, 128>(a, s) : big<64, 64>(a, s);
 }
 
 // Up to 16 rows whose bytes fit beside the sums in 64 KB: one launch from the features.

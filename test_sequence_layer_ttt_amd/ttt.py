@@ -15,7 +15,8 @@ from . import _lib
 from ._lib import TTT_BF16, TTT_F32, TTTError  # noqa: F401
 from .block import (ttt_block_norm, ttt_block_norm_backward, ttt_block_norm_backward_workspace,  # noqa: F401
                     ttt_conv_backward, ttt_conv_backward_workspace, ttt_conv_forward, ttt_conv_step,
-                    ttt_i8_linear, ttt_i8_linear_workspace, ttt_i8_project, ttt_i8_quantize,
+                    ttt_i8_linear, ttt_i8_linear_workspace, ttt_i8_project, ttt_i8_project_workspace,
+                    ttt_i8_quantize,
                     ttt_lru_backward, ttt_lru_backward_workspace, ttt_lru_forward,
                     ttt_lru_forward_workspace, ttt_lru_step, ttt_qkv_project_i8,
                     ttt_ssm_backward, ttt_ssm_backward_workspace, ttt_ssm_forward,

@@ -224,5 +224,9 @@ def test_refusals():
         ttt.ttt_i8_linear(f, w, ws, workspace=torch.empty(4096, dtype=torch.uint8, device="cuda")[1:])
     with pytest.raises(ttt.TTTError):
         ttt.ttt_i8_quantize(torch.zeros(1, 65537, device="cuda"))
+    ox, oxs, ow, ows, _ = _operands(70, 33, 8, 12)
+    assert ttt.ttt_i8_project_workspace(70, ox, ow) == 78 * 128
+    with pytest.raises(ttt.TTTError):
+        ttt.ttt_i8_project(ox, oxs, ow, ows, workspace=torch.empty(78 * 128 - 16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ttt.TTTError):
         ttt.ttt_i8_linear(f, w, ws, y=f[:, :8])

@@ -166,8 +166,13 @@ def _ops(dt=BF, B=2, L=400, D=200, seed=0):
     py = torch.empty(B, L, N, dtype=dt, device="cuda")
     ops["i8_project"] = (lambda s: ttt.ttt_i8_project(q2, sc2, w, wsc, dtype=dt, y=py, stream=s), [py], [sc2])
     ly = torch.empty(B, L, N, dtype=dt, device="cuda")
-    ws3 = torch.empty(ttt.ttt_i8_linear_workspace(B * L, K), dtype=torch.uint8, device="cuda")
+    ws3 = torch.empty(ttt.ttt_i8_linear_workspace(B * L, w), dtype=torch.uint8, device="cuda")
     ops["i8_linear"] = (lambda s: ttt.ttt_i8_linear(f, w, wsc, y=ly, workspace=ws3, stream=s), [ly], [f])
+    # rows that are laid out anew
+    wo, wso = ttt.ttt_i8_quantize(r(N, K - 1))
+    qo, oy = q2[..., 1:], torch.empty(B, L, N, dtype=dt, device="cuda")
+    ws4 = torch.empty(ttt.ttt_i8_project_workspace(B * L, qo, wo), dtype=torch.uint8, device="cuda")
+    ops["i8_project_odd"] = (lambda s: ttt.ttt_i8_project(qo, sc2, wo, wso, dtype=dt, y=oy, workspace=ws4, stream=s), [oy], [sc2])
     fy = torch.empty(B, N, dtype=dt, device="cuda")
     ops["i8_linear_few"] = (lambda s: ttt.ttt_i8_linear(f[:, 0], w, wsc, y=fy, workspace=ws3, stream=s), [fy], [f])
     th, ths = ttt.ttt_i8_quantize(r(3, 128, K))
@@ -177,7 +182,8 @@ def _ops(dt=BF, B=2, L=400, D=200, seed=0):
     return ops
 
 
-NAMES = ["lru_forward", "lru_backward", "lru_step", "i8_quantize", "i8_project", "i8_linear", "i8_linear_few", "qkv_project_i8"]
+NAMES = ["lru_forward", "lru_backward", "lru_step", "i8_quantize", "i8_project", "i8_project_odd", "i8_linear",
+         "i8_linear_few", "qkv_project_i8"]
 
 
 @pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
@@ -228,7 +234,7 @@ def test_captured_and_replayed(name):
         torch.randn(1 << 16, device="cuda").sum().item()  # eager work of the program's own
 
 
-@pytest.mark.parametrize("name", ["lru_forward", "lru_backward", "i8_project", "i8_linear"])
+@pytest.mark.parametrize("name", ["lru_forward", "lru_backward", "i8_project", "i8_project_odd", "i8_linear"])
 def test_two_calls_at_once(name):
     """Two streams, each with its own workspace and outputs."""
     a, b = _ops(BF, L=3000, D=520, seed=1)[name], _ops(BF, L=3000, D=520, seed=2)[name]

@@ -46,7 +46,8 @@ ALL = {
     "ttt_i8_quantize": [("M", 4), ("K", 64), ("io", 1), ("x", PTR[0]), ("xs", None), ("q", PTR[1]), ("qs", None),
                         ("scale", PTR[2])],
     "ttt_i8_project": [("M", 4), ("K", 64), ("N", 32), ("io", 1), ("x", PTR[0]), ("xs", None), ("x_scale", PTR[1]),
-                       ("w", PTR[2]), ("ws", None), ("w_scale", PTR[3]), ("bias", PTR[4]), ("y", PTR[5]), ("ys", None)],
+                       ("w", PTR[2]), ("ws", None), ("w_scale", PTR[3]), ("bias", PTR[4]), ("y", PTR[5]), ("ys", None),
+                       ("work", None), ("bytes", 0)],
     "ttt_i8_linear": [("M", 4), ("K", 64), ("N", 32), ("io", 1), ("x", PTR[0]), ("xs", None), ("w", PTR[2]), ("ws", None),
                       ("w_scale", PTR[3]), ("bias", PTR[4]), ("y", PTR[5]), ("ys", None), ("work", PTR[6]),
                       ("bytes", 1 << 30)],
@@ -144,9 +145,7 @@ def test_refuses_strides(lib):
 
 
 QUERIES = [("ttt_lru_forward", ttt.ttt_lru_forward_workspace, (2, 200, 64), "bytes"),
-           ("ttt_lru_backward", ttt.ttt_lru_backward_workspace, (2, 200, 64), "bytes"),
-           ("ttt_i8_linear", ttt.ttt_i8_linear_workspace, (4, 64), "bytes"),
-           ("ttt_qkv_project_i8", ttt.ttt_i8_linear_workspace, (16, 64), "bytes")]
+           ("ttt_lru_backward", ttt.ttt_lru_backward_workspace, (2, 200, 64), "bytes")]
 
 
 @pytest.mark.parametrize("fn,query,args,key", QUERIES, ids=lambda v: getattr(v, "__name__", None))
@@ -161,6 +160,62 @@ def test_workspaces(lib, fn, query, args, key):
         with pytest.raises(ttt.TTTError):
             query(*args[:i], -1, *args[i + 1:])
     assert getattr(lib, query.__name__)(*args, None) == NULL
+
+
+def _need(lib, fn, *args):
+    n = ctypes.c_size_t(0)
+    assert getattr(lib, fn)(*args, ctypes.byref(n)) == _lib.TTT_OK
+    return n.value
+
+
+@pytest.mark.parametrize("fn,query,at", [("ttt_i8_linear", (4, 64, 32, PTR[2], None), {}),
+                                         ("ttt_i8_linear", (100, 64, 32, PTR[2] + 1, None), dict(M=100, w=PTR[2] + 1)),
+                                         ("ttt_qkv_project_i8", (16, 64, 384, PTR[1], None), {}),
+                                         ("ttt_qkv_project_i8", (100, 72, 384, PTR[1], None), dict(L=50, dm=72))])
+def test_workspaces_of_products_of_features(lib, fn, query, at):
+    """The quantised rows and, with more than 64 of them, a weight whose rows are no whole chunks."""
+    n = _need(lib, "ttt_i8_linear_workspace", *query)
+    M, K, N, w, _ = query
+    pad = -(-K // 128) * 128
+    assert n == M * pad + -(-M // 4) * 16 + (N * pad if M > 64 and (K % 16 or w % 16) else 0)
+    assert call(lib, fn, **at, bytes=n - 1) == SHAPE
+    assert "workspace" in msg(lib)
+    assert call(lib, fn, **at, work=PTR[6] + 8) == ALIGN
+
+
+def test_workspaces_of_products_of_rows(lib):
+    q = lambda M, K, N, x=PTR[0], xs=None, w=PTR[2], ws=None: _need(lib, "ttt_i8_project_workspace", M, K, N, x, xs, w, ws)
+    assert q(100, 64, 32) == 0 and q(64, 65, 32) == 0 and q(0, 65, 32) == 0 and q(100, 65, 0) == 0
+    assert q(100, 65, 32) == (100 + 32) * 128
+    assert q(100, 64, 32, x=PTR[0] + 8) == 100 * 128 and q(100, 64, 32, w=PTR[2] + 1) == 32 * 128
+    assert q(100, 64, 32, xs=s(72)) == 100 * 128 and q(100, 64, 32, ws=s(1 << 23)) == 32 * 128
+    kw = dict(M=100, K=65)
+    assert call(lib, "ttt_i8_project", **kw) == SHAPE and "workspace" in msg(lib)
+    assert call(lib, "ttt_i8_project", **kw, work=PTR[9], bytes=132 * 128 - 1) == SHAPE
+    assert call(lib, "ttt_i8_project", **kw, work=None, bytes=1 << 20) == NULL
+    assert call(lib, "ttt_i8_project", **kw, work=PTR[9] + 8, bytes=1 << 20) == ALIGN
+    assert call(lib, "ttt_i8_project", **kw, work=PTR[0], bytes=1 << 20) == ALIAS
+    for f, args in (("ttt_i8_project_workspace", (4, 64, 32, None, None, None, None)), ("ttt_i8_linear_workspace", (4, 64, 32, None, None))):
+        assert getattr(lib, f)(*args, None) == NULL
+        n = ctypes.c_size_t(0)
+        for i in range(3):
+            assert getattr(lib, f)(*args[:i], -1, *args[i + 1:], ctypes.byref(n)) == SHAPE
+
+
+def test_workspace_queries_in_python():
+    import torch
+    w = torch.zeros(32, 64, dtype=torch.int8)
+    assert ttt.ttt_i8_linear_workspace(100, w) == 100 * 128 + 400
+    assert ttt.ttt_i8_linear_workspace(100, w[:, 1:]) == 132 * 128 + 400
+    assert ttt.ttt_i8_project_workspace(100, w[:, 1:], w[:, 1:]) == 132 * 128
+    assert ttt.ttt_i8_project_workspace(64, w[:, 1:], w[:, 1:]) == 0
+    for fn, args in ((ttt.ttt_i8_linear_workspace, (w,)), (ttt.ttt_i8_project_workspace, (w, w))):
+        with pytest.raises(ValueError, match="too large"):
+            fn(2**32, *args)
+        with pytest.raises(ttt.TTTError):
+            fn(-1, *args)
+        with pytest.raises(TypeError):
+            fn(1, *(t.float() for t in args))
 
 
 def test_empty_calls_launch_nothing(lib):
