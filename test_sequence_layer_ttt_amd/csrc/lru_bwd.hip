@@ -19,7 +19,7 @@ using namespace lru;
 // twice as long there).
 int tile_tokens(int B, int L, int D) {
     const int64_t wide = (static_cast<int64_t>(D) + CH - 1) / CH * B;
-    int t = D % 4 ? 32 : 64;
+    int t = 32;
     while (t > 16 && wide * ((L + t - 1) / t) < 1024) t /= 2;
     return t;
 }
@@ -28,22 +28,27 @@ __device__ __forceinline__ int live_tokens(const int *lens, int b, int L) {
     return lens ? max(0, min(lens[b], L)) : L;
 }
 
+// A tile with all of its tokens and channels, as nearly all are: its loops ask for no
+// token's or channel's place, whose branches cost copies of what is held across them.
+template <int TOKENS> __device__ __forceinline__ bool whole(const LruArgs &a, int n) {
+    return (blockIdx.x + 1) * TOKENS <= static_cast<unsigned>(n) && (blockIdx.y + 1) * CH <= static_cast<unsigned>(a.D);
+}
+
 // U tokens of V channels as stored, all asked for at once; rows past the
 // sequence's end are read from its last.
-template <typename T, int V, int U> struct Tokens {
+template <typename T, int V, int U, bool GATED, bool FULL> struct Tokens {
     typename VecIO<T, V>::Raw x[U], r[U], i[U], dy[U];
-    bool gated;
-    __device__ __forceinline__ Tokens(const LruBwdArgs &g, int b, int c, int t0, int n) : gated(g.f.i != nullptr) {
+    __device__ __forceinline__ Tokens(const LruBwdArgs &g, int b, int c, int t0, int n) {
         const LruArgs &a = g.f;
         const T *px = static_cast<const T *>(a.x) + b * a.xb + c, *pr = static_cast<const T *>(a.r) + b * a.rb + c,
                 *pd = static_cast<const T *>(g.dy) + b * g.dyb + c, *pi = static_cast<const T *>(a.i) + b * a.ib + c;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t t = min(t0 + u, n - 1);
+            const int64_t t = FULL ? t0 + u : min(t0 + u, n - 1);
             x[u] = VecIO<T, V>::raw(px + t * a.xt);
             r[u] = VecIO<T, V>::raw(pr + t * a.rt);
             dy[u] = VecIO<T, V>::raw(pd + t * g.dyt);
-            if (gated) i[u] = VecIO<T, V>::raw(pi + t * a.it);
+            if (GATED) i[u] = VecIO<T, V>::raw(pi + t * a.it);
         }
     }
     Tokens() = default;
@@ -51,35 +56,32 @@ template <typename T, int V, int U> struct Tokens {
 
 // Each tile's decay A, its own share H of the state behind it and its own
 // share K = sum A_t dy_t of what flows out before it: ws[b][tile][3][D].
-template <typename T, int V, int U, bool RATE>
-__global__ __launch_bounds__(NT) void lru_bwd_shares(LruBwdArgs g, int nt) {
+template <typename T, int V, int U, bool RATE, bool GATED, bool FULL>
+__device__ __forceinline__ void shares(const LruBwdArgs &g, int nt, int n, float2 (*sm)[CH], float (*smk)[CH]) {
     constexpr int CL = CH / V, TG = NT / CL;  // lanes along the channels, runs of tokens
-    __shared__ float2 sm[TG][CH];
-    __shared__ float smk[TG][CH];
     const LruArgs &a = g.f;
     const int lane = threadIdx.x % CL, run = threadIdx.x / CL;
     const int b = blockIdx.z, tile = blockIdx.x, c0 = blockIdx.y * CH, c = c0 + lane * V;
-    const int n = live_tokens(a.lens, b, a.L);
     const int t0 = (tile * TG + run) * U;
     float A[V], H[V], K[V], rate[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = K[v] = 0.f, rate[v] = 0.f;
-    if (RATE && c < a.D) load_rate<V>(a.rate + c, rate);
-    if (c < a.D && t0 < n) {
-        const Tokens<T, V, U> p(g, b, c, t0, n);
+    if (RATE && (FULL || c < a.D)) load_rate<V>(a.rate + c, rate);
+    if (FULL || (c < a.D && t0 < n)) {
+        const Tokens<T, V, U, GATED, FULL> p(g, b, c, t0, n);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (t0 + u >= n) continue;
+            if (!FULL && t0 + u >= n) continue;
             float xv[V], rv[V], iv[V] = {}, dv[V];
             VecIO<T, V>::unpack(p.x[u], xv);
             VecIO<T, V>::unpack(p.r[u], rv);
             VecIO<T, V>::unpack(p.dy[u], dv);
-            if (p.gated) VecIO<T, V>::unpack(p.i[u], iv);
+            if (GATED) VecIO<T, V>::unpack(p.i[u], iv);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const Gate k = gate<RATE>(rv[v], rate[v]);
                 float w = k.s * xv[v];
-                if (p.gated) w *= sigmoid(iv[v]);
+                if (GATED) w *= sigmoid(iv[v]);
                 H[v] = fmaf(k.a, H[v], w);
                 A[v] *= k.a;
                 K[v] = fmaf(A[v], dv[v], K[v]);
@@ -93,7 +95,7 @@ __global__ __launch_bounds__(NT) void lru_bwd_shares(LruBwdArgs g, int nt) {
     }
     __syncthreads();
     const int cc = c0 + threadIdx.x;
-    if (threadIdx.x < CH && cc < a.D) {
+    if (threadIdx.x < CH && (FULL || cc < a.D)) {
         float2 all = make_float2(1.f, 0.f);
         float k = 0.f;
 #pragma unroll
@@ -107,6 +109,17 @@ __global__ __launch_bounds__(NT) void lru_bwd_shares(LruBwdArgs g, int nt) {
         w[a.D] = all.y;
         w[2 * static_cast<int64_t>(a.D)] = k;
     }
+}
+template <typename T, int V, int U, bool RATE, bool GATED>
+__global__ __launch_bounds__(NT) void lru_bwd_shares(LruBwdArgs g, int nt) {
+    constexpr int TG = NT / (CH / V);
+    __shared__ float2 sm[TG][CH];
+    __shared__ float smk[TG][CH];
+    const int n = live_tokens(g.f.lens, blockIdx.z, g.f.L);
+    if (whole<TG * U>(g.f, n))
+        shares<T, V, U, RATE, GATED, true>(g, nt, n, sm, smk);
+    else
+        shares<T, V, U, RATE, GATED, false>(g, nt, n, sm, smk);
 }
 
 // The state before each tile over its H (z = 0), and what flows into it from
@@ -164,49 +177,47 @@ __global__ __launch_bounds__(CC *CR) void lru_bwd_carry(LruBwdArgs g, int n) {
     }
 }
 
-template <typename T, int V, int U, bool RATE>
-__global__ __launch_bounds__(NT) void lru_bwd_grads(LruBwdArgs g, int nt) {
+template <typename T, int V, int U, bool RATE, bool GATED, bool FULL>
+__device__ __forceinline__ void grads(const LruBwdArgs &g, int nt, int n, float2 (*sm)[CH], float (*smk)[CH]) {
     typedef VecIO<T, V> IO;
     constexpr int CL = CH / V, TG = NT / CL;
-    __shared__ float2 sm[TG][CH];
-    __shared__ float smk[TG][CH];
     const LruArgs &a = g.f;
     const int lane = threadIdx.x % CL, run = threadIdx.x / CL;
     const int b = blockIdx.z, tile = blockIdx.x, c0 = blockIdx.y * CH, c = c0 + lane * V;
-    const int n = live_tokens(a.lens, b, a.L);
     const int t0 = (tile * TG + run) * U;
-    const bool in = c < a.D;
+    const bool in = FULL || c < a.D;
     // held from here to the way back: the rows as stored, and of each value the decay, the scale
     // and the state before it; the gates' own values are cheaper formed again
     float A[V], H[V], K[V], rate[V], da[U][V], ds[U][V], hp[U][V];
-    Tokens<T, V, U> p;
+    Tokens<T, V, U, GATED, FULL> p;
 #pragma unroll
     for (int v = 0; v < V; ++v) A[v] = 1.f, H[v] = K[v] = 0.f, rate[v] = 0.f;
-    const bool some = in && t0 < n;
+    const bool some = FULL || (in && t0 < n);
     if (RATE && in) load_rate<V>(a.rate + c, rate);
-    if (some) p = Tokens<T, V, U>(g, b, c, t0, n);
+    if (some) p = Tokens<T, V, U, GATED, FULL>(g, b, c, t0, n);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
         for (int v = 0; v < V; ++v) hp[u][v] = H[v], da[u][v] = 1.f, ds[u][v] = 0.f;
-        if (some && t0 + u < n) {
+        if (FULL || (some && t0 + u < n)) {
             float xv[V], rv[V], iv[V] = {}, dv[V];
             IO::unpack(p.x[u], xv);
             IO::unpack(p.r[u], rv);
             IO::unpack(p.dy[u], dv);
-            if (p.gated) IO::unpack(p.i[u], iv);
+            if (GATED) IO::unpack(p.i[u], iv);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const Gate k = gate<RATE>(rv[v], rate[v]);
                 da[u][v] = k.a;
                 ds[u][v] = k.s;
                 float w = k.s * xv[v];
-                if (p.gated) w *= sigmoid(iv[v]);
+                if (GATED) w *= sigmoid(iv[v]);
                 H[v] = fmaf(k.a, H[v], w);
                 A[v] *= k.a;
                 K[v] = fmaf(A[v], dv[v], K[v]);
             }
         }
+        if (FULL) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -249,24 +260,26 @@ __global__ __launch_bounds__(NT) void lru_bwd_grads(LruBwdArgs g, int nt) {
         }
     }
     T *dx = static_cast<T *>(g.dx) + b * g.dxb + c, *drp = static_cast<T *>(g.dr) + b * g.drb + c;
-    T *di = g.di ? static_cast<T *>(g.di) + b * g.dib + c : nullptr;
+    T *di = static_cast<T *>(g.di) + b * g.dib + c;
 #pragma unroll
     for (int u = U - 1; u >= 0; --u) {
         const int t = t0 + u;
         float ox[V] = {}, orr[V] = {}, oi[V] = {};
-        if (some && t < n) {
-            float xv[V], rv[V], iv[V] = {}, dv[V];
+        if (FULL || (some && t < n)) {
+            float xv[V], rv[V] = {}, iv[V] = {}, dv[V];
             IO::unpack(p.x[u], xv);
             IO::unpack(p.dy[u], dv);
             if (RATE) IO::unpack(p.r[u], rv);
-            if (p.gated) IO::unpack(p.i[u], iv);
+            if (GATED) IO::unpack(p.i[u], iv);
+#pragma unroll
+            for (int v = 0; v < V; ++v) asm volatile("" : "+v"(rv[v]), "+v"(iv[v]));
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float at = da[u][v], st = ds[u][v], G = dv[v] + K[v], gs = G * st;
                 K[v] = at * G;
                 float x = xv[v];  // sigma(i) x
                 ox[v] = gs;
-                if (p.gated) {
+                if (GATED) {
                     float ne;
                     const float e = sigmoid2(iv[v], &ne);
                     x *= e;
@@ -285,11 +298,12 @@ __global__ __launch_bounds__(NT) void lru_bwd_grads(LruBwdArgs g, int nt) {
                 }
             }
         }
-        if (in && t < a.L) {
+        if (FULL || (in && t < a.L)) {
             stream_store<T, V>(dx + t * g.dxt, ox);
             stream_store<T, V>(drp + t * g.drt, orr);
-            if (di) stream_store<T, V>(di + t * g.dit, oi);
+            if (GATED) stream_store<T, V>(di + t * g.dit, oi);
         }
+        if (FULL) __builtin_amdgcn_sched_barrier(0);
     }
     if (in && g.dstate && tile == 0 && run == 0) {
 #pragma unroll
@@ -309,6 +323,17 @@ __global__ __launch_bounds__(NT) void lru_bwd_grads(LruBwdArgs g, int nt) {
         }
     }
 }
+template <typename T, int V, int U, bool RATE, bool GATED>
+__global__ __launch_bounds__(NT) void lru_bwd_grads(LruBwdArgs g, int nt) {
+    constexpr int TG = NT / (CH / V);
+    __shared__ float2 sm[TG][CH];
+    __shared__ float smk[TG][CH];
+    const int n = live_tokens(g.f.lens, blockIdx.z, g.f.L);
+    if (whole<TG * U>(g.f, n))
+        grads<T, V, U, RATE, GATED, true>(g, nt, n, sm, smk);
+    else
+        grads<T, V, U, RATE, GATED, false>(g, nt, n, sm, smk);
+}
 
 // L = 0: the state's gradient passes through
 __global__ __launch_bounds__(NT) void lru_bwd_pass(LruBwdArgs g) {
@@ -318,14 +343,18 @@ __global__ __launch_bounds__(NT) void lru_bwd_pass(LruBwdArgs g) {
 
 bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
-template <typename T, int V, int U, bool RATE> void tiled(const LruBwdArgs &g, int nt, hipStream_t s) {
+template <typename T, int V, int U, bool RATE, bool GATED> void tiled(const LruBwdArgs &g, int nt, hipStream_t s) {
     const LruArgs &a = g.f;
     const dim3 grid(nt, (a.D + CH - 1) / CH, a.B);
     if (nt > 1) {
-        hipLaunchKernelGGL((lru_bwd_shares<T, V, U, RATE>), grid, dim3(NT), 0, s, g, nt);
+        hipLaunchKernelGGL((lru_bwd_shares<T, V, U, RATE, GATED>), grid, dim3(NT), 0, s, g, nt);
         hipLaunchKernelGGL(lru_bwd_carry, dim3((a.D + CC - 1) / CC, a.B, 2), dim3(CC * CR), 0, s, g, nt);
     }
-    hipLaunchKernelGGL((lru_bwd_grads<T, V, U, RATE>), grid, dim3(NT), 0, s, g, nt);
+    hipLaunchKernelGGL((lru_bwd_grads<T, V, U, RATE, GATED>), grid, dim3(NT), 0, s, g, nt);
+}
+
+template <typename T, int V, int U, bool RATE> void gated(const LruBwdArgs &g, int nt, hipStream_t s) {
+    g.f.i ? tiled<T, V, U, RATE, true>(g, nt, s) : tiled<T, V, U, RATE, false>(g, nt, s);
 }
 
 template <typename T, int V, bool RATE> hipError_t backward(const LruBwdArgs &g, hipStream_t s) {
@@ -338,12 +367,10 @@ template <typename T, int V, bool RATE> hipError_t backward(const LruBwdArgs &g,
         if (g.dstate && n)
             hipLaunchKernelGGL(lru_bwd_pass, dim3(static_cast<unsigned>((n + NT - 1) / NT)), dim3(NT), 0, s, g);
     } else if (a.B) {
-        if (tokens == 64)
-            tiled<T, V, 64 / TG, RATE>(g, nt, s);
-        else if (tokens == 32)
-            tiled<T, V, 32 / TG, RATE>(g, nt, s);
+        if (tokens == 32)
+            gated<T, V, 32 / TG, RATE>(g, nt, s);
         else
-            tiled<T, V, 16 / TG, RATE>(g, nt, s);
+            gated<T, V, 16 / TG, RATE>(g, nt, s);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !RATE) return e;
