@@ -667,14 +667,14 @@ int ttt_block_norm_backward_workspace(int B, int L, int D, int gate_shape, size_
  *     a_t = sigma(r_t),            s_t = 1 - a_t           where rate is NULL
  * (sigma(i_t) = 1 where i is NULL).
  *   1 <= D <= TTT_LRU_MAX_D; 0 <= B <= 65535; B*ceil(L/64) at most
- *   TTT_LRU_MAX_TILES.
+ *   TTT_LRU_MAX_TILES, and times ceil(D/128) below 2^24 where L > 64.
  *   x, r, i, y : [B,L,D] io, strided (batch, token).
  *   rate       : [D] fp32, >= 0, or NULL. Below 0 the state would grow: s is NaN.
  *   state      : [B,D] fp32 or NULL (zeros); state_out : the same or NULL; it
  *                may be exactly `state`.
  * The workspace holds ttt_lru_forward_workspace's bytes (decays and states at
  * the borders of the tiles that run side by side; none for a prompt of one
- * tile); calls that share one must not overlap.
+ * tile), 16-byte aligned; calls that share one must not overlap.
  * Numerics: gates, decays and the state in fp32; 1 - a keeps its relative
  * accuracy where a is near 1. A value that is not finite reaches the outputs of
  * its channel from its token on, as itself or as NaN, and the state.
@@ -703,8 +703,8 @@ int ttt_lru_step(int B, int D, int io, const void *x, const int64_t *x_strides, 
  * [B,L,D] io, strided; drate [D] and dstate [B,D] fp32; di, drate and dstate
  * NULL exactly when i, rate and state are. Where a gate is so far closed that
  * s_t = 0, the derivative of s_t (infinite there) counts as 0. The workspace
- * holds ttt_lru_backward_workspace's bytes; calls that share one must not
- * overlap.
+ * holds ttt_lru_backward_workspace's bytes, 16-byte aligned; calls that share
+ * one must not overlap.
  */
 int ttt_lru_backward(int B, int L, int D, int io, const void *x, const int64_t *x_strides,
                      const void *r, const int64_t *r_strides, const void *i,

@@ -17,6 +17,8 @@ int lru_common(int B, int L, int D, int io) {
     // tiles of 64 tokens: a grid's workgroups and threads are counted in 32 bits
     if (static_cast<int64_t>(B > 1 ? B : 1) * ((static_cast<int64_t>(L) + 63) / 64) > TTT_LRU_MAX_TILES)
         return fail(TTT_E_SHAPE, "B*ceil(L/64) exceeds %d (B = %d, L = %d)", TTT_LRU_MAX_TILES, B, L);
+    if (L > 64 && B * ((static_cast<int64_t>(L) + 63) / 64) * ((D + 127) / 128) >= 1 << 24)
+        return fail(TTT_E_SHAPE, "B*ceil(L/64)*ceil(D/128) is 2^24 or more (B = %d, L = %d, D = %d)", B, L, D);
     return TTT_OK;
 }
 

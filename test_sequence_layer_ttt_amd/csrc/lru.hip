@@ -54,7 +54,6 @@ struct Plan {
     int tokens;  // of a tile
     int64_t tiles, groups;
 };
-Plan plan(int B, int L, int D);
 
 // workspace: the columns' counters, then the tiles' (A, H) [B][tiles][D], then the states behind groups [B][groups][D]
 constexpr int LINE = 16;  // words
@@ -264,14 +263,22 @@ template <typename T> bool vectors(const LruArgs &a) {
            aligned(a.x, 16) && aligned(a.r, 16) && aligned(a.i, 16) && aligned(a.y, 16);
 }
 
-// Tiles of 128 tokens where that leaves four for each compute unit, else of 64, of 32.
-Plan plan(int B, int L, int D) {
+// Tiles of 128 tokens, shorter ones where that would leave fewer than four for each compute
+// unit. With input gates, whose tokens are more work, 64 at the most from 32 columns on: 8 x
+// 2048 tokens of 2048 channels 67 -> 64 us, 16 x 4096 223 -> 205, 2 x 8192 in fp32 117 -> 101;
+// without gates they are slower (2 x 32768 146 -> 155), and over 16 columns the chain is what
+// a long prompt waits for (32768 of 2048 118 -> 133).
+Plan plan(int B, int L, int D, bool gated) {
     const int64_t wide = (static_cast<int64_t>(D) + CH - 1) / CH * B;
-    int tokens = 128;
+    int tokens = gated && wide >= 32 ? 64 : 128;
     while (tokens > 32 && wide * ((L + tokens - 1) / tokens) < 1024) tokens /= 2;
     Plan p{tokens, (static_cast<int64_t>(L) + tokens - 1) / tokens, 0};
     p.groups = p.tiles / GROUP;
     return p;
+}
+int64_t floats(const Plan &p, int B, int D) {  // in whole 16 bytes
+    const int64_t columns = (static_cast<int64_t>(D) + CH - 1) / CH * B;
+    return p.tiles > 1 ? (LINE * columns + (2 * p.tiles + p.groups) * B * D + 3) / 4 * 4 : 0;
 }
 
 template <typename T, int V, int U, bool RATE, bool GATED> hipError_t scan(const LruArgs &a, const Plan &p, hipStream_t s) {
@@ -279,7 +286,7 @@ template <typename T, int V, int U, bool RATE, bool GATED> hipError_t scan(const
     const int ncb = (a.D + CH - 1) / CH;
     if (nch > 1) {
         const dim3 grid(static_cast<unsigned>(nch) * ncb * a.B);
-        const int64_t words = lru_forward_floats(a.B, a.L, a.D) / 4;
+        const int64_t words = floats(p, a.B, a.D) / 4;
         hipLaunchKernelGGL(lru_clear, dim3(static_cast<unsigned>((words + NT - 1) / NT)), dim3(NT), 0, s,
                            reinterpret_cast<uint4 *>(a.ws), words);
         hipLaunchKernelGGL((lru_scan<T, V, U, RATE, GATED, true>), grid, dim3(NT), 0, s, a, nch, ngr);
@@ -294,7 +301,7 @@ template <typename T, int V, int U, bool RATE> hipError_t gated(const LruArgs &a
 }
 
 template <typename T, int V, bool RATE> hipError_t forward(const LruArgs &a, hipStream_t s) {
-    const Plan p = plan(a.B, a.L, a.D);
+    const Plan p = plan(a.B, a.L, a.D, a.i);
     if (!p.tiles) {  // the caller has asked for the state alone
         const int64_t n = static_cast<int64_t>(a.B) * a.D;
         hipLaunchKernelGGL(lru_pass, dim3(static_cast<unsigned>((n + NT - 1) / NT)), dim3(NT), 0, s, a);
@@ -326,12 +333,8 @@ template <typename T> hipError_t step_t(const LruArgs &a, hipStream_t s) {
 
 }  // namespace
 
-int64_t lru_forward_floats(int B, int L, int D) {
-    const Plan p = plan(B, L, D);
-    const int64_t columns = (static_cast<int64_t>(D) + CH - 1) / CH * B;
-    // in whole 16 bytes
-    return p.tiles > 1 ? (LINE * columns + (2 * p.tiles + p.groups) * B * D + 3) / 4 * 4 : 0;
-}
+// by the sizes alone: tiles are shorter with input gates, if any, and need more
+int64_t lru_forward_floats(int B, int L, int D) { return floats(plan(B, L, D, true), B, D); }
 hipError_t launch_lru_forward(const LruArgs &a, hipStream_t s) {
     return a.io ? forward_t<bf16_t>(a, s) : forward_t<float>(a, s);
 }

@@ -228,3 +228,12 @@ def test_empty_calls_launch_nothing(lib):
     assert call(lib, "ttt_i8_linear", M=0, x=None, y=None, work=None, bytes=0) == _lib.TTT_OK
     assert call(lib, "ttt_qkv_project_i8", H=0, theta=None, theta_scale=None, XQ=None, XK=None, XV=None) == _lib.TTT_OK
     assert call(lib, "ttt_qkv_project_i8", L=0, x=None, XQ=None, XK=None, XV=None, work=None, bytes=0) == _lib.TTT_OK
+
+
+@pytest.mark.parametrize("query", [ttt.ttt_lru_forward_workspace, ttt.ttt_lru_backward_workspace])
+def test_grids_are_counted_in_32_bits(query):
+    query(1, 1 << 26, 1024)
+    query(65535, 64, 1 << 20)  # one tile a sequence: a grid of two dimensions
+    for sizes in ((1, 1 << 26, 2048), (1, 1 << 27, 1024), (65535, 65, 1 << 15)):
+        with pytest.raises(ttt.TTTError, match=r"ceil\(D/128\)"):
+            query(*sizes)
