@@ -104,8 +104,8 @@ __device__ __forceinline__ void store4(const I8Args &a, int m, int n, float sx, 
 
 // Rows of K bytes at any address as rows of whole 128-byte lines, zeros past K: for
 // operands that the large products could not read 16 bytes at a time. A wave a row.
-// 16384 and 2048 rows of 2047: 16 us and the product 62, where reading them as they
-// stand for each tile took 305; 1551 and 1037 rows of 771: 4.3 and 13, and 17.
+// 16384 and 2048 rows of 2047: 14 us and the product 74, where reading them as they
+// stand for each tile took 305; 1551 and 1037 rows of 771: 4.6 and 13.5, and 17.
 __global__ __launch_bounds__(256) void i8_pad(I8PadArgs a) {
     const int lane = threadIdx.x & 63;
     int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
@@ -618,6 +618,8 @@ hipError_t launch_i8_project(const I8Args &in, hipStream_t s) {
     outputs(a);
     if (a.M <= 16) return few<1, 1>(a, s);
     if (a.M <= 32) return few<1, 2>(a, s);
+    // two tiles of features a workgroup where that still leaves half the compute units one: 64 x
+    // 2048 x 6144 11.6 -> 8.6 us (a row of x is read half as often); below, one
     if (a.M <= 64) return a.N >= 4096 ? few<2, 4>(a, s) : few<1, 4>(a, s);
     // The tile shape whose rounds over the compute units take the least, by a step's time and a
     // tile's own (us, fitted to the measurements) in a full round and, for the last, alone on the

@@ -40,11 +40,15 @@ __device__ __forceinline__ void token(const float (&x)[V], const float (&r)[V], 
 // its place by the column's counter as it starts, so that whatever a tile waits
 // for has started before it and waits for earlier ones alone. A counter for each
 // column, on lines of their own: one for all cost 8 ns a tile, one after the other.
-// A
-// published value carries its own flag: a word is ready where it is not all
-// ones (cleared to that before; a NaN of this very pattern is published as
-// another NaN). Words are written and read as single atomics at the scope of
-// the device, past the XCDs' L2 caches.
+// A published value carries its own flag: a word is ready where it is not all ones
+// (cleared to that before; a NaN of this very pattern is published as another NaN).
+// Words are written and read as single atomics at the scope of the device, past the
+// XCDs' L2 caches.
+//
+// What bounds it is HBM: every row is read and written once. 2 x 8192 tokens of 2048
+// bf16 channels (268 MB) take 57 us, 32768 without input gates (403 MB) 76 us, 4.7 and
+// 5.3 TB/s, and lru_clear 5 us before them. Groups of 8 tiles, at 32768 tokens: 83 us a
+// call; of 4 95 (a chain of twice as many links), of 16 86 (more shares to join for a tile).
 constexpr int GROUP = 8;
 constexpr uint32_t WAIT32 = 0xffffffffu;
 constexpr uint64_t WAIT64 = 0xffffffffffffffffull;
@@ -234,6 +238,7 @@ __global__ __launch_bounds__(NT) void lru_pass(LruArgs a) {
     if (k < static_cast<int64_t>(a.B) * a.D) a.state_out[k] = a.state ? a.state[k] : 0.f;
 }
 
+// A single token: a thread V channels. 64 x 2048 channels: 3.4 us, a launch.
 template <typename T, int V, bool RATE>
 __global__ __launch_bounds__(NT) void lru_step(LruArgs a) {
     typedef VecIO<T, V> IO;

@@ -6,6 +6,15 @@
 //     dx = G s sigma(i),  di = G s x sigma(i) (1 - sigma(i)),  dstate = K_1,
 //     dr = -rate l sigma(r) (1 - sigma(r)),  drate = -sum l sigma(r)   with a rate,
 //     dr = l (1 - a)                                                  without.
+//
+// Two passes over the inputs: lru_bwd_shares gives what each tile does to the state and
+// to K, lru_bwd_carry the values at the tiles' borders from those (both directions at
+// once), lru_bwd_grads walks again with them. A tile waits for both directions, so
+// that one pass would need all tiles of a column on the chip at once. Eleven rows are moved
+// instead of seven: for 2 x 8192 tokens of 2048 bf16 channels 45 + 8 + 102 us, and 6 for
+// drate's sums; both passes run at a large copy's rate (5.9 and 4.7 TB/s). A gate is
+// formed again on the way back rather than held: held, a thread takes 182 registers
+// instead of 158, and 187 us instead of 178.
 #include "block.hpp"
 #include "lru.hpp"
 
@@ -14,9 +23,9 @@ namespace {
 
 using namespace lru;
 
-// A tile's tokens: 64 where that leaves four workgroups for each compute unit, 32 or
-// 16 otherwise, and 32 at most for widths that no vector divides (a thread's run is
-// twice as long there).
+// A tile's tokens: 32, or 16 where that would leave fewer than four workgroups for each
+// compute unit. 64 take more registers than two waves a SIMD have: 2 x 8192 tokens of 2048
+// channels 200 us, 178 with 32.
 int tile_tokens(int B, int L, int D) {
     const int64_t wide = (static_cast<int64_t>(D) + CH - 1) / CH * B;
     int t = 32;
@@ -187,7 +196,7 @@ __device__ __forceinline__ void grads(const LruBwdArgs &g, int nt, int n, float2
     const int t0 = (tile * TG + run) * U;
     const bool in = FULL || c < a.D;
     // held from here to the way back: the rows as stored, and of each value the decay, the scale
-    // and the state before it; the gates' own values are cheaper formed again
+    // and the state before it
     float A[V], H[V], K[V], rate[V], da[U][V], ds[U][V], hp[U][V];
     Tokens<T, V, U, GATED, FULL> p;
 #pragma unroll
@@ -272,7 +281,7 @@ __device__ __forceinline__ void grads(const LruBwdArgs &g, int nt, int n, float2
             if (RATE) IO::unpack(p.r[u], rv);
             if (GATED) IO::unpack(p.i[u], iv);
 #pragma unroll
-            for (int v = 0; v < V; ++v) asm volatile("" : "+v"(rv[v]), "+v"(iv[v]));
+            for (int v = 0; v < V; ++v) asm volatile("" : "+v"(rv[v]), "+v"(iv[v]));  // formed again, not held
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float at = da[u][v], st = ds[u][v], G = dv[v] + K[v], gs = G * st;
