@@ -268,14 +268,11 @@ template <typename T> bool vectors(const LruArgs &a) {
            aligned(a.x, 16) && aligned(a.r, 16) && aligned(a.i, 16) && aligned(a.y, 16);
 }
 
-// Tiles of 128 tokens, shorter ones where that would leave fewer than four for each compute
-// unit. With input gates, whose tokens are more work, 64 at the most from 32 columns on: 8 x
-// 2048 tokens of 2048 channels 67 -> 64 us, 16 x 4096 223 -> 205, 2 x 8192 in fp32 117 -> 101;
-// without gates they are slower (2 x 32768 146 -> 155), and over 16 columns the chain is what
-// a long prompt waits for (32768 of 2048 118 -> 133).
-Plan plan(int B, int L, int D, bool gated) {
+// Tiles of `most` tokens, shorter ones where that would leave fewer than four for each
+// compute unit.
+Plan plan(int B, int L, int D, int most) {
     const int64_t wide = (static_cast<int64_t>(D) + CH - 1) / CH * B;
-    int tokens = gated && wide >= 32 ? 64 : 128;
+    int tokens = most;
     while (tokens > 32 && wide * ((L + tokens - 1) / tokens) < 1024) tokens /= 2;
     Plan p{tokens, (static_cast<int64_t>(L) + tokens - 1) / tokens, 0};
     p.groups = p.tiles / GROUP;
@@ -305,17 +302,28 @@ template <typename T, int V, int U, bool RATE> hipError_t gated(const LruArgs &a
     return a.i ? scan<T, V, U, RATE, true>(a, p, s) : scan<T, V, U, RATE, false>(a, p, s);
 }
 
+// 128 tokens where a thread takes 8 channels and there are no input gates (2 x 32768 tokens of
+// 2048 channels 146 us, with 64 155) or fewer than 32 columns, whose chain a long prompt waits
+// for (32768 of 2048 118, 133). Otherwise 64: with input gates, whose tokens are more work (8 x
+// 2048 of 2048 67 -> 64 us, 16 x 4096 223 -> 205), and with fewer channels a thread, whose runs
+// are as many times longer (2 x 8192 of 2048 in fp32 117 -> 101, 32768 of 2047 in bf16 320 -> 210).
+template <int V> int most_tokens(const LruArgs &a) {
+    const int64_t wide = (static_cast<int64_t>(a.D) + CH - 1) / CH * a.B;
+    return V == 8 && !(a.i && wide >= 32) ? 128 : 64;
+}
+
 template <typename T, int V, bool RATE> hipError_t forward(const LruArgs &a, hipStream_t s) {
-    const Plan p = plan(a.B, a.L, a.D, a.i);
+    const Plan p = plan(a.B, a.L, a.D, most_tokens<V>(a));
     if (!p.tiles) {  // the caller has asked for the state alone
         const int64_t n = static_cast<int64_t>(a.B) * a.D;
         hipLaunchKernelGGL(lru_pass, dim3(static_cast<unsigned>((n + NT - 1) / NT)), dim3(NT), 0, s, a);
         return hipGetLastError();
     }
     constexpr int TG = NT / (CH / V);
-    return p.tokens == 128 ? gated<T, V, 128 / TG, RATE>(a, p, s)
-           : p.tokens == 64 ? gated<T, V, 64 / TG, RATE>(a, p, s)
-                            : gated<T, V, 32 / TG, RATE>(a, p, s);
+    if constexpr (V == 8) {
+        if (p.tokens == 128) return gated<T, V, 128 / TG, RATE>(a, p, s);
+    }
+    return p.tokens == 64 ? gated<T, V, 64 / TG, RATE>(a, p, s) : gated<T, V, 32 / TG, RATE>(a, p, s);
 }
 
 template <typename T, int V, bool RATE> hipError_t step(const LruArgs &a, hipStream_t s) {
@@ -338,8 +346,8 @@ template <typename T> hipError_t step_t(const LruArgs &a, hipStream_t s) {
 
 }  // namespace
 
-// by the sizes alone: tiles are shorter with input gates, if any, and need more
-int64_t lru_forward_floats(int B, int L, int D) { return floats(plan(B, L, D, true), B, D); }
+// by the sizes alone: of the tiles that need the most
+int64_t lru_forward_floats(int B, int L, int D) { return floats(plan(B, L, D, 64), B, D); }
 hipError_t launch_lru_forward(const LruArgs &a, hipStream_t s) {
     return a.io ? forward_t<bf16_t>(a, s) : forward_t<float>(a, s);
 }

@@ -52,7 +52,7 @@ def _f64(d, B, L):
     return e, keep
 
 
-FORWARD = [  # tokens of a tile; B, L, D, type, rate, gate, lens
+FORWARD = [  # tokens of the longest tile that still fills the chip; B, L, D, type, rate, gate, lens
     (64, 32, 1020, 136, BF, True, True, True), (64, 32, 1024, 136, F32, False, True, False),
     (64, 32, 1020, 137, BF, False, True, False), (64, 32, 1020, 137, F32, True, True, True),
     (128, 32, 2040, 136, BF, True, False, False), (128, 32, 1930, 136, F32, False, False, True),
