@@ -237,10 +237,11 @@ def ttt_i8_quantize(x, q=None, scale=None, stream=None):
 
 
 def _rows(t) -> tuple:
-    """Address and row stride of a matrix, as the workspace queries take them."""
+    """Address and row stride of rows of 8-bit values, as the calls take them: a
+    dimension of size 1 has no say in the stride."""
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int8 or t.dim() < 1:
         raise TypeError("rows must be an int8 torch.Tensor")
-    stride = t.stride(-2) if t.dim() > 1 and t.numel() > t.size(-1) else t.size(-1)
+    stride = next((t.stride(d) for d in range(t.dim() - 2, -1, -1) if t.size(d) != 1), t.size(-1))
     return t.data_ptr() or None, ctypes.byref(ctypes.c_int64(stride))
 
 
