@@ -21,3 +21,29 @@ def test_a_workspace_as_large_as_the_query_says(row, at):
     y = ttt.ttt_i8_project(x, xs, w, ws, dtype=F32, workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
     assert y.shape == (100, 1, 40)
     assert torch.equal(y[:, 0], ttt.ttt_i8_project(x[:, 0].contiguous(), xs[:, 0], w, ws, dtype=F32))
+
+
+def _overlapping(M, K, seed):
+    """[M,K] in bf16 whose rows are one value apart: M different rows in M + K values."""
+    x = torch.randn(M + K, generator=torch.Generator("cuda").manual_seed(seed), device="cuda").to(BF)
+    return x.as_strided((M, K), (1, 1))
+
+
+def test_as_many_rows_as_the_quantiser_takes():
+    """2^24 rows of a workgroup each: 2^32 threads. The same bits as two calls of half as many."""
+    M, K = 1 << 24, 257
+    x = _overlapping(M, K, 2)
+    q, s = ttt.ttt_i8_quantize(x)
+    assert bool((s > 0).all())
+    for half in (slice(M // 2), slice(M // 2, M)):
+        q2, s2 = ttt.ttt_i8_quantize(x[half])
+        assert torch.equal(q[half], q2) and torch.equal(s[half], s2)
+
+
+def test_as_many_tokens_as_a_product_of_features_takes():
+    M, K = 1 << 24, 257
+    x = _overlapping(M, K, 3)
+    w, ws = ttt.ttt_i8_quantize(torch.randn(3, K, generator=torch.Generator().manual_seed(4)).cuda())
+    y = ttt.ttt_i8_linear(x, w, ws)
+    assert torch.equal(y[:M // 2], ttt.ttt_i8_linear(x[:M // 2], w, ws))
+    assert torch.equal(y[M // 2:], ttt.ttt_i8_linear(x[M // 2:], w, ws))
