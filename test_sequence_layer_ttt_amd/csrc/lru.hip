@@ -232,10 +232,11 @@ __global__ __launch_bounds__(NT) void lru_scan(LruArgs a, int nch, int ngr) {
     }
 }
 
-// L = 0: the state passes through
+// L = 0: the state passes through. Sequences in a dimension of their own: B D may pass 2^32.
 __global__ __launch_bounds__(NT) void lru_pass(LruArgs a) {
-    const int64_t k = static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x;
-    if (k < static_cast<int64_t>(a.B) * a.D) a.state_out[k] = a.state ? a.state[k] : 0.f;
+    const int c = blockIdx.x * NT + threadIdx.x;
+    const int64_t k = static_cast<int64_t>(blockIdx.y) * a.D + c;
+    if (c < a.D) a.state_out[k] = a.state ? a.state[k] : 0.f;
 }
 
 // A single token: a thread V channels. 64 x 2048 channels: 3.4 us, a launch.
@@ -315,8 +316,7 @@ template <int V> int most_tokens(const LruArgs &a) {
 template <typename T, int V, bool RATE> hipError_t forward(const LruArgs &a, hipStream_t s) {
     const Plan p = plan(a.B, a.L, a.D, most_tokens<V>(a));
     if (!p.tiles) {  // the caller has asked for the state alone
-        const int64_t n = static_cast<int64_t>(a.B) * a.D;
-        hipLaunchKernelGGL(lru_pass, dim3(static_cast<unsigned>((n + NT - 1) / NT)), dim3(NT), 0, s, a);
+        hipLaunchKernelGGL(lru_pass, dim3((a.D + NT - 1) / NT, a.B), dim3(NT), 0, s, a);
         return hipGetLastError();
     }
     constexpr int TG = NT / (CH / V);

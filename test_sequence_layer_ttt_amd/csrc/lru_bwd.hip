@@ -344,10 +344,11 @@ __global__ __launch_bounds__(NT) void lru_bwd_grads(LruBwdArgs g, int nt) {
         grads<T, V, U, RATE, GATED, false>(g, nt, n, sm, smk);
 }
 
-// L = 0: the state's gradient passes through
+// L = 0: the state's gradient passes through. Sequences in a dimension of their own: B D may pass 2^32.
 __global__ __launch_bounds__(NT) void lru_bwd_pass(LruBwdArgs g) {
-    const int64_t k = static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x;
-    if (k < static_cast<int64_t>(g.f.B) * g.f.D) g.dstate[k] = g.dstate_out ? g.dstate_out[k] : 0.f;
+    const int c = blockIdx.x * NT + threadIdx.x;
+    const int64_t k = static_cast<int64_t>(blockIdx.y) * g.f.D + c;
+    if (c < g.f.D) g.dstate[k] = g.dstate_out ? g.dstate_out[k] : 0.f;
 }
 
 bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
@@ -372,9 +373,7 @@ template <typename T, int V, bool RATE> hipError_t backward(const LruBwdArgs &g,
     const int tokens = tile_tokens(a.B, a.L, a.D), nt = (a.L + tokens - 1) / tokens;
     const int64_t rows = static_cast<int64_t>(a.B) * nt;
     if (!nt) {
-        const int64_t n = static_cast<int64_t>(a.B) * a.D;
-        if (g.dstate && n)
-            hipLaunchKernelGGL(lru_bwd_pass, dim3(static_cast<unsigned>((n + NT - 1) / NT)), dim3(NT), 0, s, g);
+        if (g.dstate && a.B) hipLaunchKernelGGL(lru_bwd_pass, dim3((a.D + NT - 1) / NT, a.B), dim3(NT), 0, s, g);
     } else if (a.B) {
         if (tokens == 32)
             gated<T, V, 32 / TG, RATE>(g, nt, s);
