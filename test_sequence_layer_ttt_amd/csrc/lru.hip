@@ -308,13 +308,14 @@ template <typename T, int V, int U, bool RATE> hipError_t gated(const LruArgs &a
 // for (32768 of 2048 118, 133). Otherwise 64: with input gates, whose tokens are more work (8 x
 // 2048 of 2048 67 -> 64 us, 16 x 4096 223 -> 205), and with fewer channels a thread, whose runs
 // are as many times longer (2 x 8192 of 2048 in fp32 117 -> 101, 32768 of 2047 in bf16 320 -> 210).
-template <int V> int most_tokens(const LruArgs &a) {
-    const int64_t wide = (static_cast<int64_t>(a.D) + CH - 1) / CH * a.B;
-    return V == 8 && !(a.i && wide >= 32) ? 128 : 64;
+int most_tokens(int B, int D, int V, bool gated) {
+    const int64_t wide = (static_cast<int64_t>(D) + CH - 1) / CH * B;
+    return V == 8 && !(gated && wide >= 32) ? 128 : 64;
 }
+Plan plan(int B, int L, int D, int V, bool gated) { return plan(B, L, D, most_tokens(B, D, V, gated)); }
 
 template <typename T, int V, bool RATE> hipError_t forward(const LruArgs &a, hipStream_t s) {
-    const Plan p = plan(a.B, a.L, a.D, most_tokens<V>(a));
+    const Plan p = plan(a.B, a.L, a.D, V, a.i != nullptr);
     if (!p.tiles) {  // the caller has asked for the state alone
         hipLaunchKernelGGL(lru_pass, dim3((a.D + NT - 1) / NT, a.B), dim3(NT), 0, s, a);
         return hipGetLastError();
@@ -348,6 +349,7 @@ template <typename T> hipError_t step_t(const LruArgs &a, hipStream_t s) {
 
 // by the sizes alone: of the tiles that need the most
 int64_t lru_forward_floats(int B, int L, int D) { return floats(plan(B, L, D, 64), B, D); }
+int lru_forward_tokens(int B, int L, int D, int V, bool gated) { return plan(B, L, D, V, gated).tokens; }
 hipError_t launch_lru_forward(const LruArgs &a, hipStream_t s) {
     return a.io ? forward_t<bf16_t>(a, s) : forward_t<float>(a, s);
 }

@@ -1,10 +1,12 @@
 """Workspace queries of the 8-bit products in Python: they answer for the rows
-that the calls take, whatever dimensions these come in."""
+that the calls take, whatever dimensions these come in. And the tiles that the
+recurrence takes by size, by which its tests choose theirs."""
 import ctypes
 
 import pytest
 import torch
 
+from tests import lru_tiles as T
 from test_sequence_layer_ttt_amd import _lib, ttt
 
 I8 = torch.int8
@@ -48,3 +50,22 @@ def test_one_row_has_no_stride():
     row = _buffer(3, 1001)[1:2, :992]
     for x in (row, row[0], row[None]):
         assert ttt.ttt_i8_project_workspace(100, x, _buffer(32, 992)) == _project(100, 992, 32, x, 992, _buffer(32, 992), 992)
+
+
+@pytest.mark.parametrize("case", T.LONG, ids=str)
+def test_sizes_of_the_longest_tiles(case):
+    B, L, D, dt, _, gate, _ = case
+    assert T.forward_tokens(B, L, D, dt, gate) == 128
+
+
+# B, L, D, type, gate: the tile's tokens by the width of a thread's loads, input gates and columns
+TOKENS = [((32, 2040, 136, torch.bfloat16, False), 128), ((32, 2040, 136, torch.bfloat16, True), 64),
+          ((15, 4400, 136, torch.bfloat16, True), 128), ((15, 4400, 137, torch.bfloat16, True), 64),
+          ((32, 1930, 136, torch.float32, False), 64), ((32, 2040, 137, torch.float32, False), 64),
+          ((32, 1900, 136, torch.bfloat16, False), 64), ((32, 900, 136, torch.bfloat16, True), 32),
+          ((1, 300, 136, torch.float32, True), 32)]
+
+
+@pytest.mark.parametrize("sizes,tokens", TOKENS, ids=str)
+def test_tiles_by_size(sizes, tokens):
+    assert T.forward_tokens(*sizes) == tokens
