@@ -6,10 +6,6 @@ namespace {
 
 using namespace lru;
 
-__device__ __forceinline__ int live_tokens(const int *lens, int b, int L) {
-    return lens ? max(0, min(lens[b], L)) : L;
-}
-
 // a and u of one token for V channels
 template <int V, bool RATE>
 __device__ __forceinline__ void token(const float (&x)[V], const float (&r)[V], const float (&i)[V], bool gated,
@@ -89,9 +85,8 @@ __global__ __launch_bounds__(NT) void lru_clear(uint4 *p, int64_t n) {
 }
 
 // A run's own scan from a zero state: (A, H) behind each token, all loads asked for at
-// once. FULL: a tile with all of its tokens and channels, as nearly all are, asks for
-// nothing's place; the branches cost copies of what is held across them (8k prompt of
-// 2 x 2048 channels 71 -> 66 us, 32k 91 -> 83). Otherwise rows past the sequence's end are read from its last.
+// once. FULL: a whole tile (8k prompt of 2 x 2048 channels 71 -> 66 us, 32k 91 -> 83).
+// Otherwise rows past the sequence's end are read from its last.
 template <typename T, int V, int U, bool RATE, bool GATED, bool FULL>
 __device__ __forceinline__ void own_scan(const LruArgs &a, int b, int c, int t0, int n, bool some, const float (&rate)[V],
                                          float (&A)[V], float (&H)[V], float (&At)[U][V], float (&Ht)[U][V]) {
@@ -154,7 +149,7 @@ __global__ __launch_bounds__(NT) void lru_scan(LruArgs a, int nch, int ngr) {
     if constexpr (MANY) __syncthreads();
     const int k = MANY ? static_cast<int>(min(place, static_cast<uint32_t>(nch - 1))) : 0, t0 = (k * TG + run) * U;
     const bool some = in && t0 < n;
-    if ((k + 1) * (TG * U) <= n && c0 + CH <= a.D)
+    if (whole(k, TG * U, n, c0, a.D))
         own_scan<T, V, U, RATE, GATED, true>(a, b, c, t0, n, some, rate, A, H, At, Ht);
     else
         own_scan<T, V, U, RATE, GATED, false>(a, b, c, t0, n, some, rate, A, H, At, Ht);
@@ -260,8 +255,6 @@ __global__ __launch_bounds__(NT) void lru_step(LruArgs a) {
     VecIO<float, V>::store(a.state_out + b * a.D + c, h);
     IO::store(static_cast<T *>(a.y) + b * a.yb + c, h);
 }
-
-bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 template <typename T> bool vectors(const LruArgs &a) {
     constexpr int V = 16 / sizeof(T);

@@ -52,6 +52,17 @@ constexpr int CH = 128;     // channels of its tile
 
 constexpr float LOG2E = 1.44269504f;
 
+__device__ __forceinline__ int live_tokens(const int *lens, int b, int L) {
+    return lens ? max(0, min(lens[b], L)) : L;
+}
+// A tile with all of its tokens (of a sequence of n) and channels, as nearly all are: its loops
+// ask for no token's or channel's place, whose branches cost copies of what is held across them.
+__device__ __forceinline__ bool whole(int tile, int tokens, int n, int c0, int D) {
+    return (tile + 1) * tokens <= n && c0 + CH <= D;
+}
+
+inline bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * LOG2E); }
 __device__ __forceinline__ float sigmoid(float v) { return __builtin_amdgcn_rcpf(1.0f + fast_exp(-v)); }
 // sigma(v) and 1 - sigma(v) = e^-v sigma(v), which is 1 where e^-v is out of the reciprocal's range

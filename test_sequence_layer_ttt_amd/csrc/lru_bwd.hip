@@ -33,16 +33,6 @@ int tile_tokens(int B, int L, int D) {
     return t;
 }
 
-__device__ __forceinline__ int live_tokens(const int *lens, int b, int L) {
-    return lens ? max(0, min(lens[b], L)) : L;
-}
-
-// A tile with all of its tokens and channels, as nearly all are: its loops ask for no
-// token's or channel's place, whose branches cost copies of what is held across them.
-template <int TOKENS> __device__ __forceinline__ bool whole(const LruArgs &a, int n) {
-    return (blockIdx.x + 1) * TOKENS <= static_cast<unsigned>(n) && (blockIdx.y + 1) * CH <= static_cast<unsigned>(a.D);
-}
-
 // U tokens of V channels as stored, all asked for at once; rows past the
 // sequence's end are read from its last.
 template <typename T, int V, int U, bool GATED, bool FULL> struct Tokens {
@@ -125,7 +115,7 @@ __global__ __launch_bounds__(NT) void lru_bwd_shares(LruBwdArgs g, int nt) {
     __shared__ float2 sm[TG][CH];
     __shared__ float smk[TG][CH];
     const int n = live_tokens(g.f.lens, blockIdx.z, g.f.L);
-    if (whole<TG * U>(g.f, n))
+    if (whole(blockIdx.x, TG * U, n, blockIdx.y * CH, g.f.D))
         shares<T, V, U, RATE, GATED, true>(g, nt, n, sm, smk);
     else
         shares<T, V, U, RATE, GATED, false>(g, nt, n, sm, smk);
@@ -338,7 +328,7 @@ __global__ __launch_bounds__(NT) void lru_bwd_grads(LruBwdArgs g, int nt) {
     __shared__ float2 sm[TG][CH];
     __shared__ float smk[TG][CH];
     const int n = live_tokens(g.f.lens, blockIdx.z, g.f.L);
-    if (whole<TG * U>(g.f, n))
+    if (whole(blockIdx.x, TG * U, n, blockIdx.y * CH, g.f.D))
         grads<T, V, U, RATE, GATED, true>(g, nt, n, sm, smk);
     else
         grads<T, V, U, RATE, GATED, false>(g, nt, n, sm, smk);
@@ -350,8 +340,6 @@ __global__ __launch_bounds__(NT) void lru_bwd_pass(LruBwdArgs g) {
     const int64_t k = static_cast<int64_t>(blockIdx.y) * g.f.D + c;
     if (c < g.f.D) g.dstate[k] = g.dstate_out ? g.dstate_out[k] : 0.f;
 }
-
-bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 template <typename T, int V, int U, bool RATE, bool GATED> void tiled(const LruBwdArgs &g, int nt, hipStream_t s) {
     const LruArgs &a = g.f;
