@@ -8,6 +8,10 @@ namespace {
 
 constexpr int NT = 256;
 
+// A grid's threads are counted in 32 bits along each of its dimensions: 2^24 rows of a
+// workgroup each would be 2^32, so the workgroups go on in the second dimension after MOST.
+constexpr int MOST = 1 << 22;
+
 // One row to W threads, V values of 16 bytes (or one) at a time. R: the row is
 // held in R of them a thread and read once; R = 0: of any length, read twice (the
 // second time from the chip's caches).
@@ -16,7 +20,7 @@ __global__ __launch_bounds__(NT) void quantize(I8QuantArgs a) {
     typedef VecIO<T, V> IO;
     __shared__ uint32_t red[NT / 64];
     const int lane = threadIdx.x % W;
-    const int64_t m = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * (NT / W) + threadIdx.x / W;
+    const int64_t m = (static_cast<int64_t>(blockIdx.y) * MOST + blockIdx.x) * (NT / W) + threadIdx.x / W;
     if (m >= a.M) return;  // whole waves, and with W > 64 whole workgroups
     const T *x = static_cast<const T *>(a.x) + m * a.xr;
     int8_t *q = a.q + m * a.qr;
@@ -65,12 +69,9 @@ __global__ __launch_bounds__(NT) void quantize(I8QuantArgs a) {
     }
 }
 
-// A grid's threads are counted in 32 bits along each of its dimensions: 2^24 rows of a
-// workgroup each would be 2^32, so more than 2^22 workgroups go on in the second.
 template <typename T, int V, int W, int R> hipError_t go(const I8QuantArgs &a, hipStream_t s) {
-    constexpr int64_t per = NT / W, most = 1 << 22;
-    const int64_t n = (a.M + per - 1) / per;
-    const dim3 grid(static_cast<unsigned>(n < most ? n : most), static_cast<unsigned>((n + most - 1) / most));
+    const int64_t per = NT / W, n = (a.M + per - 1) / per;
+    const dim3 grid(static_cast<unsigned>(n < MOST ? n : MOST), static_cast<unsigned>((n + MOST - 1) / MOST));
     hipLaunchKernelGGL((quantize<T, V, W, R>), grid, dim3(NT), 0, s, a);
     return hipGetLastError();
 }
