@@ -227,11 +227,10 @@ __global__ __launch_bounds__(NT) void lru_scan(LruArgs a, int nch, int ngr) {
     }
 }
 
-// L = 0: the state passes through. Sequences in a dimension of their own: B D may pass 2^32.
+// L = 0: the state passes through
 __global__ __launch_bounds__(NT) void lru_pass(LruArgs a) {
-    const int c = blockIdx.x * NT + threadIdx.x;
-    const int64_t k = static_cast<int64_t>(blockIdx.y) * a.D + c;
-    if (c < a.D) a.state_out[k] = a.state ? a.state[k] : 0.f;
+    const int64_t k = value_at();
+    if (k < static_cast<int64_t>(a.B) * a.D) a.state_out[k] = a.state ? a.state[k] : 0.f;
 }
 
 // A single token: a thread V channels. 64 x 2048 channels: 3.4 us, a launch.
@@ -310,7 +309,7 @@ Plan plan(int B, int L, int D, int V, bool gated) { return plan(B, L, D, most_to
 template <typename T, int V, bool RATE> hipError_t forward(const LruArgs &a, hipStream_t s) {
     const Plan p = plan(a.B, a.L, a.D, V, a.i != nullptr);
     if (!p.tiles) {  // the caller has asked for the state alone
-        hipLaunchKernelGGL(lru_pass, dim3((a.D + NT - 1) / NT, a.B), dim3(NT), 0, s, a);
+        hipLaunchKernelGGL(lru_pass, values_grid(static_cast<int64_t>(a.B) * a.D), dim3(NT), 0, s, a);
         return hipGetLastError();
     }
     constexpr int TG = NT / (CH / V);

@@ -61,6 +61,17 @@ __device__ __forceinline__ bool whole(int tile, int tokens, int n, int c0, int D
     return (tile + 1) * tokens <= n && c0 + CH <= D;
 }
 
+// A value to a thread, for any number of them: a grid's threads are counted in 32 bits along each
+// of its dimensions, so the workgroups go on in the second after MOST.
+constexpr int MOST = 1 << 22;
+inline dim3 values_grid(int64_t n) {
+    const int64_t g = (n + NT - 1) / NT;
+    return dim3(static_cast<unsigned>(g < MOST ? g : MOST), static_cast<unsigned>((g + MOST - 1) / MOST));
+}
+__device__ __forceinline__ int64_t value_at() {
+    return (static_cast<int64_t>(blockIdx.y) * MOST + blockIdx.x) * NT + threadIdx.x;
+}
+
 inline bool aligned(const void *p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * LOG2E); }

@@ -334,11 +334,10 @@ __global__ __launch_bounds__(NT) void lru_bwd_grads(LruBwdArgs g, int nt) {
         grads<T, V, U, RATE, GATED, false>(g, nt, n, sm, smk);
 }
 
-// L = 0: the state's gradient passes through. Sequences in a dimension of their own: B D may pass 2^32.
+// L = 0: the state's gradient passes through
 __global__ __launch_bounds__(NT) void lru_bwd_pass(LruBwdArgs g) {
-    const int c = blockIdx.x * NT + threadIdx.x;
-    const int64_t k = static_cast<int64_t>(blockIdx.y) * g.f.D + c;
-    if (c < g.f.D) g.dstate[k] = g.dstate_out ? g.dstate_out[k] : 0.f;
+    const int64_t k = value_at();
+    if (k < static_cast<int64_t>(g.f.B) * g.f.D) g.dstate[k] = g.dstate_out ? g.dstate_out[k] : 0.f;
 }
 
 template <typename T, int V, int U, bool RATE, bool GATED> void tiled(const LruBwdArgs &g, int nt, hipStream_t s) {
@@ -361,7 +360,8 @@ template <typename T, int V, bool RATE> hipError_t backward(const LruBwdArgs &g,
     const int tokens = tile_tokens(a.B, a.L, a.D), nt = (a.L + tokens - 1) / tokens;
     const int64_t rows = static_cast<int64_t>(a.B) * nt;
     if (!nt) {
-        if (g.dstate && a.B) hipLaunchKernelGGL(lru_bwd_pass, dim3((a.D + NT - 1) / NT, a.B), dim3(NT), 0, s, g);
+        if (g.dstate && a.B)
+            hipLaunchKernelGGL(lru_bwd_pass, values_grid(static_cast<int64_t>(a.B) * a.D), dim3(NT), 0, s, g);
     } else if (a.B) {
         if (tokens == 32)
             gated<T, V, 32 / TG, RATE>(g, nt, s);
