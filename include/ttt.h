@@ -674,10 +674,16 @@ int ttt_block_norm_backward_workspace(int B, int L, int D, int gate_shape, size_
  *                may be exactly `state`.
  * The workspace holds ttt_lru_forward_workspace's bytes (decays and states at
  * the borders of the tiles that run side by side; none for a prompt of one
- * tile), 16-byte aligned; calls that share one must not overlap.
+ * tile), 16-byte aligned; calls that share one must not overlap. A tile waits
+ * for the tiles before it through these words, for a second or two at most: of
+ * a workspace that something else writes during the call, NaNs may come out,
+ * from that tile's tokens on and in the state, but no call waits for ever.
  * Numerics: gates, decays and the state in fp32; 1 - a keeps its relative
- * accuracy where a is near 1. A value that is not finite reaches the outputs of
- * its channel from its token on, as itself or as NaN, and the state.
+ * accuracy where a is near 1. Infinite gates take their limits, finite ones for
+ * finite features and states: with a rate r = -infinity is a = 1, s = 0 and
+ * r = infinity a = e^-rate, without one they are a = 0, s = 1 and a = 1, s = 0;
+ * sigma(i) is 0 or 1. An infinite feature or state, or a NaN, reaches the
+ * outputs of its channel from its token on, as itself or as NaN, and the state.
  */
 #define TTT_LRU_MAX_D (1 << 20)
 #define TTT_LRU_MAX_TILES ((1 << 22) - 1)

@@ -48,7 +48,9 @@ __device__ __forceinline__ void token(const float (&x)[V], const float (&r)[V], 
 constexpr int GROUP = 8;
 constexpr uint32_t WAIT32 = 0xffffffffu;
 constexpr uint64_t WAIT64 = 0xffffffffffffffffull;
-constexpr int POLLS = 1 << 20;  // about a second: a word that never comes is a NaN then
+// About a second. What a tile waits for comes from tiles that are on the chip, microseconds later;
+// a word that never comes (a workspace that something else writes) is a NaN then, to the column's end.
+constexpr int POLLS = 1 << 20;
 
 struct Plan {
     int tokens;  // of a tile

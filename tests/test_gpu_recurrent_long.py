@@ -113,3 +113,22 @@ def test_values_carried_without_a_rounding(B, L, D, dt, gate, lens):
     assert torch.equal(got["dx"].cpu(), dx.float().to(dt)) and torch.equal(got["dstate"].cpu(), G.float())
     for k in ("dr", "di"):
         assert k not in got or not bool(got[k].any())
+
+
+@pytest.mark.parametrize("rate", [True, False], ids=["rate", "sigma"])
+@pytest.mark.parametrize("what", ["x", "state", "r", "i"])
+def test_what_is_not_finite_reaches_its_channel_from_its_token_on(what, rate):
+    """Infinite features and states and NaN gates: no earlier token, no other channel."""
+    B, L, D, t = 2, 700, 16, 333
+    d = _inputs(B, L, D, F32, rate, True, False, 11)
+    call = lambda: ttt.ttt_lru_forward(d["x"], d["r"], d["rate"], d["i"], d["state"])
+    y, so = call()
+    if what == "state":
+        d["state"][1, 3], t = float("inf"), 0
+    else:
+        d[what][1, t, 3] = float("inf") if what == "x" else float("nan")
+    gy, gs = call()
+    bad = ~torch.isfinite(gy)
+    assert bool(bad[1, t:, 3].all()) and int(bad.sum()) == L - t
+    assert not bool(torch.isfinite(gs[1, 3])) and int((~torch.isfinite(gs)).sum()) == 1
+    assert torch.equal(torch.where(bad, y, gy), y)
