@@ -1,8 +1,10 @@
 // Sums over the rows of a matrix of partial results, in a fixed order (the
 // same bits on every run). A workgroup takes 64 columns of one range and
 // splits the rows over 16 lanes' worth of threads that meet in LDS. The callers
-// keep the partials to a few percent of their own bytes, so a call is bound by
-// its launch: 4.1 us for 64 rows of 4480, 4.7 us for 512 rows of 2304.
+// keep the partials to a few percent of their own bytes, so a call of a few hundred
+// rows is bound by its launch: 4.1 us for 64 rows of 4480, 4.7 us for 512 rows of 2304.
+// Many rows of few columns are one workgroup's, 64 of them at a time, and latency adds
+// up: 87 us for 16384 rows of 16 (the recurrence's drate over 16 x 32768 tokens).
 #include "block.hpp"
 
 namespace ttt {

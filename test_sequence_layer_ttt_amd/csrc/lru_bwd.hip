@@ -9,12 +9,16 @@
 //
 // Two passes over the inputs: lru_bwd_shares gives what each tile does to the state and
 // to K, lru_bwd_carry the values at the tiles' borders from those (both directions at
-// once), lru_bwd_grads walks again with them. A tile waits for both directions, so
-// that one pass would need all tiles of a column on the chip at once. Eleven rows are moved
+// once), lru_bwd_grads walks again with them. A tile needs both directions, and one pass that
+// got both from its neighbours would need all tiles of a column on the chip at once; a
+// pass from the last token on could take the states before its tiles from a first one over
+// x, r and i alone. Eleven rows are moved
 // instead of seven: for 2 x 8192 tokens of 2048 bf16 channels 45 + 8 + 102 us, and 6 for
-// drate's sums; both passes run at a large copy's rate (5.9 and 4.7 TB/s). A gate is
+// drate's sums; the passes run at 5.9 and 4.6 TB/s (a large copy: 5.0). A gate is
 // formed again on the way back rather than held: held, a thread takes 182 registers
-// instead of 158, and 187 us instead of 178.
+// instead of 158, and 187 us instead of 178. In fp32 107 + 8 + 189 + 6 us; rows of 2047
+// bf16 channels, value by value, 79 + 12 + 181 + 7. 16 x 32768 tokens of 16 channels, where
+// drate's 16384 partial rows are one workgroup's, 72 + 13 + 161 + 87.
 #include "block.hpp"
 #include "lru.hpp"
 
