@@ -245,10 +245,19 @@ def _rows(t) -> tuple:
     return t.data_ptr() or None, ctypes.byref(ctypes.c_int64(stride))
 
 
+def _weight(w) -> tuple:
+    """Sizes K, N and rows of a weight [N,K]."""
+    rows = _rows(w)
+    if w.dim() != 2:
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected 2 dimensions")
+    return w.size(1), w.size(0), rows
+
+
 def ttt_i8_project_workspace(M: int, x, w) -> int:
     """Bytes of device workspace ttt_i8_project needs for M rows of x and the
     weight w [N,K]: 0 unless M > 64 and rows are not whole 16-byte chunks."""
-    return _need("ttt_i8_project_workspace", M, w.shape[-1], w.shape[0], pointers=(*_rows(x), *_rows(w)))
+    K, N, rows = _weight(w)
+    return _need("ttt_i8_project_workspace", M, K, N, pointers=(*_rows(x), *rows))
 
 
 def ttt_i8_project(x, x_scale, w, w_scale, bias=None, dtype=torch.bfloat16, y=None, workspace=None, stream=None):
@@ -268,7 +277,8 @@ def ttt_i8_project(x, x_scale, w, w_scale, bias=None, dtype=torch.bfloat16, y=No
 def ttt_i8_linear_workspace(M: int, w) -> int:
     """Bytes of device workspace ttt_i8_linear needs for M rows and the weight w
     [N,K] (ttt_qkv_project_i8 for B L rows and theta as [3 H 64, d_model])."""
-    return _need("ttt_i8_linear_workspace", M, w.shape[-1], w.shape[0], pointers=_rows(w))
+    K, N, rows = _weight(w)
+    return _need("ttt_i8_linear_workspace", M, K, N, pointers=rows)
 
 
 def ttt_i8_linear(x, w, w_scale, bias=None, y=None, workspace=None, stream=None):

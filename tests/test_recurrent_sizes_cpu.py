@@ -69,3 +69,14 @@ TOKENS = [((32, 2040, 136, torch.bfloat16, False), 128), ((32, 2040, 136, torch.
 @pytest.mark.parametrize("sizes,tokens", TOKENS, ids=str)
 def test_tiles_by_size(sizes, tokens):
     assert T.forward_tokens(*sizes) == tokens
+
+
+def test_queries_refuse_a_weight_that_the_calls_refuse():
+    """Three projections' weight counts 3 rows by its first dimension."""
+    w = torch.zeros(3, 128, 64, dtype=I8)
+    for bad in (w, w[0, 0]):
+        with pytest.raises(ValueError, match="2 dimensions"):
+            ttt.ttt_i8_linear_workspace(100, bad)
+        with pytest.raises(ValueError, match="2 dimensions"):
+            ttt.ttt_i8_project_workspace(100, w[0], bad)
+    assert ttt.ttt_i8_linear_workspace(100, w.flatten(0, 1)) == 100 * 128 + 400
