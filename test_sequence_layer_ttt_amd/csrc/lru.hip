@@ -265,10 +265,13 @@ template <typename T> bool vectors(const LruArgs &a) {
 
 // Tiles of `most` tokens, shorter ones where that would leave fewer than four for each
 // compute unit.
-Plan plan(int B, int L, int D, int most) {
+int tile_tokens(int B, int L, int D, int most) {
     const int64_t wide = (static_cast<int64_t>(D) + CH - 1) / CH * B;
     int tokens = most;
     while (tokens > 32 && wide * ((L + tokens - 1) / tokens) < 1024) tokens /= 2;
+    return tokens;
+}
+Plan plan(int L, int tokens) {
     Plan p{tokens, (static_cast<int64_t>(L) + tokens - 1) / tokens, 0};
     p.groups = p.tiles / GROUP;
     return p;
@@ -306,10 +309,9 @@ int most_tokens(int B, int D, int V, bool gated) {
     const int64_t wide = (static_cast<int64_t>(D) + CH - 1) / CH * B;
     return V == 8 && !(gated && wide >= 32) ? 128 : 64;
 }
-Plan plan(int B, int L, int D, int V, bool gated) { return plan(B, L, D, most_tokens(B, D, V, gated)); }
 
 template <typename T, int V, bool RATE> hipError_t forward(const LruArgs &a, hipStream_t s) {
-    const Plan p = plan(a.B, a.L, a.D, V, a.i != nullptr);
+    const Plan p = plan(a.L, lru_forward_tokens(a.B, a.L, a.D, V, a.i != nullptr));
     if (!p.tiles) {  // the caller has asked for the state alone
         hipLaunchKernelGGL(lru_pass, values_grid(static_cast<int64_t>(a.B) * a.D), dim3(NT), 0, s, a);
         return hipGetLastError();
@@ -342,8 +344,10 @@ template <typename T> hipError_t step_t(const LruArgs &a, hipStream_t s) {
 }  // namespace
 
 // by the sizes alone: of the tiles that need the most
-int64_t lru_forward_floats(int B, int L, int D) { return floats(plan(B, L, D, 64), B, D); }
-int lru_forward_tokens(int B, int L, int D, int V, bool gated) { return plan(B, L, D, V, gated).tokens; }
+int64_t lru_forward_floats(int B, int L, int D) { return floats(plan(L, tile_tokens(B, L, D, 64)), B, D); }
+int lru_forward_tokens(int B, int L, int D, int V, bool gated) {
+    return tile_tokens(B, L, D, most_tokens(B, D, V, gated));
+}
 hipError_t launch_lru_forward(const LruArgs &a, hipStream_t s) {
     return a.io ? forward_t<bf16_t>(a, s) : forward_t<float>(a, s);
 }

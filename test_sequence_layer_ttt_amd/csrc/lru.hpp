@@ -42,7 +42,7 @@ hipError_t launch_lru_step(const LruArgs &a, hipStream_t stream);  // state_out 
 hipError_t launch_lru_backward(const LruBwdArgs &a, hipStream_t stream);
 int64_t lru_forward_floats(int B, int L, int D);   // workspace
 int64_t lru_backward_floats(int B, int L, int D);
-// tokens of a prompt's tile where a thread takes V channels; the tests choose their sizes by it
+// tokens of a prompt's tile where a thread takes V channels
 int lru_forward_tokens(int B, int L, int D, int V, bool gated);
 
 namespace lru {
